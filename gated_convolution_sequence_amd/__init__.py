@@ -432,3 +432,9 @@ class HyenaConvLong(torch.autograd.Function):
         ctx.workspace = None
         return (dq, dk if need[1] else None, dv if need[2] else None,
                 dh.to(h.dtype) if dh is not None else None, None)
+
+
+from .layer import (  # noqa: E402,F401  (the operators around the convolution)
+    ACTS, GATES, LAYER_EXPORTS, LAYER_LIB_PATH, STATE_ROWS, GatedScan, LayerError, LinearAct, conv_cache_fill,
+    conv_step, layer_lib, layer_strerror, linear_bwd, linear_fwd, linear_workspace_bytes, scan_bwd, scan_fwd,
+    scan_step, scan_workspace_bytes)

@@ -9,6 +9,9 @@ ROOT = os.path.dirname(PKG)
 SOURCES = [os.path.join(PKG, "csrc", name) for name in ("hyena_conv.hip", "hyena_fft.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libhyena_conv.so")
+# the sequence-layer operators (include/hyena_layer.h)
+LAYER_SOURCES = [os.path.join(PKG, "csrc", name) for name in ("hyena_scan.hip", "hyena_step.hip", "hyena_linear.hip")]
+LAYER_LIB = os.path.join(PKG, "libhyena_layer.so")
 # the benchmark's streaming reference kernel (not part of the operator's ABI)
 STREAM_REF_SOURCE = os.path.join(PKG, "csrc", "stream_ref.hip")
 STREAM_REF_LIB = os.path.join(PKG, "libhyena_stream_ref.so")
@@ -41,6 +44,11 @@ def _compile(sources, lib, verbose):
 def build_library(verbose: bool = False) -> str:
     """Compile the operator's csrc/*.hip sources into libhyena_conv.so next to this file."""
     return _compile(SOURCES, LIB, verbose)
+
+
+def build_layer_library(verbose: bool = False) -> str:
+    """Compile the sequence-layer operators' csrc/*.hip sources into libhyena_layer.so next to this file."""
+    return _compile(LAYER_SOURCES, LAYER_LIB, verbose)
 
 
 def build_stream_ref(verbose: bool = False) -> str:

@@ -1,0 +1,110 @@
+// What the sequence-layer kernels (hyena_scan.hip, hyena_step.hip,
+// hyena_linear.hip) share: element access, gates, buffer descriptors and the
+// host's argument checks.
+#ifndef HYENA_LAYER_COMMON_H
+#define HYENA_LAYER_COMMON_H
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "hyena_layer.h"
+
+namespace layer {
+
+typedef __bf16 bf16_t;
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+
+constexpr int kStateRows = 64;  // rows between saved states (hyena_layer.h)
+
+// ---- device -----------------------------------------------------------------
+
+__device__ inline float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ inline float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+__device__ inline uint32_t pack_bf16(float a, float b) {
+    bf16x2_t r = {(__bf16)a, (__bf16)b};  // round to nearest even
+    return __builtin_bit_cast(uint32_t, r);
+}
+
+// One element of a bf16 or fp32 array.
+template <bool F32> __device__ inline float load1(const void *p, size_t i) {
+    if constexpr (F32) return ((const float *)p)[i];
+    else return (float)((const bf16_t *)p)[i];
+}
+template <bool F32> __device__ inline void store1(void *p, size_t i, float x) {
+    if constexpr (F32) ((float *)p)[i] = x;
+    else ((bf16_t *)p)[i] = (bf16_t)x;
+}
+
+// The decay a of a gate and, where wanted, da/dg.  With e = exp(-|g|) and
+// r = 1 / (1 + e): sigmoid(g) is r or e r and its slope e r^2 for either sign,
+// which keeps 1 - a exact to rounding where a is near 1.  g = -inf gives
+// a = 0, g = +inf a = 1, both with slope 0.
+template <bool LOG> __device__ inline float decay(float g) {
+    if constexpr (LOG) {
+        return __expf(g);
+    } else {
+        const float e = __expf(-fabsf(g));
+        const float r = __builtin_amdgcn_rcpf(1.0f + e);
+        return g < 0.0f ? e * r : r;
+    }
+}
+template <bool LOG> __device__ inline float decay(float g, float &slope) {
+    if constexpr (LOG) {
+        return slope = __expf(g);
+    } else {
+        const float e = __expf(-fabsf(g));
+        const float r = __builtin_amdgcn_rcpf(1.0f + e);
+        slope = e * r * r;
+        return g < 0.0f ? e * r : r;
+    }
+}
+
+// ---- host -------------------------------------------------------------------
+
+// Rows of `width` bytes, `pitch` bytes apart.
+struct Rows {
+    const void *p;
+    int64_t rows, width, pitch;
+};
+
+inline bool same_range(const Rows &a, const Rows &b) {
+    return a.p == b.p && a.rows == b.rows && a.width == b.width && a.pitch == b.pitch;
+}
+
+// Whether two strided arrays share a byte.  Column slices of one buffer have
+// the same pitch and interleave without sharing any; arrays of different
+// pitch count as overlapping where their address ranges meet.
+inline bool overlap(const Rows &a, const Rows &b) {
+    if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0 || a.width <= 0 || b.width <= 0) return false;
+    const uint64_t a0 = (uint64_t)(uintptr_t)a.p, b0 = (uint64_t)(uintptr_t)b.p;
+    const uint64_t an = (uint64_t)(a.rows - 1) * (uint64_t)a.pitch + (uint64_t)a.width;
+    const uint64_t bn = (uint64_t)(b.rows - 1) * (uint64_t)b.pitch + (uint64_t)b.width;
+    if (a0 < b0 ? b0 - a0 >= an : a0 - b0 >= bn) return false;
+    if (a.pitch != b.pitch || (a.rows == 1 && b.rows == 1)) return true;
+    const uint64_t pitch = (uint64_t)a.pitch;
+    const uint64_t d = a0 <= b0 ? (b0 - a0) % pitch : (pitch - (a0 - b0) % pitch) % pitch;
+    return d < (uint64_t)a.width || d + (uint64_t)b.width > pitch;
+}
+
+// bytes = a b c, false where that passes 2^62 or a factor is negative.
+inline bool mul_fits(int64_t a, int64_t b, int64_t c, int64_t *out) {
+    if (a < 0 || b < 0 || c < 0) return false;
+    int64_t r;
+    if (__builtin_mul_overflow(a, b, &r) || __builtin_mul_overflow(r, c, &r)) return false;
+    if (r >= (int64_t)1 << 62) return false;
+    *out = r;
+    return true;
+}
+
+inline bool aligned(const void *p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+__host__ __device__ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline int launch_status() { return hipGetLastError() == hipSuccess ? HYENA_OK : HYENA_ERR_LAUNCH; }
+
+}  // namespace layer
+
+#endif

@@ -1,0 +1,347 @@
+"""The gated recurrence on the GPU (scan_fwd, scan_bwd) against the 64-bit walk of layer_ref."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import gated_convolution_sequence_amd as hc
+import layer_ref as ref
+from gpu_util import DEV, log
+from layer_ref import check, to_np
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    assert torch.cuda.is_available(), "GPU tests need a visible GPU"
+    hc.layer_lib()
+    yield
+    torch.cuda.synchronize()
+
+
+def inputs(B, L, D, dtype, gate, seed, resets=0.0, fused=False, n=5):
+    """q, k, v, g, dy on the GPU: N(0,1), gates of memories from a row to some hundreds; a share of resets."""
+    gen = torch.Generator().manual_seed(seed)
+    ts = [torch.randn(B, L, D, generator=gen) for _ in range(n)]
+    ts[3] = 1.5 * ts[3] + 3.0 if gate == "sigmoid" else -torch.exp(1.2 * ts[3] - 2.5)
+    if resets:
+        ts[3][torch.rand(B, L, generator=gen) < resets] = -math.inf
+    ts = [t.to(dtype) for t in ts]
+    if fused:
+        big = torch.cat(ts[:4], dim=2).to(DEV)
+        return [big[:, :, i * D:(i + 1) * D] for i in range(4)] + [t.to(DEV) for t in ts[4:]]
+    return [t.to(DEV) for t in ts]
+
+
+def states_of(B, D, seed):
+    gen = torch.Generator().manual_seed(seed)
+    return (2 * torch.randn(B, D, generator=gen)).to(DEV), torch.randn(B, D, generator=gen).to(DEV)
+
+
+def check_fwd(ts, gate, s0, what):
+    q, k, v, g = ts[:4]
+    y, last, states = hc.scan_fwd(q, k, v, g, gate=gate, s0=s0, save_states=True)
+    f = ref.scan_fwd(*(to_np(t) for t in ts[:4]), gate, None if s0 is None else to_np(s0))
+    check(last, f["last"], f["elast"], F32, what + " s_last")
+    check(states, f["states"], f["estates"], F32, what + " states")
+    check(y, f["y"], f["ey"], q.dtype, what + " y")
+    return y, last, states
+
+
+def check_bwd(ts, gate, s0, ds_last, states, what):
+    got = hc.scan_bwd(*ts[:5], states, gate=gate, ds_last=ds_last)
+    want = ref.scan_bwd(*(to_np(t) for t in ts[:5]), gate, None if s0 is None else to_np(s0),
+                        None if ds_last is None else to_np(ds_last))
+    for name, t in zip(("dq", "dk", "dv", "dg", "ds0"), got):
+        check(t, *want[name], F32 if name == "ds0" else ts[0].dtype, "%s %s" % (what, name))
+    return got
+
+
+SHAPES = [(1, 1, 1), (1, 1, 64), (2, 2, 7), (1, 63, 8), (3, 64, 16), (1, 65, 24), (2, 127, 33), (1, 128, 256),
+          (1, 129, 130), (2, 300, 72), (1, 511, 520), (1, 1000, 66), (5, 7, 1000), (1, 2049, 40), (17, 130, 12)]
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("gate", ["sigmoid", "log"])
+def test_forward_and_backward(shape, dtype, gate):
+    B, L, D = shape
+    seed = L * 1000 + D
+    log("scan %s %s %s" % (shape, dtype, gate))
+    with_state = (L + D) % 2 == 0
+    ts = inputs(B, L, D, dtype, gate, seed, resets=0.01 if L % 3 else 0.0, fused=D % 3 == 0)
+    s0, ds_last = states_of(B, D, seed) if with_state else (None, None)
+    _, _, states = check_fwd(ts, gate, s0, "fwd")
+    check_bwd(ts, gate, s0, ds_last, states, "bwd")
+
+
+@pytest.mark.parametrize("D", [64, 520, 37])
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_long_memory_over_many_tiles(D, dtype):
+    """Gates so near 1 that a state reaches across the whole sequence (many tiles' carries)."""
+    log("scan long memory D=%d %s" % (D, dtype))
+    ts = inputs(2, 3000, D, dtype, "sigmoid", 5, fused=D == 64)
+    ts[3].fill_(9.0)
+    s0, ds_last = states_of(2, D, 6)
+    _, _, states = check_fwd(ts, "sigmoid", s0, "fwd")
+    check_bwd(ts, "sigmoid", s0, ds_last, states, "bwd")
+
+
+def test_closed_gates_are_a_plain_product():
+    """Every gate 0: y = q k v, no gradient reaches the gates or the first state."""
+    ts = inputs(2, 200, 72, F32, "sigmoid", 9)
+    ts[3].fill_(-math.inf)
+    s0, ds_last = states_of(2, 72, 3)
+    y, last, states = hc.scan_fwd(*ts[:4], s0=s0, save_states=True)
+    q, k, v, g, dy = ts
+    assert torch.equal(y, q * (k * v)) and torch.equal(last, (k * v)[:, -1])
+    dq, dk, dv, dg, ds0 = hc.scan_bwd(*ts, states, ds_last=ds_last)
+    ds = q * dy
+    ds[:, -1] += ds_last
+    # q dy + ds_last may be one fused operation
+    check(dk, to_np(ds * v), 4 * ref.U * (to_np((q * dy).abs()) + 4) * to_np(v.abs()), F32, "dk")
+    assert torch.all(dg == 0) and torch.all(ds0 == 0)
+
+
+@pytest.mark.parametrize("bad", [math.inf, math.nan])
+@pytest.mark.parametrize("D", [64, 9])
+def test_a_reset_drops_what_is_not_finite(bad, D):
+    """An infinite or NaN state ends with its document: row 150 starts afresh."""
+    log("scan reset %r D=%d" % (bad, D))
+    ts = inputs(1, 700, D, F32, "sigmoid", 11)
+    ts[1][0, 20, : D // 2] = bad
+    ts[3][0, 150] = -math.inf
+    s0 = states_of(1, D, 4)[0]
+    y, last, states = check_fwd(ts, "sigmoid", s0, "fwd")
+    assert torch.isfinite(y[:, 150:]).all() and not torch.isfinite(y[0, 20:150, 0]).any()
+    clean = hc.scan_fwd(*(t[:, 150:].contiguous() for t in ts[:4]))
+    assert torch.isfinite(clean[0]).all()
+    got = hc.scan_bwd(*ts, states)
+    for t in got[:4]:
+        assert torch.isfinite(t[:, 151:]).all()
+    assert torch.isfinite(got[3][:, 150]).all()
+
+
+def test_an_infinite_state_lives_on_without_a_reset():
+    """Only a gate of exactly 0 drops the state: small gates whose product underflows do not."""
+    ts = inputs(1, 600, 64, F32, "log", 12)
+    ts[3].fill_(-3.0)  # e^-3 a row: the product over a few rows underflows
+    ts[1][0, 5, 3], ts[2][0, 5, 3] = math.inf, 1.0
+    y, last, _ = hc.scan_fwd(*ts[:4], gate="log", save_states=True)
+    assert torch.isinf(last[0, 3]) and torch.isfinite(last[0, :3]).all() and torch.isfinite(last[0, 4:]).all()
+
+
+def test_an_infinite_gradient_does_not_pass_a_reset():
+    ts = inputs(1, 400, 72, F32, "sigmoid", 13)
+    ts[3][0, 200] = -math.inf
+    ts[4][0, 300, 5] = math.inf
+    _, _, states = hc.scan_fwd(*ts[:4], save_states=True)
+    dq, dk, dv, dg, ds0 = hc.scan_bwd(*ts, states)
+    assert torch.isfinite(dk[0, :200]).all() and torch.isfinite(dg[0, :201]).all() and torch.isfinite(ds0).all()
+    assert not torch.isfinite(dk[0, 200:300, 5]).any()
+
+
+@pytest.mark.parametrize("cut", [1, 64, 100, 257])
+def test_shards_chain_through_their_states(cut):
+    """Two shards with the state handed over give the whole sequence, forward and back."""
+    ts = inputs(2, 500, 96, F32, "log", 20)
+    whole = hc.scan_fwd(*ts[:4], gate="log", save_states=True)
+    a, b = [t[:, :cut].contiguous() for t in ts], [t[:, cut:].contiguous() for t in ts]
+    ya, sa, sta = hc.scan_fwd(*a[:4], gate="log", save_states=True)
+    yb, sb, stb = hc.scan_fwd(*b[:4], gate="log", s0=sa, save_states=True)
+    f = ref.scan_fwd(*(to_np(t) for t in ts[:4]), "log")
+    check(torch.cat([ya, yb], 1), f["y"], f["ey"], F32, "y")
+    gb = hc.scan_bwd(*b, stb, gate="log")
+    ga = hc.scan_bwd(*a, sta, gate="log", ds_last=gb[4])
+    want = ref.scan_bwd(*(to_np(t) for t in ts), "log")
+    for i, name in enumerate(("dq", "dk", "dv", "dg")):
+        check(torch.cat([ga[i], gb[i]], 1), *want[name], F32, name)
+    check(ga[4], *want["ds0"], F32, "ds0")
+
+
+@pytest.mark.parametrize("dtype,off,ld", [(BF16, 0, 200), (BF16, 1, 201), (BF16, 8, 264), (F32, 3, 77), (F32, 4, 80)])
+def test_strides_and_offsets_give_the_same(dtype, off, ld):
+    """Any row stride and any element offset: the bits of the contiguous call, and nothing else written."""
+    B, L, D = 2, 333, 72
+    ts = inputs(B, L, D, dtype, "sigmoid", 31, resets=0.01)
+    views = []
+    for t in ts[:4]:
+        big = torch.full((off + B * L * ld,), float("nan"), dtype=dtype, device=DEV)
+        view = big[off:].view(B, L, ld)[:, :, :D]
+        view.copy_(t)
+        views.append(view)
+    f = ref.scan_fwd(*(to_np(t) for t in ts[:4]), "sigmoid")
+    y, last, states = hc.scan_fwd(*views, save_states=True)
+    check(y, f["y"], f["ey"], dtype, "y")
+    check(states, f["states"], f["estates"], F32, "states")
+    bigs = [torch.full((off + B * L * ld,), 7.0, dtype=dtype, device=DEV) for _ in range(4)]
+    outs = [b[off:].view(B, L, ld)[:, :, :D] for b in bigs]
+    got = hc.scan_bwd(*views, ts[4], states, grads=outs)
+    want = ref.scan_bwd(*(to_np(t) for t in ts), "sigmoid")
+    for name, t, b in zip(("dq", "dk", "dv", "dg"), got, bigs):
+        check(t, *want[name], dtype, name)
+        assert torch.all(b[:off] == 7.0) and torch.all(b[off:].view(B, L, ld)[:, :, D:] == 7.0), name
+
+
+def test_gradients_into_slices_of_one_buffer():
+    B, L, D = 2, 190, 64
+    ts = inputs(B, L, D, BF16, "sigmoid", 33, fused=True)
+    _, _, states = hc.scan_fwd(*ts[:4], save_states=True)
+    big = torch.zeros(B, L, 4 * D, dtype=BF16, device=DEV)
+    outs = [big[:, :, i * D:(i + 1) * D] for i in range(4)]
+    hc.scan_bwd(*ts, states, grads=outs)
+    want = hc.scan_bwd(*ts, states)
+    for i in range(4):
+        assert torch.equal(outs[i], want[i])
+
+
+def test_offsets_past_32_bits():
+    """Rows 2^16 elements apart: element offsets pass 2^31, byte offsets 2^32."""
+    L, D, ld = 36000, 72, 1 << 16
+    log("scan past 32 bits")
+    ts = inputs(1, L, D, BF16, "sigmoid", 40, resets=0.001)
+    big = torch.empty(L * ld, dtype=BF16, device=DEV).view(1, L, ld)
+    views = [big[:, :, i * 8192:i * 8192 + D] for i in range(4)]
+    for view, t in zip(views, ts):
+        view.copy_(t)
+    got, want = hc.scan_fwd(*views, save_states=True), hc.scan_fwd(*ts[:4], save_states=True)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    outs = [big[:, :, (4 + i) * 8192:(4 + i) * 8192 + D] for i in range(4)]
+    hc.scan_bwd(*views, ts[4], want[2], grads=outs)
+    for a, b in zip(outs, hc.scan_bwd(*ts, want[2])):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("shape", [(1, 5000, 264), (3, 1500, 1000), (1, 300, 24)], ids=str)
+def test_runs_give_the_same_bits(shape):
+    ts = inputs(*shape, BF16, "sigmoid", 50)
+    first = hc.scan_fwd(*ts[:4], save_states=True)
+    g1 = hc.scan_bwd(*ts, first[2])
+    for _ in range(5):
+        for a, b in zip(hc.scan_fwd(*ts[:4], save_states=True), first):
+            assert torch.equal(a, b)
+        for a, b in zip(hc.scan_bwd(*ts, first[2]), g1):
+            assert torch.equal(a, b)
+
+
+def test_empty_and_partial_calls():
+    q = torch.empty(2, 0, 16, dtype=BF16, device=DEV)
+    s0 = torch.randn(2, 16, device=DEV)
+    y, last, states = hc.scan_fwd(q, q, q, q, s0=s0, save_states=True)
+    assert y.shape == q.shape and torch.equal(last, s0) and states.shape == (2, 0, 16)
+    assert torch.equal(hc.scan_fwd(q, q, q, q)[1], torch.zeros_like(s0))
+    assert torch.equal(hc.scan_bwd(q, q, q, q, q, states, ds_last=s0)[4], s0)
+    e = torch.empty(0, 5, 16, dtype=BF16, device=DEV)
+    assert hc.scan_fwd(e, e, e, e, save_states=True)[2].shape == (0, 1, 16)
+    # states alone, and each gradient alone, through the C ABI
+    B, L, D = 2, 200, 40
+    ts = inputs(B, L, D, BF16, "sigmoid", 60)
+    _, last, states = hc.scan_fwd(*ts[:4], save_states=True)
+    n = hc.scan_workspace_bytes(B, L, D)
+    ws = torch.empty(max(n, 16), dtype=torch.uint8, device=DEV)
+    stream = torch.cuda.current_stream().cuda_stream
+    alone = torch.empty_like(states)
+    assert hc.layer_lib().hyena_scan_fwd(None, ts[1].data_ptr(), ts[2].data_ptr(), ts[3].data_ptr(), B, L, D, D, 0,
+                                         None, None, None, alone.data_ptr(), ws.data_ptr(), n, 0, stream) == 0
+    assert torch.equal(alone, states)
+    want = hc.scan_bwd(*ts, states)
+    for i in range(5):
+        outs = [None] * 5
+        outs[i] = torch.full_like(want[i], float("nan"))
+        ptrs = [None if t is None else t.data_ptr() for t in outs]
+        assert hc.layer_lib().hyena_scan_bwd(*(t.data_ptr() for t in ts), states.data_ptr(), None, B, L, D, D, D, 0,
+                                             *ptrs, ws.data_ptr(), n, 0, stream) == 0
+        assert torch.equal(outs[i], want[i])
+
+
+def test_on_another_stream_and_in_a_graph():
+    B, L, D = 1, 1300, 264
+    side = torch.cuda.Stream()
+    static = inputs(B, L, D, BF16, "sigmoid", 70)
+    ws = [torch.empty(max(16, hc.scan_workspace_bytes(B, L, D)), dtype=torch.uint8, device=DEV) for _ in range(2)]
+
+    def both(ts):
+        y, last, states = hc.scan_fwd(*ts[:4], save_states=True, workspace=ws[0])
+        return (y, last, *hc.scan_bwd(*ts, states, workspace=ws[1]))
+
+    want = both(static)
+    torch.cuda.synchronize()
+    y, last, states = hc.scan_fwd(*static[:4], save_states=True, stream=side)
+    got = hc.scan_bwd(*static, states, stream=side)
+    side.synchronize()
+    for a, b in zip((y, last, *got), want):
+        assert torch.equal(a, b)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = both(static)
+    for r in range(3):
+        for s, t in zip(static, inputs(B, L, D, BF16, "sigmoid", 80 + r)):
+            s.copy_(t)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        kept = [t.clone() for t in outs]
+        for a, b in zip(kept, both(static)):
+            assert torch.equal(a, b), "replay %d" % r
+
+
+def test_autograd_against_differences():
+    """Every gradient against central differences of the forward (fp32; steps of 2^-5 in a loss of order 1).
+
+    The loss is linear in q, k, v and s0: their differences are exact but for rounding (2^-23 of the
+    loss's terms over the step, 2^-18 in all); in g the third derivative adds at most h^2 / 6 of the gate's
+    and its products' slopes (< 2^-10 of the terms).  Bound: 2^-8 of the largest gradient."""
+    B, L, D = 1, 70, 3
+    ts = [t.to(F32).requires_grad_(True) for t in inputs(B, L, D, F32, "sigmoid", 90)[:4]]
+    s0 = states_of(B, D, 1)[0].requires_grad_(True)
+    wy = torch.randn(B, L, D, device=DEV) / L
+    wl = torch.randn(B, D, device=DEV) / L
+
+    def loss(*args):
+        y, last = hc.GatedScan.apply(*args[:4], "sigmoid", args[4])
+        return (y * wy).double().sum() + (last * wl).double().sum()
+
+    args = [*ts, s0]
+    loss(*args).backward()
+    h = 2.0 ** -5
+    for i, t in enumerate(args):
+        num = torch.empty_like(t)
+        flat = t.detach().clone()
+        for j in range(t.numel()):
+            vals = []
+            for sign in (1, -1):
+                moved = flat.clone()
+                moved.view(-1)[j] += sign * h
+                with torch.no_grad():
+                    vals.append(loss(*[moved if m == i else a.detach() for m, a in enumerate(args)]))
+            num.view(-1)[j] = (vals[0] - vals[1]) / (2 * h)
+        scale = t.grad.abs().max()
+        assert (num - t.grad).abs().max() <= 2.0 ** -8 * scale, (i, (num - t.grad).abs().max(), scale)
+
+
+def test_refusals():
+    t = torch.zeros(1, 8, 16, dtype=BF16, device=DEV)
+    with pytest.raises(ValueError):
+        hc.scan_fwd(t, t, t, t, gate="tanh")
+    with pytest.raises(ValueError):
+        hc.scan_fwd(t, t, t, t[:, :4])
+    with pytest.raises(ValueError):
+        hc.scan_fwd(t, t, t, t.float())
+    with pytest.raises(TypeError):
+        hc.scan_fwd(*(t.half() for _ in range(4)))
+    with pytest.raises(ValueError):
+        hc.scan_fwd(t, t, t, t, s0=torch.zeros(1, 16, dtype=BF16, device=DEV))
+    with pytest.raises(ValueError):  # columns apart
+        wide = torch.zeros(1, 8, 32, dtype=BF16, device=DEV)
+        hc.scan_fwd(wide[:, :, ::2], t, t, t)
+    with pytest.raises(ValueError):  # two row strides
+        hc.scan_fwd(torch.zeros(1, 8, 32, dtype=BF16, device=DEV)[:, :, :16], t, t, t)
+    with pytest.raises(hc.LayerError) as e:  # y on top of q
+        hc.scan_fwd(t, t, t, t, out=t)
+    assert e.value.status == -6
+    with pytest.raises(ValueError):
+        hc.scan_bwd(t, t, t, t, t, torch.zeros(1, 2, 16, device=DEV))
