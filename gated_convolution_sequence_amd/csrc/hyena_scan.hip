@@ -2,12 +2,46 @@
 //     s_t = a_t s_{t-1} + k_t v_t,   y_t = q_t s_t,   a = sigmoid(g) or exp(g),
 // and its backward (hyena_layer.h has the formulas and layouts).
 //
-// One lane walks one channel of one batch row through time.
+// Method.  A row maps the state by s -> a s + x, and such maps compose: over
+// any run of rows s -> P s + S with P the product of the decays.  Time is cut
+// into tiles of T rows; a workgroup owns one tile of C channels, keeps it in
+// registers and works in three steps:
+//   1. each lane composes its own R rows of each of its channels,
+//   2. one lane per channel composes the tile's NS slices in LDS, publishes
+//      the tile's (P, S), takes the state that enters the tile from the tiles
+//      before it, and publishes the state that leaves it,
+//   3. each lane walks its rows once more, from the state that enters them,
+//      and writes its outputs.
+// So every input is read once and every output written once (10 B a token and
+// channel forward, 18 B backward in bf16), which is what bounds the kernels;
+// two kernels with the tiles' maps in between would read g, k and v twice.
+//
+// Carries between workgroups (step 2).  Tile m of a chain publishes one 64-bit
+// word per channel: first (P, S), then, once known, the state that leaves it.
+// A tile reads the words of the kWindow tiles before it and walks forward from
+// the nearest one that holds a state.  That state was reached by the same
+// sequence of operations, so the result does not depend on which words were
+// there yet: runs give the same bits.  The words are single relaxed atomics
+// that carry their own readiness, so no fence is wanted.
+// The waiting ends: tiles are handed out by a counter in chain order, so a
+// workgroup only waits for workgroups that have started before it and the
+// first unfinished one waits for none.
+//
+// A gate of exactly 0 drops the state, whatever it holds.  P is therefore kept
+// at 0 exactly where a run holds such a gate, and off 0 (at the least positive
+// fp32) where a product of small gates underflows.
+
+#include <initializer_list>
 
 #include "layer_common.h"
 
 namespace layer {
 namespace {
+
+constexpr int kWindow = 8;
+constexpr int kThreads = 256;
+constexpr uint32_t kEmpty = 0xffffffffu;  // high half of a word not yet written
+constexpr uint32_t kState = 0x80000000u;  // high half of a word that holds a state (a map has P >= 0 there)
 
 struct ScanParams {
     const void *q, *k, *v, *g, *dy;
@@ -15,58 +49,365 @@ struct ScanParams {
     void *y, *dq, *dk, *dv, *dg;
     float *s_last, *states, *ds0;
     int64_t B, L, D, ld, ldd;
+    int64_t n_tiles, c_tiles;  // tiles of a chain, channel tiles of a row
+    uint32_t *counter;         // tiles handed out so far; null: one tile a chain, nothing to carry
+    uint64_t *words;           // [n_tiles][B][c_tiles * C]
 };
 
-template <bool F32, bool LOG>
-__global__ __launch_bounds__(64) void scan_fwd_kernel(ScanParams p) {
-    const int64_t i = (int64_t)blockIdx.x * 64 + threadIdx.x;
-    if (i >= p.B * p.D) return;
-    const int64_t b = i / p.D, d = i % p.D;
-    const int64_t chunks = ceil_div(p.L, kStateRows);
-    float s = p.s0 ? p.s0[i] : 0.0f;
-    for (int64_t t = 0; t < p.L; ++t) {
-        const int64_t e = (b * p.L + t) * p.ld + d;
-        if (p.states && t % kStateRows == 0) p.states[(b * chunks + t / kStateRows) * p.D + d] = s;
-        const float a = decay<LOG>(load1<F32>(p.g, e));
-        s = (a == 0.0f ? 0.0f : a * s) + load1<F32>(p.k, e) * load1<F32>(p.v, e);
-        if (p.y) store1<F32>(p.y, (b * p.L + t) * p.D + d, load1<F32>(p.q, e) * s);
-    }
-    if (p.s_last) p.s_last[i] = s;
+// P of a run that holds no gate of 0 (least = its smallest gate).
+__device__ inline float keep_off_zero(float P, float least) {
+    return least == 0.0f ? 0.0f : fmaxf(P, __uint_as_float(1u));
+}
+__device__ inline float apply(float P, float S, float s) { return P == 0.0f ? S : fmaf(P, s, S); }
+__device__ inline float join(float P1, float P2) {
+    return P1 == 0.0f || P2 == 0.0f ? 0.0f : fmaxf(P1 * P2, __uint_as_float(1u));
 }
 
-template <bool F32, bool LOG>
-__global__ __launch_bounds__(64) void scan_bwd_kernel(ScanParams p) {
-    __shared__ float sm[kStateRows][64];
-    const int64_t i = (int64_t)blockIdx.x * 64 + threadIdx.x;
-    if (i >= p.B * p.D) return;
-    const int64_t b = i / p.D, d = i % p.D;
-    const int64_t chunks = ceil_div(p.L, kStateRows);
-    float c = p.ds_last ? p.ds_last[i] : 0.0f;
-    for (int64_t n = chunks - 1; n >= 0; --n) {
-        float s = p.states_in[(b * chunks + n) * p.D + d];
-        const int rows = (int)min((int64_t)kStateRows, p.L - n * kStateRows);
-        for (int r = 0; r < rows; ++r) {
-            sm[r][threadIdx.x] = s;  // the state before row r
-            const int64_t e = (b * p.L + n * kStateRows + r) * p.ld + d;
-            const float a = decay<LOG>(load1<F32>(p.g, e));
-            s = (a == 0.0f ? 0.0f : a * s) + load1<F32>(p.k, e) * load1<F32>(p.v, e);
+__device__ inline void put_word(uint64_t *w, uint32_t hi, float lo) {
+    __hip_atomic_store(w, ((uint64_t)hi << 32) | __float_as_uint(lo), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// The state that enters tile m of a chain whose words are `stride` apart;
+// `first` enters tile 0.
+__device__ inline float carry_in(uint64_t *words, int64_t stride, int64_t m, float first) {
+    for (;;) {
+        uint64_t w[kWindow];
+#pragma unroll
+        for (int i = 0; i < kWindow; ++i) {
+            const int64_t at = m - 1 - i;
+            w[i] = ((uint64_t)kState << 32) | __float_as_uint(first);
+            if (at >= 0) w[i] = __hip_atomic_load(words + at * stride, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
-        for (int r = rows - 1; r >= 0; --r) {
-            const int64_t row = b * p.L + n * kStateRows + r, e = row * p.ld + d, o = row * p.ldd + d;
-            const float dy = load1<F32>(p.dy, row * p.D + d);
-            float slope;
-            const float a = decay<LOG>(load1<F32>(p.g, e), slope);
-            const float prev = sm[r][threadIdx.x];
-            const float ds = load1<F32>(p.q, e) * dy + c;
-            if (p.dq) store1<F32>(p.dq, o, dy * s);
-            if (p.dk) store1<F32>(p.dk, o, ds * load1<F32>(p.v, e));
-            if (p.dv) store1<F32>(p.dv, o, ds * load1<F32>(p.k, e));
-            if (p.dg) store1<F32>(p.dg, o, a == 0.0f ? 0.0f : ds * prev * slope);
-            c = a == 0.0f ? 0.0f : a * ds;
-            s = prev;
+        float s = 0.0f;
+        bool known = false;
+#pragma unroll
+        for (int i = kWindow - 1; i >= 0; --i) {
+            const uint32_t hi = (uint32_t)(w[i] >> 32);
+            const float lo = __uint_as_float((uint32_t)w[i]);
+            if (hi == kState) {
+                s = lo;
+                known = true;
+            } else if (hi == kEmpty) {
+                known = false;
+            } else {
+                s = apply(__uint_as_float(hi), lo, s);
+            }
+        }
+        if (known) return s;
+        __builtin_amdgcn_s_sleep(1);
+    }
+}
+
+__global__ __launch_bounds__(256) void scan_init_kernel(uint32_t *counter, uint64_t *words, int64_t n) {
+    const int64_t step = (int64_t)gridDim.x * 256;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += step) words[i] = ~(uint64_t)0;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *counter = 0;
+}
+
+// No rows: the state that leaves is the one that enters.
+__global__ __launch_bounds__(256) void scan_none_kernel(const float *from, float *to, int64_t n) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i < n) to[i] = from ? from[i] : 0.0f;
+}
+
+// What one lane reads and writes at a time: 16 bytes, or one element where
+// pointers, row strides or D are not multiples of that.
+template <bool F32, bool WIDE> struct Lane;
+template <> struct Lane<false, true> {
+    static constexpr int VEC = 8, LANES = 16;
+    typedef u32x4_t raw;
+    __device__ static raw load(const void *p, size_t e) {
+        return __builtin_nontemporal_load((const u32x4_t *)((const bf16_t *)p + e));
+    }
+    __device__ static float get(const raw &r, int i) { return i & 1 ? bf_hi(r[i >> 1]) : bf_lo(r[i >> 1]); }
+    __device__ static void store(void *p, size_t e, const float (&x)[8]) {
+        const u32x4_t r = {pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])};
+        __builtin_nontemporal_store(r, (u32x4_t *)((bf16_t *)p + e));
+    }
+};
+template <> struct Lane<true, true> {
+    static constexpr int VEC = 4, LANES = 16;
+    typedef f32x4_t raw;
+    __device__ static raw load(const void *p, size_t e) {
+        return __builtin_nontemporal_load((const f32x4_t *)((const float *)p + e));
+    }
+    __device__ static float get(const raw &r, int i) { return r[i]; }
+    __device__ static void store(void *p, size_t e, const float (&x)[4]) {
+        const f32x4_t r = {x[0], x[1], x[2], x[3]};
+        __builtin_nontemporal_store(r, (f32x4_t *)((float *)p + e));
+    }
+};
+template <bool F32> struct Lane<F32, false> {
+    static constexpr int VEC = 1, LANES = 64;
+    typedef float raw;
+    __device__ static raw load(const void *p, size_t e) { return load1<F32>(p, e); }
+    __device__ static float get(const raw &r, int) { return r; }
+    __device__ static void store(void *p, size_t e, const float (&x)[1]) { store1<F32>(p, e, x[0]); }
+};
+
+// Geometry of a tile: R rows a lane, NS slices of them, LANES lanes a row.
+template <bool F32, bool WIDE, int ROWS> struct Tile {
+    using L = Lane<F32, WIDE>;
+    static constexpr int VEC = L::VEC, LANES = L::LANES;
+    static constexpr int R = ROWS;
+    static constexpr int NS = kThreads / LANES;
+    static constexpr int T = NS * R;
+    static constexpr int C = LANES * VEC;
+    static_assert(T % kStateRows == 0 && kStateRows % R == 0, "saved states lie on slices");
+};
+template <bool F32, bool WIDE> using FwdTile = Tile<F32, WIDE, WIDE ? 8 : 16>;
+template <bool F32, bool WIDE> using BwdTile = Tile<F32, WIDE, WIDE ? 4 : 16>;
+
+// The tile this workgroup works on: chain position m, batch row b, channel tile.
+__device__ inline void take_tile(const ScanParams &p, int64_t &m, int64_t &b, int64_t &ct) {
+    __shared__ uint32_t ticket;
+    int64_t i = blockIdx.x;
+    if (p.counter) {
+        if (threadIdx.x == 0)
+            ticket = __hip_atomic_fetch_add(p.counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __syncthreads();
+        i = __builtin_amdgcn_readfirstlane(ticket);
+    }
+    ct = i % p.c_tiles;
+    i /= p.c_tiles;
+    b = i % p.B;
+    m = i / p.B;
+}
+
+template <bool F32, bool LOG, bool WIDE>
+__global__ __launch_bounds__(kThreads) void scan_fwd_kernel(ScanParams p) {
+    using G = FwdTile<F32, WIDE>;
+    using Ln = typename G::L;
+    constexpr int VEC = G::VEC, R = G::R, NS = G::NS, C = G::C;
+    __shared__ float sP[NS][C], sS[NS][C], sIn[C];
+
+    int64_t m, b, ct;
+    take_tile(p, m, b, ct);
+    const int lane = threadIdx.x % G::LANES, slice = threadIdx.x / G::LANES;
+    const int64_t t0 = m * G::T + slice * R;          // first row of this lane
+    const int64_t d0 = ct * C + lane * VEC;
+    const bool d_in = d0 < p.D;                       // wide: D is a multiple of VEC
+    const size_t row0 = (size_t)b * p.L;
+    const size_t dd = d_in ? d0 : 0;
+    auto row_at = [&](int r) { return row0 + (t0 + r < p.L ? t0 + r : p.L - 1); };  // rows past the end read the last
+
+    // 1. a and x of the lane's rows, and their composition
+    float a[R][VEC], x[R][VEC];
+    {
+        typename Ln::raw g[R], k[R], v[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const size_t e = row_at(r) * p.ld + dd;
+            g[r] = Ln::load(p.g, e);
+            k[r] = Ln::load(p.k, e);
+            v[r] = Ln::load(p.v, e);
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const bool in = t0 + r < p.L;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                a[r][i] = in ? decay<LOG>(Ln::get(g[r], i)) : 1.0f;  // rows past the end pass the state on
+                x[r][i] = in ? Ln::get(k[r], i) * Ln::get(v[r], i) : 0.0f;
+            }
         }
     }
-    if (p.ds0) p.ds0[i] = c;
+    typename Ln::raw q[R];
+    if (p.y) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) q[r] = Ln::load(p.q, row_at(r) * p.ld + dd);
+    }
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+        float P = 1.0f, S = 0.0f, least = 1.0f;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            P *= a[r][i];
+            least = fminf(least, a[r][i]);
+            S = apply(a[r][i], x[r][i], S);
+        }
+        sP[slice][lane * VEC + i] = keep_off_zero(P, least);
+        sS[slice][lane * VEC + i] = S;
+    }
+    __syncthreads();
+
+    // 2. one lane per channel: the slices' maps from the tile's start on, and the carry
+    if (threadIdx.x < C) {
+        const int c = threadIdx.x;
+        const int64_t d = ct * C + c;
+        float P = 1.0f, S = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NS; ++j) {
+            const float pj = sP[j][c], sj = sS[j][c];
+            sP[j][c] = P, sS[j][c] = S;
+            P = join(P, pj), S = apply(pj, sj, S);
+        }
+        const float first = p.s0 && d < p.D ? p.s0[b * p.D + d] : 0.0f;
+        float in = first;
+        if (p.counter) {
+            const int64_t pitch = p.c_tiles * C, stride = p.B * pitch;
+            uint64_t *words = p.words + b * pitch + ct * C + c;
+            if (m > 0) {
+                if (m + 1 < p.n_tiles) put_word(words + m * stride, __float_as_uint(P), S);
+                in = carry_in(words, stride, m, first);
+            }
+            if (m + 1 < p.n_tiles) put_word(words + m * stride, kState, apply(P, S, in));
+        }
+        sIn[c] = in;
+        if (p.s_last && m + 1 == p.n_tiles && d < p.D) p.s_last[b * p.D + d] = apply(P, S, in);
+    }
+    __syncthreads();
+
+    // 3. the walk
+    float s[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+        const int c = lane * VEC + i;
+        s[i] = apply(sP[slice][c], sS[slice][c], sIn[c]);
+    }
+    if (!d_in) return;
+    if (p.states && t0 % kStateRows == 0 && t0 < p.L) {
+        const int64_t chunks = ceil_div(p.L, kStateRows);
+        float *to = p.states + (b * chunks + t0 / kStateRows) * p.D + d0;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) to[i] = s[i];
+    }
+    if (!p.y) return;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        if (t0 + r >= p.L) break;
+        float y[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            s[i] = apply(a[r][i], x[r][i], s[i]);
+            y[i] = Ln::get(q[r], i) * s[i];
+        }
+        Ln::store(p.y, (row0 + t0 + r) * p.D + d0, y);
+    }
+}
+
+// The backward walks chains from the end of time: c -> a (q dy + c) maps the
+// gradient of a row's state to that of the row before, with the same decays.
+// The states inside a tile are walked again from the saved state at its start.
+template <bool F32, bool LOG, bool WIDE>
+__global__ __launch_bounds__(kThreads) void scan_bwd_kernel(ScanParams p) {
+    using G = BwdTile<F32, WIDE>;
+    using Ln = typename G::L;
+    constexpr int VEC = G::VEC, R = G::R, NS = G::NS, C = G::C;
+    __shared__ float sP[NS][C], sS[NS][C], sC[NS][C], sIn[C];
+
+    int64_t m, b, ct;
+    take_tile(p, m, b, ct);
+    const int64_t n = p.n_tiles - 1 - m;
+    const int lane = threadIdx.x % G::LANES, slice = threadIdx.x / G::LANES;
+    const int64_t t0 = n * G::T + slice * R;
+    const int64_t d0 = ct * C + lane * VEC;
+    const bool d_in = d0 < p.D;
+    const size_t row0 = (size_t)b * p.L;
+    const size_t dd = d_in ? d0 : 0;
+    auto row_at = [&](int r) { return row0 + (t0 + r < p.L ? t0 + r : p.L - 1); };
+
+    typename Ln::raw g[R], k[R], v[R], q[R], dy[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const size_t e = row_at(r) * p.ld + dd;
+        g[r] = Ln::load(p.g, e);
+        k[r] = Ln::load(p.k, e);
+        v[r] = Ln::load(p.v, e);
+        q[r] = Ln::load(p.q, e);
+        dy[r] = Ln::load(p.dy, row_at(r) * p.D + dd);
+    }
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+        float P = 1.0f, S = 0.0f, least = 1.0f, a[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const bool in = t0 + r < p.L;
+            a[r] = in ? decay<LOG>(Ln::get(g[r], i)) : 1.0f;
+            P *= a[r];
+            least = fminf(least, a[r]);
+            S = apply(a[r], in ? Ln::get(k[r], i) * Ln::get(v[r], i) : 0.0f, S);
+        }
+        float c = 0.0f;
+#pragma unroll
+        for (int r = R - 1; r >= 0; --r) {
+            const float u = t0 + r < p.L ? Ln::get(q[r], i) * Ln::get(dy[r], i) : 0.0f;
+            c = apply(a[r], 0.0f, u + c);
+        }
+        sP[slice][lane * VEC + i] = keep_off_zero(P, least);
+        sS[slice][lane * VEC + i] = S;
+        sC[slice][lane * VEC + i] = c;
+    }
+    __syncthreads();
+
+    if (threadIdx.x < C) {
+        const int c = threadIdx.x;
+        const int64_t d = ct * C + c;
+        // the state that enters each slice
+        float s = 0.0f;
+        if (d < p.D) s = p.states_in[(b * ceil_div(p.L, kStateRows) + n * (G::T / kStateRows)) * p.D + d];
+#pragma unroll
+        for (int j = 0; j < NS; ++j) {
+            const float pj = sP[j][c], sj = sS[j][c];
+            sS[j][c] = s;
+            s = apply(pj, sj, s);
+        }
+        // the maps from the tile's end back to the end of each slice
+        float P = 1.0f, S = 0.0f;
+#pragma unroll
+        for (int j = NS - 1; j >= 0; --j) {
+            const float pj = sP[j][c], cj = sC[j][c];
+            sP[j][c] = P, sC[j][c] = S;
+            P = join(P, pj), S = apply(pj, cj, S);
+        }
+        const float first = p.ds_last && d < p.D ? p.ds_last[b * p.D + d] : 0.0f;
+        float in = first;
+        if (p.counter) {
+            const int64_t pitch = p.c_tiles * C, stride = p.B * pitch;
+            uint64_t *words = p.words + b * pitch + ct * C + c;
+            if (m > 0) {
+                if (m + 1 < p.n_tiles) put_word(words + m * stride, __float_as_uint(P), S);
+                in = carry_in(words, stride, m, first);
+            }
+            if (m + 1 < p.n_tiles) put_word(words + m * stride, kState, apply(P, S, in));
+        }
+        sIn[c] = in;
+        if (p.ds0 && m + 1 == p.n_tiles && d < p.D) p.ds0[b * p.D + d] = apply(P, S, in);
+    }
+    __syncthreads();
+    if (!d_in) return;
+
+    float s[R + 1][VEC], c[VEC];  // s[r]: before row r
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+        const int ch = lane * VEC + i;
+        s[0][i] = sS[slice][ch];
+        c[i] = apply(sP[slice][ch], sC[slice][ch], sIn[ch]);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            s[r + 1][i] = apply(decay<LOG>(Ln::get(g[r], i)), Ln::get(k[r], i) * Ln::get(v[r], i), s[r][i]);
+    }
+#pragma unroll
+    for (int r = R - 1; r >= 0; --r) {
+        if (t0 + r >= p.L) continue;
+        float dq[VEC], dk[VEC], dv[VEC], dg[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            float slope;
+            const float a = decay<LOG>(Ln::get(g[r], i), slope), dyi = Ln::get(dy[r], i);
+            const float ds = fmaf(Ln::get(q[r], i), dyi, c[i]);
+            dq[i] = dyi * s[r + 1][i];
+            dk[i] = ds * Ln::get(v[r], i);
+            dv[i] = ds * Ln::get(k[r], i);
+            dg[i] = a == 0.0f ? 0.0f : ds * s[r][i] * slope;
+            c[i] = a == 0.0f ? 0.0f : a * ds;
+        }
+        const size_t o = (row0 + t0 + r) * p.ldd + d0;
+        if (p.dq) Ln::store(p.dq, o, dq);
+        if (p.dk) Ln::store(p.dk, o, dk);
+        if (p.dv) Ln::store(p.dv, o, dv);
+        if (p.dg) Ln::store(p.dg, o, dg);
+    }
 }
 
 int check_sizes(int64_t B, int64_t L, int64_t D, int gate, int dtype) {
@@ -79,11 +420,53 @@ int check_sizes(int64_t B, int64_t L, int64_t D, int gate, int dtype) {
     return HYENA_OK;
 }
 
-template <typename K> int launch(K kernel, const ScanParams &p, void *stream) {
-    const int64_t blocks = ceil_div(p.B * p.D, 64);
-    if (blocks > 0x7fffffff) return HYENA_ERR_UNSUPPORTED;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(64), 0, (hipStream_t)stream, p);
+// Rows and channels of the smallest tile of any variant bound the words.
+constexpr int64_t kLeastRows = 64, kMostChannels = 128;
+
+int64_t workspace_bytes(int64_t B, int64_t L, int64_t D) {
+    if (L <= kLeastRows || B == 0 || D == 0) return 0;
+    return 16 + 8 * ceil_div(L, kLeastRows) * B * (ceil_div(D, kMostChannels) * kMostChannels);
+}
+
+template <typename G, typename K> int launch(K kernel, ScanParams p, void *workspace, void *stream) {
+    static_assert(G::T >= kLeastRows && kMostChannels % G::C == 0, "the workspace holds every variant's words");
+    p.n_tiles = ceil_div(p.L, G::T);
+    p.c_tiles = ceil_div(p.D, G::C);
+    int64_t blocks;
+    if (!mul_fits(p.n_tiles, p.B, p.c_tiles, &blocks) || blocks > 0x7fffffff) return HYENA_ERR_UNSUPPORTED;
+    hipStream_t s = (hipStream_t)stream;
+    if (p.n_tiles > 1) {
+        p.counter = (uint32_t *)workspace;
+        p.words = (uint64_t *)((char *)workspace + 16);
+        const int64_t words = p.n_tiles * p.B * p.c_tiles * G::C;
+        const int64_t grid = ceil_div(words, 1024);
+        hipLaunchKernelGGL(scan_init_kernel, dim3((unsigned)(grid < 2048 ? grid : 2048)), dim3(256), 0, s, p.counter,
+                           p.words, words);
+    }
+    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(kThreads), 0, s, p);
     return launch_status();
+}
+
+int launch_none(const float *from, float *to, int64_t n, void *stream) {
+    if (!to) return HYENA_OK;
+    if (ceil_div(n, 256) > 0x7fffffff) return HYENA_ERR_UNSUPPORTED;
+    hipLaunchKernelGGL(scan_none_kernel, dim3((unsigned)ceil_div(n, 256)), dim3(256), 0, (hipStream_t)stream, from, to, n);
+    return launch_status();
+}
+
+template <bool F32, bool LOG, bool WIDE> int launch_fwd(const ScanParams &p, void *ws, void *stream) {
+    return launch<FwdTile<F32, WIDE>>(scan_fwd_kernel<F32, LOG, WIDE>, p, ws, stream);
+}
+template <bool F32, bool LOG, bool WIDE> int launch_bwd(const ScanParams &p, void *ws, void *stream) {
+    return launch<BwdTile<F32, WIDE>>(scan_bwd_kernel<F32, LOG, WIDE>, p, ws, stream);
+}
+
+// 16-byte accesses of all of these arrays (null ones do not matter).
+bool wide_ok(int64_t D, int64_t ld, int64_t ldd, int64_t eb, std::initializer_list<const void *> ps) {
+    if ((D * eb) % 16 || (ld * eb) % 16 || (ldd * eb) % 16) return false;
+    for (const void *p : ps)
+        if (!aligned(p, 16)) return false;
+    return true;
 }
 
 }  // namespace
@@ -97,7 +480,7 @@ int hyena_scan_workspace(int64_t B, int64_t L, int64_t D, int dtype, int64_t *by
     const int st = check_sizes(B, L, D, HYENA_GATE_SIGMOID, dtype);
     if (st != HYENA_OK) return st;
     if (!bytes_out) return HYENA_ERR_NULL;
-    *bytes_out = 0;
+    *bytes_out = workspace_bytes(B, L, D);
     return HYENA_OK;
 }
 
@@ -134,8 +517,12 @@ int hyena_scan_fwd(const void *q, const void *k, const void *v, const void *g, i
     p.y = y, p.s_last = s_last, p.states = states;
     p.B = B, p.L = L, p.D = D, p.ld = ld;
     const bool f32 = dtype == HYENA_DTYPE_F32, lg = gate == HYENA_GATE_LOG;
-    return launch(f32 ? (lg ? scan_fwd_kernel<true, true> : scan_fwd_kernel<true, false>)
-                      : (lg ? scan_fwd_kernel<false, true> : scan_fwd_kernel<false, false>), p, stream);
+    if (L == 0) return launch_none(s0, s_last, B * D, stream);
+    if (wide_ok(D, ld, D, eb, {q, k, v, g, y}))
+        return f32 ? (lg ? launch_fwd<true, true, true>(p, workspace, stream) : launch_fwd<true, false, true>(p, workspace, stream))
+                   : (lg ? launch_fwd<false, true, true>(p, workspace, stream) : launch_fwd<false, false, true>(p, workspace, stream));
+    return f32 ? (lg ? launch_fwd<true, true, false>(p, workspace, stream) : launch_fwd<true, false, false>(p, workspace, stream))
+               : (lg ? launch_fwd<false, true, false>(p, workspace, stream) : launch_fwd<false, false, false>(p, workspace, stream));
 }
 
 int hyena_scan_bwd(const void *q, const void *k, const void *v, const void *g, const void *dy, const float *states,
@@ -174,8 +561,12 @@ int hyena_scan_bwd(const void *q, const void *k, const void *v, const void *g, c
     p.dq = dq, p.dk = dk, p.dv = dv, p.dg = dg, p.ds0 = ds0;
     p.B = B, p.L = L, p.D = D, p.ld = ld, p.ldd = ldd;
     const bool f32 = dtype == HYENA_DTYPE_F32, lg = gate == HYENA_GATE_LOG;
-    return launch(f32 ? (lg ? scan_bwd_kernel<true, true> : scan_bwd_kernel<true, false>)
-                      : (lg ? scan_bwd_kernel<false, true> : scan_bwd_kernel<false, false>), p, stream);
+    if (L == 0) return launch_none(ds_last, ds0, B * D, stream);
+    if (wide_ok(D, ld, ldd, eb, {q, k, v, g, dy, dq, dk, dv, dg}))
+        return f32 ? (lg ? launch_bwd<true, true, true>(p, workspace, stream) : launch_bwd<true, false, true>(p, workspace, stream))
+                   : (lg ? launch_bwd<false, true, true>(p, workspace, stream) : launch_bwd<false, false, true>(p, workspace, stream));
+    return f32 ? (lg ? launch_bwd<true, true, false>(p, workspace, stream) : launch_bwd<true, false, false>(p, workspace, stream))
+               : (lg ? launch_bwd<false, true, false>(p, workspace, stream) : launch_bwd<false, false, false>(p, workspace, stream));
 }
 
 }  // extern "C"
