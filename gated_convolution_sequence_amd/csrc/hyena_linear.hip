@@ -33,6 +33,14 @@ typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef short s16x8_t __attribute__((ext_vector_type(8)));
 #define LDS_PTR __attribute__((address_space(3)))
 
+// sigmoid(z), and its slope e r^2 with e = exp(-|z|), r = 1 / (1 + e): finite
+// for every z, and exact to rounding at both ends.
+__device__ inline float sigmoid(float z, float &slope) {
+    const float e = __expf(-fabsf(z)), r = __builtin_amdgcn_rcpf(1.0f + e);
+    slope = e * r * r;
+    return z < 0.0f ? e * r : r;
+}
+
 template <int ACT> __device__ inline float act_value(float z) {
     if constexpr (ACT == HYENA_ACT_RELU) return z < 0.0f ? 0.0f : z;
     else if constexpr (ACT == HYENA_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
@@ -48,11 +56,11 @@ template <int ACT> __device__ inline float act_slope(float z) {
         return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) + z * __expf(-0.5f * z * z) * 0.39894228040143268f;
     } else if constexpr (ACT == HYENA_ACT_SILU) {
         float slope;
-        const float p = decay<false>(z, slope);
+        const float p = sigmoid(z, slope);
         return p + z * slope;
     } else if constexpr (ACT == HYENA_ACT_SIGMOID) {
         float slope;
-        decay<false>(z, slope);
+        sigmoid(z, slope);
         return slope;
     } else {
         return 1.0f;
@@ -170,32 +178,41 @@ template <bool F32, bool TALL, int X, int NT> struct Operand {
         row = q / ROW_CHUNKS;
         const int c = q % ROW_CHUNKS;
         if constexpr (TALL) chunk = ((c / BC) ^ turn(row)) * BC + c % BC;
-        else chunk = c ^ (row & 7);
+        else chunk = c ^ (row >> 1 & 7);
     }
 
     // Direct loads.  off[i]: the lane's byte offset in the tile, or past every
-    // range where its m is outside the matrix; `edge`: its first value of c.
-    __device__ static void plan(uint32_t (&off)[LOADS], int (&edge)[LOADS], int64_t ld, int x_left) {
+    // range where its m is outside the matrix.
+    static constexpr uint32_t kOutside = 0x80000000u;
+    __device__ static void plan(uint32_t (&off)[LOADS], int64_t ld, int x_left) {
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {
             int row, chunk;
             source(i * NT + threadIdx.x, row, chunk);
             const int x = TALL ? chunk * CE : row;
             off[i] = x < x_left ? (uint32_t)(row * ld + chunk * CE) * sizeof(typename El<F32>::type) : kOutside;
-            edge[i] = TALL ? row : chunk * CE;
         }
     }
-    static constexpr uint32_t kOutside = 0x80000000u;
-    __device__ static void fetch(const typename El<F32>::type *tile, const uint32_t (&off)[LOADS],
-                                 const int (&edge)[LOADS], int c_left, LDS_PTR unsigned char *lds) {
+    __device__ static void fetch(const typename El<F32>::type *tile, const uint32_t (&off)[LOADS], int c_left,
+                                 LDS_PTR unsigned char *lds) {
         // offsets stay below 2^31 (the host checks), so only kOutside is out of range
         const __amdgpu_buffer_rsrc_t rs =
             __builtin_amdgcn_make_buffer_rsrc((void *)tile, (short)0, 0x7fffffff, 0x00020000);
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        if (c_left >= BK) {
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LDS_PTR void *)(lds + (i * NT + wave * 64) * 16), 16,
-                                                     edge[i] < c_left ? off[i] : kOutside, 0, 0, 0);
+            for (int i = 0; i < LOADS; ++i)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LDS_PTR void *)(lds + (i * NT + wave * 64) * 16), 16,
+                                                         off[i], 0, 0, 0);
+        } else {  // the last step: zeros past the end of c
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) {
+                int row, chunk;
+                source(i * NT + threadIdx.x, row, chunk);
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LDS_PTR void *)(lds + (i * NT + wave * 64) * 16), 16,
+                                                         (TALL ? row : chunk * CE) < c_left ? off[i] : kOutside, 0, 0, 0);
+            }
+        }
     }
     // Single elements, through registers.
     __device__ static void fetch_narrow(const typename El<F32>::type *tile, int64_t ld, int x_left, int c_left,
@@ -222,7 +239,7 @@ template <bool F32, bool TALL, int X, int NT> struct Operand {
     __device__ static typename El<F32>::frag read(LDS_PTR unsigned char *lds, int x0, int kk, int i, int j) {
         if constexpr (!TALL) {
             const int row = x0 + i;
-            return *(LDS_PTR typename El<F32>::frag *)(lds + row * 128 + (((kk * 4 + j) ^ (row & 7)) << 4));
+            return *(LDS_PTR typename El<F32>::frag *)(lds + row * 128 + (((kk * 4 + j) ^ (row >> 1 & 7)) << 4));
         } else if constexpr (F32) {
             f32x4_t f;
 #pragma unroll
@@ -288,15 +305,14 @@ __global__ __launch_bounds__(64 * WM *WN, 2) void gemm_kernel(GemmParams p) {
     const int64_t step_a = TALL_A ? BK * p.lda : BK, step_b = TALL_B ? BK * p.ldb : BK;
 
     uint32_t off_a[A::LOADS], off_b[B::LOADS];
-    int edge_a[A::LOADS], edge_b[B::LOADS];
     if constexpr (DIRECT) {
-        A::plan(off_a, edge_a, p.lda, p.M - m0);
-        B::plan(off_b, edge_b, p.ldb, p.N - n0);
+        A::plan(off_a, p.lda, p.M - m0);
+        B::plan(off_b, p.ldb, p.N - n0);
     }
     auto fetch = [&](unsigned char *la, unsigned char *lb, int c_left) {
         if constexpr (DIRECT) {
-            A::fetch(a, off_a, edge_a, c_left, (LDS_PTR unsigned char *)la);
-            B::fetch(b, off_b, edge_b, c_left, (LDS_PTR unsigned char *)lb);
+            A::fetch(a, off_a, c_left, (LDS_PTR unsigned char *)la);
+            B::fetch(b, off_b, c_left, (LDS_PTR unsigned char *)lb);
         } else {
             A::fetch_narrow(a, p.lda, p.M - m0, c_left, (LDS_PTR unsigned char *)la);
             B::fetch_narrow(b, p.ldb, p.N - n0, c_left, (LDS_PTR unsigned char *)lb);

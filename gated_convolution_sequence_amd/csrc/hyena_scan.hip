@@ -31,7 +31,7 @@
 // at 0 exactly where a run holds such a gate, and off 0 (at the least positive
 // fp32) where a product of small gates underflows.
 
-#include <initializer_list>
+#include <type_traits>
 
 #include "layer_common.h"
 
@@ -39,7 +39,8 @@ namespace layer {
 namespace {
 
 constexpr int kWindow = 8;
-constexpr int kThreads = 256;
+constexpr int kMostCounters = 32;
+constexpr int kCounterGap = 32;  // counters lie on lines of their own
 constexpr uint32_t kEmpty = 0xffffffffu;  // high half of a word not yet written
 constexpr uint32_t kState = 0x80000000u;  // high half of a word that holds a state (a map has P >= 0 there)
 
@@ -50,7 +51,9 @@ struct ScanParams {
     float *s_last, *states, *ds0;
     int64_t B, L, D, ld, ldd;
     int64_t n_tiles, c_tiles;  // tiles of a chain, channel tiles of a row
-    uint32_t *counter;         // tiles handed out so far; null: one tile a chain, nothing to carry
+    int64_t n_chains;          // B * c_tiles
+    uint32_t *counters;        // tiles handed out so far, one every kCounterGap; null: one tile a chain, no carries
+    int32_t n_counters;        // a power of two that divides n_chains
     uint64_t *words;           // [n_tiles][B][c_tiles * C]
 };
 
@@ -98,10 +101,10 @@ __device__ inline float carry_in(uint64_t *words, int64_t stride, int64_t m, flo
     }
 }
 
-__global__ __launch_bounds__(256) void scan_init_kernel(uint32_t *counter, uint64_t *words, int64_t n) {
+__global__ __launch_bounds__(256) void scan_init_kernel(uint32_t *counters, uint64_t *words, int64_t n) {
     const int64_t step = (int64_t)gridDim.x * 256;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += step) words[i] = ~(uint64_t)0;
-    if (blockIdx.x == 0 && threadIdx.x == 0) *counter = 0;
+    if (blockIdx.x == 0 && threadIdx.x < kMostCounters) counters[threadIdx.x * kCounterGap] = 0;
 }
 
 // No rows: the state that leaves is the one that enters.
@@ -110,131 +113,213 @@ __global__ __launch_bounds__(256) void scan_none_kernel(const float *from, float
     if (i < n) to[i] = from ? from[i] : 0.0f;
 }
 
-// What one lane reads and writes at a time: 16 bytes, or one element where
-// pointers, row strides or D are not multiples of that.
-template <bool F32, bool WIDE> struct Lane;
-template <> struct Lane<false, true> {
-    static constexpr int VEC = 8, LANES = 16;
+// What one lane reads and writes at a time: 16 bytes at any element's address
+// (the hardware takes global accesses of any alignment), or the first n
+// channels of them at the right edge of D.
+template <bool F32> struct Lane;
+template <> struct Lane<false> {
+    static constexpr int VEC = 8;
     typedef u32x4_t raw;
+    typedef u32x4_t raw_any __attribute__((aligned(2)));
     __device__ static raw load(const void *p, size_t e) {
-        return __builtin_nontemporal_load((const u32x4_t *)((const bf16_t *)p + e));
+        return __builtin_nontemporal_load((const raw_any *)((const bf16_t *)p + e));
+    }
+    __device__ static raw load_part(const void *p, size_t e, int n) {
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = i < n ? load1<false>(p, e + i) : 0.0f;
+        return pack(x);
     }
     __device__ static float get(const raw &r, int i) { return i & 1 ? bf_hi(r[i >> 1]) : bf_lo(r[i >> 1]); }
+    __device__ static raw pack(const float (&x)[8]) {
+        return raw{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])};
+    }
     __device__ static void store(void *p, size_t e, const float (&x)[8]) {
-        const u32x4_t r = {pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])};
-        __builtin_nontemporal_store(r, (u32x4_t *)((bf16_t *)p + e));
+        __builtin_nontemporal_store(pack(x), (raw_any *)((bf16_t *)p + e));
     }
 };
-template <> struct Lane<true, true> {
-    static constexpr int VEC = 4, LANES = 16;
+template <> struct Lane<true> {
+    static constexpr int VEC = 4;
     typedef f32x4_t raw;
+    typedef f32x4_t raw_any __attribute__((aligned(4)));
     __device__ static raw load(const void *p, size_t e) {
-        return __builtin_nontemporal_load((const f32x4_t *)((const float *)p + e));
+        return __builtin_nontemporal_load((const raw_any *)((const float *)p + e));
+    }
+    __device__ static raw load_part(const void *p, size_t e, int n) {
+        raw r;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[i] = i < n ? load1<true>(p, e + i) : 0.0f;
+        return r;
     }
     __device__ static float get(const raw &r, int i) { return r[i]; }
     __device__ static void store(void *p, size_t e, const float (&x)[4]) {
-        const f32x4_t r = {x[0], x[1], x[2], x[3]};
-        __builtin_nontemporal_store(r, (f32x4_t *)((float *)p + e));
+        __builtin_nontemporal_store(raw{x[0], x[1], x[2], x[3]}, (raw_any *)((float *)p + e));
     }
 };
-template <bool F32> struct Lane<F32, false> {
-    static constexpr int VEC = 1, LANES = 64;
-    typedef float raw;
-    __device__ static raw load(const void *p, size_t e) { return load1<F32>(p, e); }
-    __device__ static float get(const raw &r, int) { return r; }
-    __device__ static void store(void *p, size_t e, const float (&x)[1]) { store1<F32>(p, e, x[0]); }
-};
+template <bool F32> __device__ inline void store_part(void *p, size_t e, const float (&x)[Lane<F32>::VEC], int n) {
+#pragma unroll
+    for (int i = 0; i < Lane<F32>::VEC; ++i)
+        if (i < n) store1<F32>(p, e + i, x[i]);
+}
 
 // Geometry of a tile: R rows a lane, NS slices of them, LANES lanes a row.
-template <bool F32, bool WIDE, int ROWS> struct Tile {
-    using L = Lane<F32, WIDE>;
-    static constexpr int VEC = L::VEC, LANES = L::LANES;
+template <bool F32, int THREADS, int ROWS, int LANES_> struct Tile {
+    static constexpr int VEC = Lane<F32>::VEC, LANES = LANES_, NT = THREADS;
     static constexpr int R = ROWS;
-    static constexpr int NS = kThreads / LANES;
+    static constexpr int NS = NT / LANES;
     static constexpr int T = NS * R;
     static constexpr int C = LANES * VEC;
     static_assert(T % kStateRows == 0 && kStateRows % R == 0, "saved states lie on slices");
+    static_assert(C <= NT, "a lane per channel");
 };
-template <bool F32, bool WIDE> using FwdTile = Tile<F32, WIDE, WIDE ? 8 : 16>;
-template <bool F32, bool WIDE> using BwdTile = Tile<F32, WIDE, WIDE ? 4 : 16>;
+template <bool F32> using FwdTile = Tile<F32, 256, 8, 16>;
+template <bool F32> using BwdTile = Tile<F32, 256, 4, 16>;
 
-// The tile this workgroup works on: chain position m, batch row b, channel tile.
-__device__ inline void take_tile(const ScanParams &p, int64_t &m, int64_t &b, int64_t &ct) {
-    __shared__ uint32_t ticket;
-    int64_t i = blockIdx.x;
-    if (p.counter) {
-        if (threadIdx.x == 0)
-            ticket = __hip_atomic_fetch_add(p.counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        __syncthreads();
-        i = __builtin_amdgcn_readfirstlane(ticket);
-    }
-    ct = i % p.c_tiles;
-    i /= p.c_tiles;
-    b = i % p.B;
-    m = i / p.B;
+// Waits for this wave's LDS accesses and meets the others.  Loads from memory
+// stay in flight (__syncthreads would wait for them).
+__device__ inline void lds_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
 }
 
-template <bool F32, bool LOG, bool WIDE>
-__global__ __launch_bounds__(kThreads) void scan_fwd_kernel(ScanParams p) {
-    using G = FwdTile<F32, WIDE>;
-    using Ln = typename G::L;
+// Tiles in order: ticket i is tile i / n_chains of chain i % n_chains.
+// Counter j hands out the tickets that are j modulo n_counters, so a chain's
+// tiles come from one counter, in order.  One ticket a workgroup.
+__device__ inline int64_t next_ticket(const ScanParams &p) {
+    if (!p.counters) return blockIdx.x;
+    const int j = blockIdx.x & (p.n_counters - 1);
+    const uint32_t t = __hip_atomic_fetch_add(p.counters + j * kCounterGap, 1u, __ATOMIC_RELAXED,
+                                              __HIP_MEMORY_SCOPE_AGENT);
+    return (int64_t)t * p.n_counters + j;
+}
+
+__device__ inline int64_t uniform(int64_t x) {
+    return (int64_t)(((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)x >> 32)) << 32) |
+                     (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)x));
+}
+
+// Where a lane stands in the tile of a ticket.
+template <typename G> struct Place {
+    int64_t m, b, ct;    // chain position, batch row, channel tile
+    int64_t t0, d0;      // the lane's first row and channel
+    int n_ch;            // its channels; <= 0: none
+    __device__ void set(const ScanParams &p, int64_t ticket, bool backward) {
+        const int64_t chain = ticket % p.n_chains;
+        m = ticket / p.n_chains;
+        ct = chain % p.c_tiles;
+        b = chain / p.c_tiles;
+        t0 = (backward ? p.n_tiles - 1 - m : m) * G::T + threadIdx.x / G::LANES * G::R;
+        d0 = ct * G::C + threadIdx.x % G::LANES * G::VEC;
+        n_ch = (int)min((int64_t)G::VEC, p.D - d0);
+    }
+    // Row r of the lane in [B L]; rows past the end read the last one.
+    __device__ size_t row(const ScanParams &p, int r) const {
+        return (size_t)b * p.L + (t0 + r < p.L ? t0 + r : p.L - 1);
+    }
+};
+
+// Whether any lane of the wave says so.
+__device__ inline bool any_lane(bool x) { return __builtin_amdgcn_ballot_w64(x) != 0; }
+
+// s -> a s + x; RESETS: where a may be 0 and must drop s.
+template <bool RESETS> __device__ inline float walk(float a, float x, float s) {
+    if constexpr (RESETS) return apply(a, x, s);
+    else return fmaf(a, s, x);
+}
+
+template <bool F32, bool LOG>
+__global__ __launch_bounds__(FwdTile<F32>::NT, 2) void scan_fwd_kernel(ScanParams p) {
+    using G = FwdTile<F32>;
+    using Ln = Lane<F32>;
     constexpr int VEC = G::VEC, R = G::R, NS = G::NS, C = G::C;
     __shared__ float sP[NS][C], sS[NS][C], sIn[C];
+    __shared__ int64_t sTicket;
 
-    int64_t m, b, ct;
-    take_tile(p, m, b, ct);
+    if (threadIdx.x == 0) sTicket = next_ticket(p);
+    __syncthreads();
+    Place<G> at;
+    at.set(p, uniform(sTicket), false);
     const int lane = threadIdx.x % G::LANES, slice = threadIdx.x / G::LANES;
-    const int64_t t0 = m * G::T + slice * R;          // first row of this lane
-    const int64_t d0 = ct * C + lane * VEC;
-    const bool d_in = d0 < p.D;                       // wide: D is a multiple of VEC
-    const size_t row0 = (size_t)b * p.L;
-    const size_t dd = d_in ? d0 : 0;
-    auto row_at = [&](int r) { return row0 + (t0 + r < p.L ? t0 + r : p.L - 1); };  // rows past the end read the last
 
     // 1. a and x of the lane's rows, and their composition
     float a[R][VEC], x[R][VEC];
     {
-        typename Ln::raw g[R], k[R], v[R];
+        typename Ln::raw g[R] = {}, k[R] = {}, v[R] = {};
+        if (at.n_ch == VEC) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const size_t e = row_at(r) * p.ld + dd;
-            g[r] = Ln::load(p.g, e);
-            k[r] = Ln::load(p.k, e);
-            v[r] = Ln::load(p.v, e);
-        }
+            for (int r = 0; r < R; ++r) {
+                const size_t e = at.row(p, r) * p.ld + at.d0;
+                g[r] = Ln::load(p.g, e);
+                k[r] = Ln::load(p.k, e);
+                v[r] = Ln::load(p.v, e);
+            }
+        } else if (at.n_ch > 0) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const bool in = t0 + r < p.L;
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                a[r][i] = in ? decay<LOG>(Ln::get(g[r], i)) : 1.0f;  // rows past the end pass the state on
-                x[r][i] = in ? Ln::get(k[r], i) * Ln::get(v[r], i) : 0.0f;
+            for (int r = 0; r < R; ++r) {
+                const size_t e = at.row(p, r) * p.ld + at.d0;
+                g[r] = Ln::load_part(p.g, e, at.n_ch);
+                k[r] = Ln::load_part(p.k, e, at.n_ch);
+                v[r] = Ln::load_part(p.v, e, at.n_ch);
             }
         }
-    }
-    typename Ln::raw q[R];
-    if (p.y) {
-#pragma unroll
-        for (int r = 0; r < R; ++r) q[r] = Ln::load(p.q, row_at(r) * p.ld + dd);
-    }
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-        float P = 1.0f, S = 0.0f, least = 1.0f;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            P *= a[r][i];
-            least = fminf(least, a[r][i]);
-            S = apply(a[r][i], x[r][i], S);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                a[r][i] = decay<LOG>(Ln::get(g[r], i));
+                x[r][i] = Ln::get(k[r], i) * Ln::get(v[r], i);
+            }
         }
-        sP[slice][lane * VEC + i] = keep_off_zero(P, least);
-        sS[slice][lane * VEC + i] = S;
+        if (at.t0 + R > p.L) {  // rows past the end pass the state on
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int i = 0; i < VEC; ++i)
+                    if (at.t0 + r >= p.L) a[r][i] = 1.0f, x[r][i] = 0.0f;
+        }
     }
-    __syncthreads();
+    typename Ln::raw q[R] = {};
+    if (p.y && at.n_ch == VEC) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) q[r] = Ln::load(p.q, at.row(p, r) * p.ld + at.d0);
+    } else if (p.y && at.n_ch > 0) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) q[r] = Ln::load_part(p.q, at.row(p, r) * p.ld + at.d0, at.n_ch);
+    }
+    float P[VEC], S[VEC], least[VEC], least_of_all = 1.0f;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+        least[i] = P[i] = a[0][i];
+#pragma unroll
+        for (int r = 1; r < R; ++r) {
+            P[i] *= a[r][i];
+            least[i] = fminf(least[i], a[r][i]);
+        }
+        least_of_all = fminf(least_of_all, least[i]);
+    }
+    const bool resets = any_lane(least_of_all == 0.0f);
+    auto compose = [&](auto sel) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            S[i] = x[0][i];
+#pragma unroll
+            for (int r = 1; r < R; ++r) S[i] = walk<decltype(sel)::value>(a[r][i], x[r][i], S[i]);
+        }
+    };
+    if (resets) compose(std::true_type());
+    else compose(std::false_type());
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+        sP[slice][lane * VEC + i] = keep_off_zero(P[i], least[i]);
+        sS[slice][lane * VEC + i] = S[i];
+    }
+    lds_barrier();
 
     // 2. one lane per channel: the slices' maps from the tile's start on, and the carry
     if (threadIdx.x < C) {
         const int c = threadIdx.x;
-        const int64_t d = ct * C + c;
+        const int64_t d = at.ct * C + c;
         float P = 1.0f, S = 0.0f;
 #pragma unroll
         for (int j = 0; j < NS; ++j) {
@@ -242,172 +327,223 @@ __global__ __launch_bounds__(kThreads) void scan_fwd_kernel(ScanParams p) {
             sP[j][c] = P, sS[j][c] = S;
             P = join(P, pj), S = apply(pj, sj, S);
         }
-        const float first = p.s0 && d < p.D ? p.s0[b * p.D + d] : 0.0f;
-        float in = first;
-        if (p.counter) {
+        float in = p.s0 && d < p.D ? p.s0[at.b * p.D + d] : 0.0f;
+        if (p.counters) {
             const int64_t pitch = p.c_tiles * C, stride = p.B * pitch;
-            uint64_t *words = p.words + b * pitch + ct * C + c;
-            if (m > 0) {
-                if (m + 1 < p.n_tiles) put_word(words + m * stride, __float_as_uint(P), S);
-                in = carry_in(words, stride, m, first);
+            uint64_t *words = p.words + at.b * pitch + at.ct * C + c;
+            if (at.m > 0) {
+                if (at.m + 1 < p.n_tiles) put_word(words + at.m * stride, __float_as_uint(P), S);
+                in = carry_in(words, stride, at.m, in);
             }
-            if (m + 1 < p.n_tiles) put_word(words + m * stride, kState, apply(P, S, in));
+            if (at.m + 1 < p.n_tiles) put_word(words + at.m * stride, kState, apply(P, S, in));
         }
         sIn[c] = in;
-        if (p.s_last && m + 1 == p.n_tiles && d < p.D) p.s_last[b * p.D + d] = apply(P, S, in);
+        if (p.s_last && at.m + 1 == p.n_tiles && d < p.D) p.s_last[at.b * p.D + d] = apply(P, S, in);
     }
-    __syncthreads();
+    lds_barrier();
 
     // 3. the walk
+    if (at.n_ch <= 0) return;
     float s[VEC];
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
         const int c = lane * VEC + i;
         s[i] = apply(sP[slice][c], sS[slice][c], sIn[c]);
     }
-    if (!d_in) return;
-    if (p.states && t0 % kStateRows == 0 && t0 < p.L) {
+    if (p.states && at.t0 % kStateRows == 0 && at.t0 < p.L) {
         const int64_t chunks = ceil_div(p.L, kStateRows);
-        float *to = p.states + (b * chunks + t0 / kStateRows) * p.D + d0;
+        float *to = p.states + (at.b * chunks + at.t0 / kStateRows) * p.D + at.d0;
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) to[i] = s[i];
+        for (int i = 0; i < VEC; ++i)
+            if (i < at.n_ch) to[i] = s[i];
     }
     if (!p.y) return;
+    auto outputs = [&](auto sel) {
+        const size_t first = ((size_t)at.b * p.L + at.t0) * p.D + at.d0;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        if (t0 + r >= p.L) break;
-        float y[VEC];
+        for (int r = 0; r < R; ++r) {
+            float y[VEC];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            s[i] = apply(a[r][i], x[r][i], s[i]);
-            y[i] = Ln::get(q[r], i) * s[i];
+            for (int i = 0; i < VEC; ++i) {
+                s[i] = walk<decltype(sel)::value>(a[r][i], x[r][i], s[i]);
+                y[i] = Ln::get(q[r], i) * s[i];
+            }
+            if (at.t0 + r >= p.L) continue;
+            if (at.n_ch == VEC) Ln::store(p.y, first + (size_t)r * p.D, y);
+            else store_part<F32>(p.y, first + (size_t)r * p.D, y, at.n_ch);
         }
-        Ln::store(p.y, (row0 + t0 + r) * p.D + d0, y);
-    }
+    };
+    if (resets) outputs(std::true_type());
+    else outputs(std::false_type());
 }
 
 // The backward walks chains from the end of time: c -> a (q dy + c) maps the
 // gradient of a row's state to that of the row before, with the same decays.
 // The states inside a tile are walked again from the saved state at its start.
-template <bool F32, bool LOG, bool WIDE>
-__global__ __launch_bounds__(kThreads) void scan_bwd_kernel(ScanParams p) {
-    using G = BwdTile<F32, WIDE>;
-    using Ln = typename G::L;
+template <bool F32, bool LOG>
+__global__ __launch_bounds__(BwdTile<F32>::NT, 2) void scan_bwd_kernel(ScanParams p) {
+    using G = BwdTile<F32>;
+    using Ln = Lane<F32>;
     constexpr int VEC = G::VEC, R = G::R, NS = G::NS, C = G::C;
     __shared__ float sP[NS][C], sS[NS][C], sC[NS][C], sIn[C];
+    __shared__ int64_t sTicket;
 
-    int64_t m, b, ct;
-    take_tile(p, m, b, ct);
-    const int64_t n = p.n_tiles - 1 - m;
+    if (threadIdx.x == 0) sTicket = next_ticket(p);
+    __syncthreads();
+    Place<G> at;
+    at.set(p, uniform(sTicket), true);
+    const int64_t n = p.n_tiles - 1 - at.m;  // the tile, counted in time
     const int lane = threadIdx.x % G::LANES, slice = threadIdx.x / G::LANES;
-    const int64_t t0 = n * G::T + slice * R;
-    const int64_t d0 = ct * C + lane * VEC;
-    const bool d_in = d0 < p.D;
-    const size_t row0 = (size_t)b * p.L;
-    const size_t dd = d_in ? d0 : 0;
-    auto row_at = [&](int r) { return row0 + (t0 + r < p.L ? t0 + r : p.L - 1); };
 
-    typename Ln::raw g[R], k[R], v[R], q[R], dy[R];
+    typename Ln::raw g[R] = {}, k[R] = {}, v[R] = {}, q[R] = {}, dy[R] = {};
+    float a[R][VEC];
+    {
+        if (at.n_ch == VEC) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const size_t e = row_at(r) * p.ld + dd;
-        g[r] = Ln::load(p.g, e);
-        k[r] = Ln::load(p.k, e);
-        v[r] = Ln::load(p.v, e);
-        q[r] = Ln::load(p.q, e);
-        dy[r] = Ln::load(p.dy, row_at(r) * p.D + dd);
+            for (int r = 0; r < R; ++r) {
+                const size_t row = at.row(p, r), e = row * p.ld + at.d0;
+                g[r] = Ln::load(p.g, e);
+                k[r] = Ln::load(p.k, e);
+                v[r] = Ln::load(p.v, e);
+                q[r] = Ln::load(p.q, e);
+                dy[r] = Ln::load(p.dy, row * p.D + at.d0);
+            }
+        } else if (at.n_ch > 0) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const size_t row = at.row(p, r), e = row * p.ld + at.d0;
+                g[r] = Ln::load_part(p.g, e, at.n_ch);
+                k[r] = Ln::load_part(p.k, e, at.n_ch);
+                v[r] = Ln::load_part(p.v, e, at.n_ch);
+                q[r] = Ln::load_part(p.q, e, at.n_ch);
+                dy[r] = Ln::load_part(p.dy, row * p.D + at.d0, at.n_ch);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) a[r][i] = decay<LOG>(Ln::get(g[r], i));
+        if (at.t0 + R > p.L) {  // rows past the end pass the gradient on
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                if (at.t0 + r < p.L) continue;
+                k[r] = q[r] = typename Ln::raw{};
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) a[r][i] = 1.0f;
+            }
+        }
     }
+    float least_of_all = 1.0f;
+    auto compose = [&](auto sel, int i, float &S, float &c) {
+        constexpr bool RESETS = decltype(sel)::value;
+        S = c = 0.0f;
+#pragma unroll
+        for (int r = 0; r < R; ++r) S = walk<RESETS>(a[r][i], Ln::get(k[r], i) * Ln::get(v[r], i), S);
+#pragma unroll
+        for (int r = R - 1; r >= 0; --r)
+            c = walk<RESETS>(a[r][i], 0.0f, fmaf(Ln::get(q[r], i), Ln::get(dy[r], i), c));
+    };
+    float least[VEC];
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
-        float P = 1.0f, S = 0.0f, least = 1.0f, a[R];
+        least[i] = a[0][i];
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const bool in = t0 + r < p.L;
-            a[r] = in ? decay<LOG>(Ln::get(g[r], i)) : 1.0f;
-            P *= a[r];
-            least = fminf(least, a[r]);
-            S = apply(a[r], in ? Ln::get(k[r], i) * Ln::get(v[r], i) : 0.0f, S);
-        }
-        float c = 0.0f;
+        for (int r = 1; r < R; ++r) least[i] = fminf(least[i], a[r][i]);
+        least_of_all = fminf(least_of_all, least[i]);
+    }
+    const bool resets = any_lane(least_of_all == 0.0f);
 #pragma unroll
-        for (int r = R - 1; r >= 0; --r) {
-            const float u = t0 + r < p.L ? Ln::get(q[r], i) * Ln::get(dy[r], i) : 0.0f;
-            c = apply(a[r], 0.0f, u + c);
-        }
-        sP[slice][lane * VEC + i] = keep_off_zero(P, least);
+    for (int i = 0; i < VEC; ++i) {
+        float P = a[0][i], S, c;
+#pragma unroll
+        for (int r = 1; r < R; ++r) P *= a[r][i];
+        if (resets) compose(std::true_type(), i, S, c);
+        else compose(std::false_type(), i, S, c);
+        sP[slice][lane * VEC + i] = keep_off_zero(P, least[i]);
         sS[slice][lane * VEC + i] = S;
         sC[slice][lane * VEC + i] = c;
     }
-    __syncthreads();
+    lds_barrier();
 
     if (threadIdx.x < C) {
         const int c = threadIdx.x;
-        const int64_t d = ct * C + c;
-        // the state that enters each slice
-        float s = 0.0f;
-        if (d < p.D) s = p.states_in[(b * ceil_div(p.L, kStateRows) + n * (G::T / kStateRows)) * p.D + d];
-#pragma unroll
-        for (int j = 0; j < NS; ++j) {
-            const float pj = sP[j][c], sj = sS[j][c];
-            sS[j][c] = s;
-            s = apply(pj, sj, s);
-        }
+        const int64_t d = at.ct * C + c;
         // the maps from the tile's end back to the end of each slice
-        float P = 1.0f, S = 0.0f;
+        float P = 1.0f, S = 0.0f, pj[NS];
 #pragma unroll
         for (int j = NS - 1; j >= 0; --j) {
-            const float pj = sP[j][c], cj = sC[j][c];
+            pj[j] = sP[j][c];
+            const float cj = sC[j][c];
             sP[j][c] = P, sC[j][c] = S;
-            P = join(P, pj), S = apply(pj, cj, S);
+            P = join(P, pj[j]), S = apply(pj[j], cj, S);
         }
-        const float first = p.ds_last && d < p.D ? p.ds_last[b * p.D + d] : 0.0f;
-        float in = first;
-        if (p.counter) {
-            const int64_t pitch = p.c_tiles * C, stride = p.B * pitch;
-            uint64_t *words = p.words + b * pitch + ct * C + c;
-            if (m > 0) {
-                if (m + 1 < p.n_tiles) put_word(words + m * stride, __float_as_uint(P), S);
-                in = carry_in(words, stride, m, first);
-            }
-            if (m + 1 < p.n_tiles) put_word(words + m * stride, kState, apply(P, S, in));
+        const int64_t pitch = p.c_tiles * C, stride = p.B * pitch;
+        uint64_t *words = p.words + at.b * pitch + at.ct * C + c;
+        if (p.counters && at.m > 0 && at.m + 1 < p.n_tiles) put_word(words + at.m * stride, __float_as_uint(P), S);
+        // the state that enters each slice
+        float s = 0.0f;
+        if (d < p.D) s = p.states_in[(at.b * ceil_div(p.L, kStateRows) + n * (G::T / kStateRows)) * p.D + d];
+#pragma unroll
+        for (int j = 0; j < NS; ++j) {
+            const float sj = sS[j][c];
+            sS[j][c] = s;
+            s = apply(pj[j], sj, s);
+        }
+        float in = p.ds_last && d < p.D ? p.ds_last[at.b * p.D + d] : 0.0f;
+        if (p.counters) {
+            if (at.m > 0) in = carry_in(words, stride, at.m, in);
+            if (at.m + 1 < p.n_tiles) put_word(words + at.m * stride, kState, apply(P, S, in));
         }
         sIn[c] = in;
-        if (p.ds0 && m + 1 == p.n_tiles && d < p.D) p.ds0[b * p.D + d] = apply(P, S, in);
+        if (p.ds0 && at.m + 1 == p.n_tiles && d < p.D) p.ds0[at.b * p.D + d] = apply(P, S, in);
     }
-    __syncthreads();
-    if (!d_in) return;
+    lds_barrier();
+    if (at.n_ch <= 0) return;
 
-    float s[R + 1][VEC], c[VEC];  // s[r]: before row r
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-        const int ch = lane * VEC + i;
-        s[0][i] = sS[slice][ch];
-        c[i] = apply(sP[slice][ch], sC[slice][ch], sIn[ch]);
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-            s[r + 1][i] = apply(decay<LOG>(Ln::get(g[r], i)), Ln::get(k[r], i) * Ln::get(v[r], i), s[r][i]);
-    }
-#pragma unroll
-    for (int r = R - 1; r >= 0; --r) {
-        if (t0 + r >= p.L) continue;
-        float dq[VEC], dk[VEC], dv[VEC], dg[VEC];
+    auto outputs = [&](auto sel) {
+        constexpr bool RESETS = decltype(sel)::value;
+        float s[R + 1][VEC], c[VEC];  // s[r]: before row r
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-            float slope;
-            const float a = decay<LOG>(Ln::get(g[r], i), slope), dyi = Ln::get(dy[r], i);
-            const float ds = fmaf(Ln::get(q[r], i), dyi, c[i]);
-            dq[i] = dyi * s[r + 1][i];
-            dk[i] = ds * Ln::get(v[r], i);
-            dv[i] = ds * Ln::get(k[r], i);
-            dg[i] = a == 0.0f ? 0.0f : ds * s[r][i] * slope;
-            c[i] = a == 0.0f ? 0.0f : a * ds;
+            const int ch = lane * VEC + i;
+            s[0][i] = sS[slice][ch];
+            c[i] = apply(sP[slice][ch], sC[slice][ch], sIn[ch]);
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                s[r + 1][i] = walk<RESETS>(a[r][i], Ln::get(k[r], i) * Ln::get(v[r], i), s[r][i]);
         }
-        const size_t o = (row0 + t0 + r) * p.ldd + d0;
-        if (p.dq) Ln::store(p.dq, o, dq);
-        if (p.dk) Ln::store(p.dk, o, dk);
-        if (p.dv) Ln::store(p.dv, o, dv);
-        if (p.dg) Ln::store(p.dg, o, dg);
-    }
+        const size_t first = ((size_t)at.b * p.L + at.t0) * p.ldd + at.d0;
+#pragma unroll
+        for (int r = R - 1; r >= 0; --r) {
+            float dq[VEC], dk[VEC], dv[VEC], dg[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                const float dyi = Ln::get(dy[r], i);
+                const float ds = fmaf(Ln::get(q[r], i), dyi, c[i]);
+                dq[i] = dyi * s[r + 1][i];
+                dk[i] = ds * Ln::get(v[r], i);
+                dv[i] = ds * Ln::get(k[r], i);
+                dg[i] = ds * s[r][i] * decay_slope<LOG>(Ln::get(g[r], i), a[r][i]);
+                c[i] = a[r][i] * ds;
+                if (RESETS && a[r][i] == 0.0f) dg[i] = c[i] = 0.0f;
+            }
+            if (at.t0 + r >= p.L) continue;
+            const size_t o = first + (size_t)r * p.ldd;
+            if (at.n_ch == VEC) {
+                if (p.dq) Ln::store(p.dq, o, dq);
+                if (p.dk) Ln::store(p.dk, o, dk);
+                if (p.dv) Ln::store(p.dv, o, dv);
+                if (p.dg) Ln::store(p.dg, o, dg);
+            } else {
+                if (p.dq) store_part<F32>(p.dq, o, dq, at.n_ch);
+                if (p.dk) store_part<F32>(p.dk, o, dk, at.n_ch);
+                if (p.dv) store_part<F32>(p.dv, o, dv, at.n_ch);
+                if (p.dg) store_part<F32>(p.dg, o, dg, at.n_ch);
+            }
+        }
+    };
+    if (resets) outputs(std::true_type());
+    else outputs(std::false_type());
 }
 
 int check_sizes(int64_t B, int64_t L, int64_t D, int gate, int dtype) {
@@ -422,28 +558,31 @@ int check_sizes(int64_t B, int64_t L, int64_t D, int gate, int dtype) {
 
 // Rows and channels of the smallest tile of any variant bound the words.
 constexpr int64_t kLeastRows = 64, kMostChannels = 128;
+constexpr int64_t kHeader = kMostCounters * kCounterGap * 4;
 
 int64_t workspace_bytes(int64_t B, int64_t L, int64_t D) {
     if (L <= kLeastRows || B == 0 || D == 0) return 0;
-    return 16 + 8 * ceil_div(L, kLeastRows) * B * (ceil_div(D, kMostChannels) * kMostChannels);
+    return kHeader + 8 * ceil_div(L, kLeastRows) * B * (ceil_div(D, kMostChannels) * kMostChannels);
 }
 
 template <typename G, typename K> int launch(K kernel, ScanParams p, void *workspace, void *stream) {
     static_assert(G::T >= kLeastRows && kMostChannels % G::C == 0, "the workspace holds every variant's words");
     p.n_tiles = ceil_div(p.L, G::T);
     p.c_tiles = ceil_div(p.D, G::C);
+    p.n_chains = p.B * p.c_tiles;
     int64_t blocks;
-    if (!mul_fits(p.n_tiles, p.B, p.c_tiles, &blocks) || blocks > 0x7fffffff) return HYENA_ERR_UNSUPPORTED;
+    if (!mul_fits(p.n_tiles, p.n_chains, 1, &blocks) || blocks > 0x7fffffff) return HYENA_ERR_UNSUPPORTED;
     hipStream_t s = (hipStream_t)stream;
     if (p.n_tiles > 1) {
-        p.counter = (uint32_t *)workspace;
-        p.words = (uint64_t *)((char *)workspace + 16);
-        const int64_t words = p.n_tiles * p.B * p.c_tiles * G::C;
+        p.counters = (uint32_t *)workspace;
+        p.words = (uint64_t *)((char *)workspace + kHeader);
+        for (p.n_counters = 1; p.n_counters < kMostCounters && p.n_chains % (2 * p.n_counters) == 0;) p.n_counters *= 2;
+        const int64_t words = p.n_tiles * p.n_chains * G::C;
         const int64_t grid = ceil_div(words, 1024);
-        hipLaunchKernelGGL(scan_init_kernel, dim3((unsigned)(grid < 2048 ? grid : 2048)), dim3(256), 0, s, p.counter,
+        hipLaunchKernelGGL(scan_init_kernel, dim3((unsigned)(grid < 2048 ? grid : 2048)), dim3(256), 0, s, p.counters,
                            p.words, words);
     }
-    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(kThreads), 0, s, p);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(G::NT), 0, s, p);
     return launch_status();
 }
 
@@ -454,19 +593,11 @@ int launch_none(const float *from, float *to, int64_t n, void *stream) {
     return launch_status();
 }
 
-template <bool F32, bool LOG, bool WIDE> int launch_fwd(const ScanParams &p, void *ws, void *stream) {
-    return launch<FwdTile<F32, WIDE>>(scan_fwd_kernel<F32, LOG, WIDE>, p, ws, stream);
+template <bool F32, bool LOG> int launch_fwd(const ScanParams &p, void *ws, void *stream) {
+    return launch<FwdTile<F32>>(scan_fwd_kernel<F32, LOG>, p, ws, stream);
 }
-template <bool F32, bool LOG, bool WIDE> int launch_bwd(const ScanParams &p, void *ws, void *stream) {
-    return launch<BwdTile<F32, WIDE>>(scan_bwd_kernel<F32, LOG, WIDE>, p, ws, stream);
-}
-
-// 16-byte accesses of all of these arrays (null ones do not matter).
-bool wide_ok(int64_t D, int64_t ld, int64_t ldd, int64_t eb, std::initializer_list<const void *> ps) {
-    if ((D * eb) % 16 || (ld * eb) % 16 || (ldd * eb) % 16) return false;
-    for (const void *p : ps)
-        if (!aligned(p, 16)) return false;
-    return true;
+template <bool F32, bool LOG> int launch_bwd(const ScanParams &p, void *ws, void *stream) {
+    return launch<BwdTile<F32>>(scan_bwd_kernel<F32, LOG>, p, ws, stream);
 }
 
 }  // namespace
@@ -518,11 +649,8 @@ int hyena_scan_fwd(const void *q, const void *k, const void *v, const void *g, i
     p.B = B, p.L = L, p.D = D, p.ld = ld;
     const bool f32 = dtype == HYENA_DTYPE_F32, lg = gate == HYENA_GATE_LOG;
     if (L == 0) return launch_none(s0, s_last, B * D, stream);
-    if (wide_ok(D, ld, D, eb, {q, k, v, g, y}))
-        return f32 ? (lg ? launch_fwd<true, true, true>(p, workspace, stream) : launch_fwd<true, false, true>(p, workspace, stream))
-                   : (lg ? launch_fwd<false, true, true>(p, workspace, stream) : launch_fwd<false, false, true>(p, workspace, stream));
-    return f32 ? (lg ? launch_fwd<true, true, false>(p, workspace, stream) : launch_fwd<true, false, false>(p, workspace, stream))
-               : (lg ? launch_fwd<false, true, false>(p, workspace, stream) : launch_fwd<false, false, false>(p, workspace, stream));
+    if (f32) return lg ? launch_fwd<true, true>(p, workspace, stream) : launch_fwd<true, false>(p, workspace, stream);
+    return lg ? launch_fwd<false, true>(p, workspace, stream) : launch_fwd<false, false>(p, workspace, stream);
 }
 
 int hyena_scan_bwd(const void *q, const void *k, const void *v, const void *g, const void *dy, const float *states,
@@ -562,11 +690,8 @@ int hyena_scan_bwd(const void *q, const void *k, const void *v, const void *g, c
     p.B = B, p.L = L, p.D = D, p.ld = ld, p.ldd = ldd;
     const bool f32 = dtype == HYENA_DTYPE_F32, lg = gate == HYENA_GATE_LOG;
     if (L == 0) return launch_none(ds_last, ds0, B * D, stream);
-    if (wide_ok(D, ld, ldd, eb, {q, k, v, g, dy, dq, dk, dv, dg}))
-        return f32 ? (lg ? launch_bwd<true, true, true>(p, workspace, stream) : launch_bwd<true, false, true>(p, workspace, stream))
-                   : (lg ? launch_bwd<false, true, true>(p, workspace, stream) : launch_bwd<false, false, true>(p, workspace, stream));
-    return f32 ? (lg ? launch_bwd<true, true, false>(p, workspace, stream) : launch_bwd<true, false, false>(p, workspace, stream))
-               : (lg ? launch_bwd<false, true, false>(p, workspace, stream) : launch_bwd<false, false, false>(p, workspace, stream));
+    if (f32) return lg ? launch_bwd<true, true>(p, workspace, stream) : launch_bwd<true, false>(p, workspace, stream);
+    return lg ? launch_bwd<false, true>(p, workspace, stream) : launch_bwd<false, false>(p, workspace, stream);
 }
 
 }  // extern "C"

@@ -40,28 +40,17 @@ template <bool F32> __device__ inline void store1(void *p, size_t i, float x) {
     else ((bf16_t *)p)[i] = (bf16_t)x;
 }
 
-// The decay a of a gate and, where wanted, da/dg.  With e = exp(-|g|) and
-// r = 1 / (1 + e): sigmoid(g) is r or e r and its slope e r^2 for either sign,
-// which keeps 1 - a exact to rounding where a is near 1.  g = -inf gives
-// a = 0, g = +inf a = 1, both with slope 0.
+// The decay a of a gate, and da/dg.  With e = exp(-g), sigmoid(g) = 1 / (1 + e)
+// and its slope is e a^2, which keeps 1 - a exact to rounding where a is near
+// 1.  a is 0 for g = -inf and for a finite g whose e overflows (g < -88); the
+// slope of those is not a number and not used.
 template <bool LOG> __device__ inline float decay(float g) {
-    if constexpr (LOG) {
-        return __expf(g);
-    } else {
-        const float e = __expf(-fabsf(g));
-        const float r = __builtin_amdgcn_rcpf(1.0f + e);
-        return g < 0.0f ? e * r : r;
-    }
+    if constexpr (LOG) return __expf(g);
+    else return __builtin_amdgcn_rcpf(1.0f + __expf(-g));
 }
-template <bool LOG> __device__ inline float decay(float g, float &slope) {
-    if constexpr (LOG) {
-        return slope = __expf(g);
-    } else {
-        const float e = __expf(-fabsf(g));
-        const float r = __builtin_amdgcn_rcpf(1.0f + e);
-        slope = e * r * r;
-        return g < 0.0f ? e * r : r;
-    }
+template <bool LOG> __device__ inline float decay_slope(float g, float a) {
+    if constexpr (LOG) return a;
+    else return __expf(-g) * a * a;
 }
 
 // ---- host -------------------------------------------------------------------
