@@ -19,9 +19,12 @@
 //     fragments are 4 values of c, each its own v_mfma_f32_16x16x4_f32; the
 //     order of c inside a step differs from memory's, alike for both operands.
 //   * The products are formed as B A^T, so a lane ends up with 4 consecutive n
-//     of one m, which the epilogue turns into one 8- or 16-byte access.
-// Sizes, pointers or strides that do not allow 16-byte fetches take the same
-// kernel with a loader that fetches single elements.
+//     of one m, and the epilogue's way through LDS is in 16-byte accesses.
+// Operands whose 16-byte chunks are not aligned (odd sizes, strides or
+// pointers) cannot be fetched straight into LDS: the same kernels take them
+// through registers, a step ahead, with unaligned 16-byte loads.
+
+#include <initializer_list>
 
 #include "layer_common.h"
 
@@ -77,57 +80,101 @@ template <int ACT> __device__ inline float act_slope(float z) {
     default: F(HYENA_ACT_NONE); break;                      \
     }
 
-// ---- epilogue -----------------------------------------------------------------
+// ---- V values of a row ------------------------------------------------------------
+
+template <bool F32> struct El;
+template <> struct El<false> {
+    static constexpr int CE = 8;   // values per 16-byte chunk
+    typedef bf16x8_t frag;
+    typedef bf16_t type;
+    typedef u32x4_t chunk_any __attribute__((aligned(2)));  // at any element's address
+};
+template <> struct El<true> {
+    static constexpr int CE = 4;
+    typedef f32x4_t frag;
+    typedef float type;
+    typedef u32x4_t chunk_any __attribute__((aligned(4)));
+};
+
+// V = 4 or 8 values as they lie in memory, read or written in as few accesses
+// as possible at any element's address; n of them where that is fewer.
+template <bool F32, int V> struct Pack {
+    static constexpr int WORDS = F32 ? V : V / 2;
+    typedef uint32_t words __attribute__((ext_vector_type(WORDS > 4 ? 4 : WORDS)));
+    typedef words words_any __attribute__((aligned(F32 ? 4 : 2)));
+    static constexpr int PARTS = WORDS > 4 ? 2 : 1;
+    words w[PARTS];
+
+    __device__ static Pack zero() { return Pack{}; }
+    __device__ uint32_t word(int i) const { return w[i / 4][i % 4]; }
+    __device__ float get(int i) const {
+        if constexpr (F32) return __uint_as_float(word(i));
+        else return i & 1 ? bf_hi(word(i >> 1)) : bf_lo(word(i >> 1));
+    }
+    __device__ static Pack of(const float (&x)[V]) {
+        Pack r;
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) r.w[i / 4][i % 4] = F32 ? __float_as_uint(x[i]) : pack_bf16(x[2 * i % V], x[(2 * i + 1) % V]);
+        return r;
+    }
+    __device__ static Pack load(const void *p, size_t e, int n) {
+        using T = typename El<F32>::type;
+        Pack r;
+        if (n >= V) {
+#pragma unroll
+            for (int i = 0; i < PARTS; ++i) r.w[i] = *(const words_any *)((const T *)p + e + i * 4);
+            return r;
+        }
+        float x[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = i < n ? load1<F32>(p, e + i) : 0.0f;
+        return of(x);
+    }
+    __device__ static void store(void *p, size_t e, int n, const float (&x)[V]) {
+        using T = typename El<F32>::type;
+        if (n >= V) {
+            const Pack r = of(x);
+#pragma unroll
+            for (int i = 0; i < PARTS; ++i) *(words_any *)((T *)p + e + i * 4) = r.w[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (i < n) store1<F32>(p, e + i, x[i]);
+        }
+    }
+};
 
 struct Epilogue {
     const void *bias, *residual;
     void *y, *preact;
     int64_t ldr, ldy;
-    int N;
+    int M, N;
     int act;
-    bool vec;  // four values at a time: N, strides and pointers allow it
 };
 
-template <bool F32> __device__ inline void load4(const void *p, size_t e, float (&x)[4]) {
-    if constexpr (F32) {
-        const f32x4_t r = *(const f32x4_t *)((const float *)p + e);
-        x[0] = r[0], x[1] = r[1], x[2] = r[2], x[3] = r[3];
-    } else {
-        const u32x2_t r = *(const u32x2_t *)((const bf16_t *)p + e);
-        x[0] = bf_lo(r[0]), x[1] = bf_hi(r[0]), x[2] = bf_lo(r[1]), x[3] = bf_hi(r[1]);
-    }
+// The epilogue of columns n .. n + V - 1 of row m, z without its bias.
+template <bool F32, int V>
+__device__ __forceinline__ void finish(const Epilogue &p, int64_t m, int n, float (&z)[V], const Pack<F32, V> &bias,
+                                       const Pack<F32, V> &residual) {
+    using Q = Pack<F32, V>;
+    const int left = p.N - n;
+    if (m >= p.M || left <= 0) return;
+#pragma unroll
+    for (int e = 0; e < V; ++e) z[e] += bias.get(e);
+    if (p.preact) Q::store(p.preact, m * p.N + n, left, z);
+#define ACTIVATE(ACT) \
+    _Pragma("unroll") for (int e = 0; e < V; ++e) z[e] = act_value<ACT>(z[e]);
+    if (p.act != HYENA_ACT_NONE) FOR_ACT(p.act, ACTIVATE)
+#undef ACTIVATE
+#pragma unroll
+    for (int e = 0; e < V; ++e) z[e] += residual.get(e);
+    Q::store(p.y, m * p.ldy + n, left, z);
 }
-template <bool F32> __device__ inline void store4(void *p, size_t e, const float (&x)[4]) {
-    if constexpr (F32) *(f32x4_t *)((float *)p + e) = f32x4_t{x[0], x[1], x[2], x[3]};
-    else *(u32x2_t *)((bf16_t *)p + e) = u32x2_t{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
+template <bool F32, int V> __device__ __forceinline__ Pack<F32, V> bias_of(const Epilogue &p, int n) {
+    return p.bias ? Pack<F32, V>::load(p.bias, n, p.N - n) : Pack<F32, V>::zero();
 }
-
-// z of row m, columns n .. n+3 (those below N), n a multiple of 4.
-template <bool F32, int ACT> __device__ inline void finish4(const Epilogue &p, int64_t m, int n, const float (&acc)[4]) {
-    if (n >= p.N) return;
-    float z[4], r[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (p.vec) {
-        float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (p.bias) load4<F32>(p.bias, n, b);
-        if (p.residual) load4<F32>(p.residual, m * p.ldr + n, r);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) z[i] = acc[i] + b[i];
-        if (p.preact) store4<F32>(p.preact, m * p.N + n, z);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) z[i] = act_value<ACT>(z[i]) + r[i];
-        store4<F32>(p.y, m * p.ldy + n, z);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (n + i >= p.N) break;
-            float v = acc[i];
-            if (p.bias) v += load1<F32>(p.bias, n + i);
-            if (p.preact) store1<F32>(p.preact, m * p.N + n + i, v);
-            v = act_value<ACT>(v);
-            if (p.residual) v += load1<F32>(p.residual, m * p.ldr + n + i);
-            store1<F32>(p.y, m * p.ldy + n + i, v);
-        }
-    }
+template <bool F32, int V> __device__ __forceinline__ Pack<F32, V> residual_of(const Epilogue &p, int64_t m, int n) {
+    return p.residual && m < p.M ? Pack<F32, V>::load(p.residual, m * p.ldr + n, p.N - n) : Pack<F32, V>::zero();
 }
 
 // ---- tiled product ---------------------------------------------------------------
@@ -140,18 +187,6 @@ struct GemmParams {
     int splits, c_per_split;  // c is cut into splits (a multiple of the step each, but the last)
     float *partial;           // splits > 1: [splits][M][N] sums for split_kernel; else null
     Epilogue e;
-};
-
-template <bool F32> struct El;
-template <> struct El<false> {
-    static constexpr int CE = 8;   // values per 16-byte chunk
-    typedef bf16x8_t frag;
-    typedef bf16_t type;
-};
-template <> struct El<true> {
-    static constexpr int CE = 4;
-    typedef f32x4_t frag;
-    typedef float type;
 };
 
 // One operand's LDS tile of X values of m (or n) by one step of c.
@@ -181,80 +216,116 @@ template <bool F32, bool TALL, int X, int NT> struct Operand {
         else chunk = c ^ (row >> 1 & 7);
     }
 
-    // Direct loads.  off[i]: the lane's byte offset in the tile, or past every
-    // range where its m is outside the matrix.
+    // Direct loads.  A lane's chunks are STEP rows of memory apart, and the XOR
+    // repeats every 16 rows; off holds the byte offsets of the chunks before
+    // that.  Values of m outside the matrix read zero: a flat tile's rows by the
+    // descriptor's range, a tall tile's columns by an offset past every range.
     static constexpr uint32_t kOutside = 0x80000000u;
-    __device__ static void plan(uint32_t (&off)[LOADS], int64_t ld, int x_left) {
+    static constexpr int STEP = NT / ROW_CHUNKS;
+    static constexpr int PHASES = STEP >= 16 ? 1 : 16 / STEP;
+    static_assert(NT % ROW_CHUNKS == 0 && (STEP % 16 == 0 || 16 % STEP == 0) && LOADS % PHASES == 0, "phases of the XOR");
+    struct Lane {
+        uint32_t off[PHASES], step, range;
+    };
+    __device__ static Lane plan(int64_t ld, int x_left) {
+        const uint32_t pitch = (uint32_t)ld * sizeof(typename El<F32>::type);  // below 2^23 (the host checks)
+        Lane l;
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i) {
+        for (int h = 0; h < PHASES; ++h) {
             int row, chunk;
-            source(i * NT + threadIdx.x, row, chunk);
-            const int x = TALL ? chunk * CE : row;
-            off[i] = x < x_left ? (uint32_t)(row * ld + chunk * CE) * sizeof(typename El<F32>::type) : kOutside;
+            source(h * NT + threadIdx.x, row, chunk);
+            l.off[h] = !TALL || chunk * CE < x_left ? row * pitch + chunk * 16 : kOutside;
         }
+        l.step = STEP * pitch;
+        l.range = TALL ? 0x7fffffffu : (uint32_t)min(x_left, X) * pitch;
+        return l;
     }
-    __device__ static void fetch(const typename El<F32>::type *tile, const uint32_t (&off)[LOADS], int c_left,
+    __device__ static void fetch(const typename El<F32>::type *tile, const Lane &l, int c_left,
                                  LDS_PTR unsigned char *lds) {
-        // offsets stay below 2^31 (the host checks), so only kOutside is out of range
         const __amdgpu_buffer_rsrc_t rs =
-            __builtin_amdgcn_make_buffer_rsrc((void *)tile, (short)0, 0x7fffffff, 0x00020000);
+            __builtin_amdgcn_make_buffer_rsrc((void *)tile, (short)0, (int)l.range, 0x00020000);
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        if (c_left >= BK) {
+        uint32_t at[LOADS];
 #pragma unroll
-            for (int i = 0; i < LOADS; ++i)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LDS_PTR void *)(lds + (i * NT + wave * 64) * 16), 16,
-                                                         off[i], 0, 0, 0);
-        } else {  // the last step: zeros past the end of c
+        for (int i = 0; i < LOADS; ++i) at[i] = l.off[i % PHASES] + (i - i % PHASES) * l.step;
+        if (c_left < BK) {  // the last step: zeros past the end of c
 #pragma unroll
             for (int i = 0; i < LOADS; ++i) {
                 int row, chunk;
                 source(i * NT + threadIdx.x, row, chunk);
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LDS_PTR void *)(lds + (i * NT + wave * 64) * 16), 16,
-                                                         (TALL ? row : chunk * CE) < c_left ? off[i] : kOutside, 0, 0, 0);
+                if ((TALL ? row : chunk * CE) >= c_left) at[i] = kOutside;
             }
         }
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LDS_PTR void *)(lds + (i * NT + wave * 64) * 16), 16, at[i], 0,
+                                                     0, 0);
     }
-    // Single elements, through registers.
-    __device__ static void fetch_narrow(const typename El<F32>::type *tile, int64_t ld, int x_left, int c_left,
-                                        LDS_PTR unsigned char *lds) {
+    // The same chunks into registers, at any alignment ...
+    __device__ static void pull(const typename El<F32>::type *tile, int64_t ld, int x_left, int c_left,
+                                u32x4_t (&r)[LOADS]) {
+        bool part = false;
+#pragma unroll
         for (int i = 0; i < LOADS; ++i) {
             int row, chunk;
             source(i * NT + threadIdx.x, row, chunk);
-            union {
-                typename El<F32>::type v[CE];
-                u32x4_t r;
-            } u;
-            u.r = u32x4_t{0, 0, 0, 0};
-#pragma unroll
-            for (int e = 0; e < CE; ++e) {
-                const int x = TALL ? chunk * CE + e : row, c = TALL ? row : chunk * CE + e;
-                if (x < x_left && c < c_left) u.v[e] = tile[row * ld + chunk * CE + e];
+            const int along = (TALL ? x_left : c_left) - chunk * CE;  // values left along memory's row
+            r[i] = u32x4_t{0, 0, 0, 0};
+            if (row < (TALL ? c_left : x_left)) {
+                if (along >= CE) r[i] = *(const typename El<F32>::chunk_any *)(tile + row * ld + chunk * CE);
+                else part |= along > 0;
             }
-            *(LDS_PTR u32x4_t *)(lds + (i * NT + threadIdx.x) * 16) = u.r;
+        }
+        if (!any_lane(part)) return;
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {  // chunks across the edge
+            int row, chunk;
+            source(i * NT + threadIdx.x, row, chunk);
+            const int along = (TALL ? x_left : c_left) - chunk * CE;
+            if (row < (TALL ? c_left : x_left) && along > 0 && along < CE) {
+                typename El<F32>::type v[CE];
+#pragma unroll
+                for (int e = 0; e < CE; ++e)
+                    v[e] = e < along ? tile[row * ld + chunk * CE + e] : (typename El<F32>::type)0.0f;
+                r[i] = __builtin_bit_cast(u32x4_t, v);
+            }
         }
     }
+    // ... and from there into LDS.
+    __device__ static void push(const u32x4_t (&r)[LOADS], LDS_PTR unsigned char *lds) {
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) *(LDS_PTR u32x4_t *)(lds + (i * NT + threadIdx.x) * 16) = r[i];
+    }
 
-    // Fragment of the 16 values x0 .. x0+15 and the half `kk` of the step:
-    // lane (i, j) holds value x0 + i and c = kk BK/2 + CE j + (0 .. CE-1).
-    __device__ static typename El<F32>::frag read(LDS_PTR unsigned char *lds, int x0, int kk, int i, int j) {
+    // Fragment t of the 16-value blocks from x0 on (a multiple of 16 times a
+    // power of two no less than their number) and half kk of the step: lane (i,
+    // j) holds value x0 + 16 t + i and c = kk BK/2 + CE j + (0 .. CE-1).  `at` is
+    // start(x0, i, j); t and kk only enter as constants.
+    __device__ static int start(int x0, int i, int j) {
         if constexpr (!TALL) {
             const int row = x0 + i;
-            return *(LDS_PTR typename El<F32>::frag *)(lds + row * 128 + (((kk * 4 + j) ^ (row >> 1 & 7)) << 4));
+            return row * 128 + ((j ^ (row >> 1 & 7)) << 4);
+        } else if constexpr (F32) {
+            const int row = j * 4;  // turn() is the same for the row's next three and 16 on
+            return row * X * 4 + (((x0 >> 4) ^ turn(row)) << 6) + i * 4;
+        } else {
+            const int row = j * 8 + (i >> 2);  // turn() is the same 4 and 32 rows on
+            return row * X * 2 + (((x0 >> 4) ^ turn(row)) << 5) + (i & 3) * 8;
+        }
+    }
+    __device__ static typename El<F32>::frag read(LDS_PTR unsigned char *lds, int at, int t, int kk) {
+        if constexpr (!TALL) {
+            return *(LDS_PTR typename El<F32>::frag *)(lds + (at ^ kk << 6) + t * 2048);
         } else if constexpr (F32) {
             f32x4_t f;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int row = kk * 16 + j * 4 + e;
-                f[e] = *(LDS_PTR float *)(lds + row * X * 4 + (((x0 >> 4) ^ turn(row)) << 6) + i * 4);
-            }
+            for (int e = 0; e < 4; ++e) f[e] = *(LDS_PTR float *)(lds + (at ^ t << 6) + (kk * 16 + e) * X * 4);
             return f;
         } else {
             // 16 lanes read a block of 4 rows by 16 values and get its columns
-            const int row = kk * 32 + j * 8 + (i >> 2);
-            LDS_PTR unsigned char *at = lds + row * X * 2 + (((x0 >> 4) ^ turn(row)) << 5) + (i & 3) * 8;
-            // turn(row + 4) == turn(row)
-            const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_PTR s16x4_t *)at);
-            const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_PTR s16x4_t *)(at + 4 * X * 2));
+            LDS_PTR unsigned char *from = lds + (at ^ t << 5) + kk * 32 * X * 2;
+            const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_PTR s16x4_t *)from);
+            const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_PTR s16x4_t *)(from + 4 * X * 2));
             return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
         }
     }
@@ -270,14 +341,14 @@ template <bool F32> __device__ inline f32x4_t mma(typename El<F32>::frag b, type
     }
 }
 
-// Tile of this workgroup.  Workgroups go round the 8 XCDs in turn; each XCD
-// gets a run of neighbouring tiles (8 rows of tiles at a time), which share
-// operand panels in its L2.
-__device__ inline void place(const GemmParams &p, int &tm, int &tn, int &split) {
-    const int total = gridDim.x, per = total / 8, rest = total % 8;
-    const int xcd = blockIdx.x % 8, idx = blockIdx.x / 8;
-    const int id = xcd * per + min(xcd, rest) + idx;
+// Tile of workgroup `block` of `total`.  Workgroups go round the 8 XCDs in
+// turn; each XCD gets a run of neighbouring tiles (8 rows of tiles at a time),
+// which share operand panels in its L2.
+__device__ inline void place(const GemmParams &p, int block, int &tm, int &tn, int &split) {
     const int tiles = p.tiles_m * p.tiles_n;
+    const int total = tiles * p.splits, per = total / 8, rest = total % 8;
+    const int xcd = block % 8, idx = block / 8;
+    const int id = xcd * per + min(xcd, rest) + idx;
     split = id / tiles;
     const int t = id % tiles, band = 8 * p.tiles_n;
     const int first = t / band * 8, rows = min(p.tiles_m - first, 8);
@@ -285,132 +356,258 @@ __device__ inline void place(const GemmParams &p, int &tm, int &tn, int &split) 
     tn = t % band / rows;
 }
 
-// WM x WN waves, each MT x NTL tiles of 16 x 16.
-template <bool F32, bool TALL_A, bool TALL_B, bool DIRECT, int WM, int WN, int MT, int NTL>
-__global__ __launch_bounds__(64 * WM *WN, 2) void gemm_kernel(GemmParams p) {
-    constexpr int NT = 64 * WM * WN, BM = WM * MT * 16, BN = WN * NTL * 16;
-    using A = Operand<F32, TALL_A, BM, NT>;
-    using B = Operand<F32, TALL_B, BN, NT>;
-    using T = typename El<F32>::type;
-    constexpr int BK = A::BK;
-    // four variables, so that the compiler sees which one a direct load fills
-    __shared__ __attribute__((aligned(16))) unsigned char a0[A::BYTES], a1[A::BYTES], b0[B::BYTES], b1[B::BYTES];
-
-    int tm, tn, split;
-    place(p, tm, tn, split);
-    const int m0 = tm * BM, n0 = tn * BN;
-    const int c_begin = split * p.c_per_split, c_end = min(p.C, c_begin + p.c_per_split);
-    const T *a = (const T *)p.a + (TALL_A ? (int64_t)c_begin * p.lda + m0 : (int64_t)m0 * p.lda + c_begin);
-    const T *b = (const T *)p.b + (TALL_B ? (int64_t)c_begin * p.ldb + n0 : (int64_t)n0 * p.ldb + c_begin);
-    const int64_t step_a = TALL_A ? BK * p.lda : BK, step_b = TALL_B ? BK * p.ldb : BK;
-
-    uint32_t off_a[A::LOADS], off_b[B::LOADS];
-    if constexpr (DIRECT) {
-        A::plan(off_a, p.lda, p.M - m0);
-        B::plan(off_b, p.ldb, p.N - n0);
-    }
-    auto fetch = [&](unsigned char *la, unsigned char *lb, int c_left) {
-        if constexpr (DIRECT) {
-            A::fetch(a, off_a, c_left, (LDS_PTR unsigned char *)la);
-            B::fetch(b, off_b, c_left, (LDS_PTR unsigned char *)lb);
-        } else {
-            A::fetch_narrow(a, p.lda, p.M - m0, c_left, (LDS_PTR unsigned char *)la);
-            B::fetch_narrow(b, p.ldb, p.N - n0, c_left, (LDS_PTR unsigned char *)lb);
-        }
-        a += step_a;
-        b += step_b;
-    };
-
-    const int wave = threadIdx.x >> 6, i = threadIdx.x & 15, j = (threadIdx.x >> 4) & 3;
-    const int wm = wave / WN * MT * 16, wn = wave % WN * NTL * 16;
-    f32x4_t acc[MT][NTL] = {};
-    auto multiply = [&](unsigned char *la, unsigned char *lb) {
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            typename El<F32>::frag fa[MT], fb[NTL];
-#pragma unroll
-            for (int t = 0; t < NTL; ++t) fb[t] = B::read((LDS_PTR unsigned char *)lb, wn + t * 16, kk, i, j);
-#pragma unroll
-            for (int t = 0; t < MT; ++t) fa[t] = A::read((LDS_PTR unsigned char *)la, wm + t * 16, kk, i, j);
-#pragma unroll
-            for (int t = 0; t < MT; ++t)
-#pragma unroll
-                for (int u = 0; u < NTL; ++u) acc[t][u] = mma<F32>(fb[u], fa[t], acc[t][u]);
-        }
-    };
-
-    // two steps a turn (past the end of c: zeros); a buffer is filled while the
-    // other is multiplied, and the barrier (which waits for the fills) stands
-    // between the two uses
-    int left = c_end - c_begin;
-    fetch(a0, b0, left);
-    for (; left > 0; left -= 2 * BK) {
-        __syncthreads();
-        fetch(a1, b1, left - BK);
-        multiply(a0, b0);
-        __syncthreads();
-        if (left > 2 * BK) fetch(a0, b0, left - 2 * BK);
-        multiply(a1, b1);
-    }
-
-    if (p.partial) {
-        float *out = p.partial + (int64_t)split * p.M * p.N;
-        const bool vec = (p.N & 3) == 0;
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            const int m = m0 + wm + t * 16 + i;
-            if (m >= p.M) continue;
-#pragma unroll
-            for (int u = 0; u < NTL; ++u) {
-                const int n = n0 + wn + u * 16 + j * 4;
-                float *to = out + (int64_t)m * p.N + n;
-                if (vec && n < p.N) {
-                    *(f32x4_t *)to = acc[t][u];
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (n + e < p.N) to[e] = acc[t][u][e];
-                }
-            }
-        }
-        return;
-    }
-#define FINISH(ACT)                                                                     \
-    _Pragma("unroll") for (int t = 0; t < MT; ++t) {                                    \
-        const int m = m0 + wm + t * 16 + i;                                             \
-        if (m >= p.M) continue;                                                         \
-        _Pragma("unroll") for (int u = 0; u < NTL; ++u) {                               \
-            const float z[4] = {acc[t][u][0], acc[t][u][1], acc[t][u][2], acc[t][u][3]}; \
-            finish4<F32, ACT>(p.e, m, n0 + wn + u * 16 + j * 4, z);                     \
-        }                                                                               \
-    }
-    FOR_ACT(p.e.act, FINISH)
-#undef FINISH
+// Waits until at most N of this wave's direct loads are on their way and for
+// its LDS reads, then for the other waves.
+template <int N> __device__ __forceinline__ void step_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((N & 15) | 7 << 4 | N >> 4 << 14);  // vmcnt(N) lgkmcnt(0), a form the compiler counts with
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
 }
 
-// Sums of the splits, then the epilogue: four columns a thread.
-template <bool F32> __global__ __launch_bounds__(256) void split_kernel(GemmParams p) {
+// A workgroup of WM x WN waves, each MT x NTL tiles of 16 x 16, with ST
+// operand buffers: ST - 1 steps of c are on their way while one is multiplied.
+template <bool F32, int WM, int WN, int MT, int NTL, int ST> struct Shape {
+    static constexpr int NT = 64 * WM * WN, BM = WM * MT * 16, BN = WN * NTL * 16;
+    static constexpr int CE = El<F32>::CE, BK = 8 * CE;
+    static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128, STAGES = ST;
+    static constexpr int WAVES = ST * (A_BYTES + B_BYTES) > 80 * 1024 ? NT / 256 : NT / 128;  // a SIMD, by LDS
+
+    // The workgroup's tile of one product; la and lb are the operands' buffers.
+    template <bool TALL_A, bool TALL_B, bool DIRECT>
+    __device__ __forceinline__ static void run(const GemmParams &p, int block, unsigned char *const (&la)[ST],
+                                               unsigned char *const (&lb)[ST]) {
+        using A = Operand<F32, TALL_A, BM, NT>;
+        using B = Operand<F32, TALL_B, BN, NT>;
+        using T = typename El<F32>::type;
+        typedef LDS_PTR unsigned char *lds;
+        int tm, tn, split;
+        place(p, block, tm, tn, split);
+        const int m0 = tm * BM, n0 = tn * BN;
+        const int c_begin = split * p.c_per_split, c_end = min(p.C, c_begin + p.c_per_split);
+        const T *a = (const T *)p.a + (TALL_A ? (int64_t)c_begin * p.lda + m0 : (int64_t)m0 * p.lda + c_begin);
+        const T *b = (const T *)p.b + (TALL_B ? (int64_t)c_begin * p.ldb + n0 : (int64_t)n0 * p.ldb + c_begin);
+        const int64_t step_a = TALL_A ? BK * p.lda : BK, step_b = TALL_B ? BK * p.ldb : BK;
+
+        const int wave = threadIdx.x >> 6, i = threadIdx.x & 15, j = (threadIdx.x >> 4) & 3;
+        const int wm = wave / WN * MT * 16, wn = wave % WN * NTL * 16;
+        f32x4_t acc[MT][NTL] = {};
+        const int start_a = A::start(wm, i, j), start_b = B::start(wn, i, j);
+        auto multiply = [&](unsigned char *la, unsigned char *lb) {
+            // hidden from the compiler, or it would keep the addresses of all
+            // fragments in registers that the sums need
+            int at_a = start_a, at_b = start_b;
+            asm volatile("" : "+v"(at_a), "+v"(at_b));
+            typename El<F32>::frag fa[2][MT], fb[2][NTL];
+            auto read = [&](int kk) {
+#pragma unroll
+                for (int t = 0; t < NTL; ++t) fb[kk][t] = B::read((lds)lb, at_b, t, kk);
+#pragma unroll
+                for (int t = 0; t < MT; ++t) fa[kk][t] = A::read((lds)la, at_a, t, kk);
+            };
+            auto products = [&](int kk) {
+#pragma unroll
+                for (int t = 0; t < MT; ++t)
+#pragma unroll
+                    for (int u = 0; u < NTL; ++u) acc[t][u] = mma<F32>(fb[kk][u], fa[kk][t], acc[t][u]);
+            };
+            if constexpr (MT * NTL <= 16) {
+                // registers for a whole step's fragments: all reads go out
+                // first, and the second half's overlap the first's products
+                read(0);
+                read(1);
+                __builtin_amdgcn_sched_barrier(0);
+                products(0);
+                products(1);
+            } else {
+                // the halves apart, so that their fragments share registers
+                if (TALL_A) __builtin_amdgcn_sched_barrier(0);
+                read(0);
+                products(0);
+                if (TALL_A) __builtin_amdgcn_sched_barrier(0);
+                read(1);
+                products(1);
+            }
+        };
+
+        // ST steps a turn.  The barrier before a step waits for its fills, and
+        // for every wave to be done with the buffer that is filled next.
+        // Fills past the end of c are zeros, so that their number is the same.
+        int left = c_end - c_begin;
+        if constexpr (DIRECT) {
+            constexpr int LOADS = A::LOADS + B::LOADS;
+            const typename A::Lane lane_a = A::plan(p.lda, p.M - m0);
+            const typename B::Lane lane_b = B::plan(p.ldb, p.N - n0);
+            auto fetch = [&](int s, int c_left) {
+                A::fetch(a, lane_a, c_left, (lds)la[s]);
+                B::fetch(b, lane_b, c_left, (lds)lb[s]);
+                a += step_a;
+                b += step_b;
+            };
+#pragma unroll
+            for (int s = 0; s < ST - 1; ++s) fetch(s, left - s * BK);
+            for (; left > 0; left -= ST * BK) {
+#pragma unroll
+                for (int s = 0; s < ST; ++s) {
+                    step_barrier<(ST - 2) * LOADS>();
+                    fetch((s + ST - 1) % ST, left - (s + ST - 1) * BK);
+                    if (ST == 2 || left > s * BK) multiply(la[s], lb[s]);
+                }
+            }
+        } else {
+            static_assert(DIRECT || ST == 2, "through registers: one step ahead");
+            u32x4_t ra[A::LOADS], rb[B::LOADS];
+            auto pull = [&](int c_left) {
+                A::pull(a, p.lda, p.M - m0, c_left, ra);
+                B::pull(b, p.ldb, p.N - n0, c_left, rb);
+                a += step_a;
+                b += step_b;
+            };
+            pull(left);
+            A::push(ra, (lds)la[0]), B::push(rb, (lds)lb[0]);
+            for (; left > 0; left -= 2 * BK) {
+                __syncthreads();
+                pull(left - BK);
+                multiply(la[0], lb[0]);
+                A::push(ra, (lds)la[1]), B::push(rb, (lds)lb[1]);
+                __syncthreads();
+                if (left > 2 * BK) pull(left - 2 * BK);
+                multiply(la[1], lb[1]);
+                A::push(ra, (lds)la[0]), B::push(rb, (lds)lb[0]);
+            }
+        }
+
+        // The sums go through LDS, 64 rows by 64 columns a wave at a time in
+        // its own 16 KB, so that 8 lanes write a row's 64 columns: 16 bytes a
+        // lane in bf16, whole 128-byte lines.  Rows are 256 bytes, their
+        // 16-byte chunks XOR-ed with the row: no bank conflicts either way.
+        static_assert(NTL == 4 && MT % 4 == 0 && A_BYTES == B_BYTES, "64 x 64 pieces of a wave");
+        constexpr int PER = A_BYTES / 16384;  // waves a buffer holds
+        unsigned char *const buf[4] = {la[0], la[1], lb[0], lb[1]};
+        lds piece = (lds)la[0];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (wave / PER == q) piece = (lds)buf[q] + wave % PER * 16384;
+        const int c8 = threadIdx.x & 7, r8 = (threadIdx.x >> 3) & 7;
+        const int n = n0 + wn + c8 * 8;
+        const Epilogue &ep = p.e;
+        float *partial = p.partial ? p.partial + (int64_t)split * p.M * p.N : nullptr;
+        const auto bias = partial ? Pack<F32, 8>::zero() : bias_of<F32, 8>(ep, n);
+        __syncthreads();  // every wave is done with the operands
+#pragma unroll
+        for (int g = 0; g < MT; g += 4) {
+            const int m = m0 + wm + g * 16 + r8;
+            Pack<F32, 8> res[8];
+            if (!partial) {  // all fetched before the first store (y may be the residual)
+#pragma unroll
+                for (int r = 0; r < 8; ++r) res[r] = residual_of<F32, 8>(ep, m + 8 * r, n);
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    *(LDS_PTR f32x4_t *)(piece + (t * 16 + i) * 256 + (((u * 4 + j) ^ i) << 4)) = acc[g + t][u];
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the piece is this wave's own
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                const int row = r * 8 + r8;
+                const f32x4_t lo = *(LDS_PTR f32x4_t *)(piece + row * 256 + (((c8 * 2) ^ (row & 15)) << 4));
+                const f32x4_t hi = *(LDS_PTR f32x4_t *)(piece + row * 256 + (((c8 * 2 + 1) ^ (row & 15)) << 4));
+                float z[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+                if (partial) {
+                    if (m + 8 * r < p.M && n < p.N)
+                        Pack<true, 8>::store(partial, (int64_t)(m + 8 * r) * p.N + n, p.N - n, z);
+                } else {
+                    finish<F32, 8>(ep, m + 8 * r, n, z, bias, res[r]);
+                }
+            }
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        }
+    }
+};
+
+// an LDS variable for each buffer, so that the compiler sees which one a direct
+// load fills and does not wait for it before it reads another
+#define BUFFER(NAME, BYTES) __shared__ __attribute__((aligned(16))) unsigned char NAME[BYTES]
+#define TILE_BUFFERS(S)                                                                                       \
+    BUFFER(a0, S::A_BYTES); BUFFER(a1, S::A_BYTES); BUFFER(b0, S::B_BYTES); BUFFER(b1, S::B_BYTES);           \
+    BUFFER(a2, S::STAGES > 2 ? S::A_BYTES : 16); BUFFER(b2, S::STAGES > 2 ? S::B_BYTES : 16);                 \
+    BUFFER(a3, S::STAGES > 3 ? S::A_BYTES : 16); BUFFER(b3, S::STAGES > 3 ? S::B_BYTES : 16);
+
+template <bool TALL_A, bool TALL_B, bool DIRECT, typename S>
+__device__ __forceinline__ void run_tile(const GemmParams &p, int block, unsigned char *a0, unsigned char *a1,
+                                         unsigned char *a2, unsigned char *a3, unsigned char *b0, unsigned char *b1,
+                                         unsigned char *b2, unsigned char *b3) {
+    if constexpr (S::STAGES == 2) S::template run<TALL_A, TALL_B, DIRECT>(p, block, {a0, a1}, {b0, b1});
+    else if constexpr (S::STAGES == 3) S::template run<TALL_A, TALL_B, DIRECT>(p, block, {a0, a1, a2}, {b0, b1, b2});
+    else S::template run<TALL_A, TALL_B, DIRECT>(p, block, {a0, a1, a2, a3}, {b0, b1, b2, b3});
+}
+
+// The forward's product.
+template <bool F32, bool DIRECT, typename S> __global__ __launch_bounds__(S::NT, S::WAVES) void fwd_kernel(GemmParams p) {
+    TILE_BUFFERS(S)
+    run_tile<false, false, DIRECT, S>(p, blockIdx.x, a0, a1, a2, a3, b0, b1, b2, b3);
+}
+
+// The backward's products side by side: the first `blocks` workgroups form
+// dw = dz^T x, the others dx = dz w.
+template <bool F32, bool DIRECT, typename S>
+__global__ __launch_bounds__(S::NT, S::WAVES) void bwd_kernel(GemmParams dw, GemmParams dx, int blocks) {
+    TILE_BUFFERS(S)
+    if ((int)blockIdx.x < blocks) run_tile<true, true, DIRECT, S>(dw, blockIdx.x, a0, a1, a2, a3, b0, b1, b2, b3);
+    else run_tile<false, true, DIRECT, S>(dx, blockIdx.x - blocks, a0, a1, a2, a3, b0, b1, b2, b3);
+}
+// One of them (256 x 256 tiles fill the card alone, and have no registers to spare).
+template <bool TALL_A, typename S> __global__ __launch_bounds__(S::NT, S::WAVES) void large_kernel(GemmParams p) {
+    TILE_BUFFERS(S)
+    run_tile<TALL_A, true, true, S>(p, blockIdx.x, a0, a1, a2, a3, b0, b1, b2, b3);
+}
+
+// What remains after the products: the sums of the splits with their epilogue
+// (four columns a thread), and db from the row blocks' column sums.
+struct FinishParams {
+    GemmParams g[2];
+    int64_t blocks[2];   // workgroups of each
+    const float *sums;   // [n_sums][N] or null
+    int n_sums, N;
+    void *db;
+};
+
+template <bool F32> __device__ inline void sum_splits(const GemmParams &p, int64_t id) {
     const int quads = (p.N + 3) / 4;
-    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (id >= (int64_t)p.M * quads) return;
     const int64_t m = id / quads;
     const int n = (int)(id % quads) * 4;
-    float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int s = 0; s < p.splits; ++s) {
-        const float *from = p.partial + ((int64_t)s * p.M + m) * p.N + n;
-        if ((p.N & 3) == 0) {
-            const f32x4_t v = *(const f32x4_t *)from;
+    const float *from = p.partial;
+    float z[4] = {};
+#pragma unroll 4
+    for (int s = 0; s < p.splits; ++s, from += (int64_t)p.M * p.N) {
+        const auto v = Pack<true, 4>::load(from, m * p.N + n, p.N - n);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) z[e] += v[e];
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (n + e < p.N) z[e] += from[e];
-        }
+        for (int e = 0; e < 4; ++e) z[e] += v.get(e);
     }
-#define FINISH(ACT) finish4<F32, ACT>(p.e, m, n, z);
-    FOR_ACT(p.e.act, FINISH)
-#undef FINISH
+    finish<F32, 4>(p.e, m, n, z, bias_of<F32, 4>(p.e, n), residual_of<F32, 4>(p.e, m, n));
+}
+
+template <bool F32> __global__ __launch_bounds__(256) void finish_kernel(FinishParams p) {
+    __shared__ float part[4][64];
+    int64_t block = blockIdx.x;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+        if (block < p.blocks[g]) return sum_splits<F32>(p.g[g], block * 256 + threadIdx.x);
+        block -= p.blocks[g];
+    }
+    // 64 columns, four lanes each
+    const int c = threadIdx.x & 63, r = threadIdx.x >> 6;
+    const int64_t n = block * 64 + c;
+    float s = 0.0f;
+    if (n < p.N) {
+#pragma unroll 8
+        for (int b = r; b < p.n_sums; b += 4) s += p.sums[(int64_t)b * p.N + n];
+    }
+    part[r][c] = s;
+    __syncthreads();
+    if (r == 0 && n < p.N) store1<F32>(p.db, n, part[0][c] + part[1][c] + part[2][c] + part[3][c]);
 }
 
 // ---- few rows ----------------------------------------------------------------------
@@ -429,79 +626,99 @@ struct RowsParams {
 };
 
 constexpr int kRowWaves = 8;
+constexpr int kRowSteps = 4;  // steps of c in flight a wave
 
-template <bool F32, bool WIDE, int MT>
+template <bool F32, int MT>
 __global__ __launch_bounds__(64 * kRowWaves) void rows_kernel(RowsParams p) {
-    using T = typename El<F32>::type;
-    using frag = typename El<F32>::frag;
-    constexpr int CE = El<F32>::CE, BK = 8 * CE;
+    using E = El<F32>;
+    using T = typename E::type;
+    using frag = typename E::frag;
+    constexpr int CE = E::CE, BK = 8 * CE;
     __shared__ __attribute__((aligned(16))) float sums[kRowWaves][MT][16][16];
     const int wave = threadIdx.x >> 6, i = threadIdx.x & 15, j = (threadIdx.x >> 4) & 3;
-    const int n0 = blockIdx.x * 16, m0 = blockIdx.y * MT * 16;
-    const bool n_in = n0 + i < p.N;
-    const T *w = (const T *)p.w + (int64_t)(n_in ? n0 + i : 0) * p.K;
-
-    auto load = [&](const T *row, bool in, int c) {
-        union {
-            u32x4_t r;
-            T v[CE];
-            frag f;
-        } u;
-        u.r = u32x4_t{0, 0, 0, 0};
-        if constexpr (WIDE) {
-            if (in && c < p.K) u.r = *(const u32x4_t *)(row + c);
-        } else {
+    const int n0 = blockIdx.x * 16;
+    const T *w = (const T *)p.w + (int64_t)(n0 + i) * p.K + j * 2 * CE;
+    const T *x[MT];
 #pragma unroll
-            for (int e = 0; e < CE; ++e)
-                if (in && c + e < p.K) u.v[e] = row[c + e];
-        }
-        return u.f;
-    };
+    for (int t = 0; t < MT; ++t) x[t] = (const T *)p.x + (int64_t)(t * 16 + i) * p.ldx + j * 2 * CE;
 
     f32x4_t acc[MT] = {};
-    // steps of BK in turn between the waves, two at a time
-    for (int c0 = wave * BK; c0 < p.K; c0 += 2 * kRowWaves * BK) {
-        frag fw[4], fx[MT][4];
+    auto multiply = [&](const u32x4_t (&fw)[kRowSteps][2], const u32x4_t (&fx)[MT][kRowSteps][2]) {
 #pragma unroll
-        for (int s = 0; s < 4; ++s) fw[s] = load(w, n_in, c0 + (s >> 1) * kRowWaves * BK + (j * 2 + (s & 1)) * CE);
+        for (int s = 0; s < kRowSteps; ++s)
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            const int m = m0 + t * 16 + i;
-            const T *x = (const T *)p.x + (int64_t)(m < p.M ? m : 0) * p.ldx;
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int s = 0; s < 4; ++s)
-                fx[t][s] = load(x, m < p.M, c0 + (s >> 1) * kRowWaves * BK + (j * 2 + (s & 1)) * CE);
+                for (int t = 0; t < MT; ++t)
+                    acc[t] = mma<F32>(__builtin_bit_cast(frag, fw[s][h]), __builtin_bit_cast(frag, fx[t][s][h]), acc[t]);
+    };
+    // the waves take turns at spans of kRowSteps steps; c: the span's start
+    const int span = kRowSteps * BK;
+    int c = wave * span;
+    for (; c + span <= p.K; c += kRowWaves * span) {
+        u32x4_t fw[kRowSteps][2] = {}, fx[MT][kRowSteps][2] = {};
+        if (n0 + i < p.N) {
+#pragma unroll
+            for (int s = 0; s < kRowSteps; ++s)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    fw[s][h] = __builtin_nontemporal_load((const typename E::chunk_any *)(w + c + s * BK + h * CE));
         }
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
+        for (int t = 0; t < MT; ++t)
+            if (t * 16 + i < p.M) {
 #pragma unroll
-            for (int t = 0; t < MT; ++t) acc[t] = mma<F32>(fw[s], fx[t][s], acc[t]);
+                for (int s = 0; s < kRowSteps; ++s)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) fx[t][s][h] = *(const typename E::chunk_any *)(x[t] + c + s * BK + h * CE);
+            }
+        multiply(fw, fx);
+    }
+    if (c < p.K) {  // the last span, cut short
+        u32x4_t fw[kRowSteps][2] = {}, fx[MT][kRowSteps][2] = {};
+        auto edge = [&](const T *row, int at) {
+            const int left = p.K - at - j * 2 * CE;
+            if (left >= CE) return (u32x4_t)*(const typename E::chunk_any *)(row + at);
+            T v[CE];
+#pragma unroll
+            for (int e = 0; e < CE; ++e) v[e] = e < left ? row[at + e] : (T)0.0f;
+            return __builtin_bit_cast(u32x4_t, v);
+        };
+#pragma unroll
+        for (int s = 0; s < kRowSteps; ++s)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int at = c + s * BK + h * CE;
+                if (n0 + i < p.N) fw[s][h] = edge(w, at);
+#pragma unroll
+                for (int t = 0; t < MT; ++t)
+                    if (t * 16 + i < p.M) fx[t][s][h] = edge(x[t], at);
+            }
+        multiply(fw, fx);
     }
     // lane (i, j): row t 16 + i of x, columns 4 j .. 4 j + 3
 #pragma unroll
     for (int t = 0; t < MT; ++t) *(f32x4_t *)&sums[wave][t][i][j * 4] = acc[t];
     __syncthreads();
-    for (int id = threadIdx.x; id < MT * 64; id += 64 * kRowWaves) {
-        const int t = id >> 6, r = id >> 2 & 15, q = (id & 3) * 4;
-        const int64_t m = m0 + t * 16 + r;
-        if (m >= p.M) continue;
-        float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (threadIdx.x < MT * 64) {
+        const int t = threadIdx.x >> 6, r = threadIdx.x >> 2 & 15, q = (threadIdx.x & 3) * 4;
+        const int m = t * 16 + r, n = n0 + q;
+        const auto bias = bias_of<F32, 4>(p.e, n), res = residual_of<F32, 4>(p.e, m, n);
+        float z[4] = {};
 #pragma unroll
         for (int v = 0; v < kRowWaves; ++v) {
-            const f32x4_t s = *(const f32x4_t *)&sums[v][t][r][q];
+            const f32x4_t x = *(const f32x4_t *)&sums[v][t][r][q];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) z[e] += s[e];
+            for (int e = 0; e < 4; ++e) z[e] += x[e];
         }
-#define FINISH(ACT) finish4<F32, ACT>(p.e, m, n0 + q, z);
-        FOR_ACT(p.e.act, FINISH)
-#undef FINISH
+        finish<F32, 4>(p.e, m, n, z, bias, res);
     }
 }
 
 // ---- dz and db -----------------------------------------------------------------------
 
-// dz = dy act'(z) (one element type rounding) and each block's column sums of
-// the unrounded dz.  A block takes 32 lanes of V columns by `rows` rows.
+// dz = dy act'(z) (rounded once) and each block's column sums of the unrounded
+// dz.  A block takes 32 lanes of four columns by `rows` rows.
 struct DzParams {
     const void *dy, *z;
     void *dz;         // null: only the sums
@@ -510,185 +727,275 @@ struct DzParams {
     int N, rows;
 };
 
-template <bool F32, int ACT, int V> __global__ __launch_bounds__(256) void dz_kernel(DzParams p) {
-    __shared__ float part[8][32 * V];
+template <bool F32, int ACT> __global__ __launch_bounds__(256) void dz_kernel(DzParams p) {
+    __shared__ float part[8][128];
     const int cl = threadIdx.x & 31, rl = threadIdx.x >> 5;
-    const int n = (blockIdx.x * 32 + cl) * V;
+    const int n = (blockIdx.x * 32 + cl) * 4, left = p.N - n;
     const int64_t first = (int64_t)blockIdx.y * p.rows, last = min(p.M, first + p.rows);
-    float sum[V] = {};
-    if (n < p.N) {
+    float sum[4] = {};
+    if (left > 0) {
 #pragma unroll 4
         for (int64_t m = first + rl; m < last; m += 8) {
-            float d[V], z[V];
-            if constexpr (V == 4) {
-                load4<F32>(p.dy, m * p.lddy + n, d);
-                if constexpr (ACT != HYENA_ACT_NONE) load4<F32>(p.z, m * p.N + n, z);
-            } else {
-                d[0] = load1<F32>(p.dy, m * p.lddy + n);
-                if constexpr (ACT != HYENA_ACT_NONE) z[0] = load1<F32>(p.z, m * p.N + n);
+            const auto rd = Pack<F32, 4>::load(p.dy, m * p.lddy + n, left);
+            float d[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) d[e] = rd.get(e);
+            if constexpr (ACT != HYENA_ACT_NONE) {
+                const auto rz = Pack<F32, 4>::load(p.z, m * p.N + n, left);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) d[e] *= act_slope<ACT>(rz.get(e));
             }
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                if constexpr (ACT != HYENA_ACT_NONE) d[e] *= act_slope<ACT>(z[e]);
-                sum[e] += d[e];
-            }
-            if (p.dz) {
-                if constexpr (V == 4) store4<F32>(p.dz, m * p.N + n, d);
-                else store1<F32>(p.dz, m * p.N + n, d[0]);
-            }
+            for (int e = 0; e < 4; ++e) sum[e] += d[e];
+            if (p.dz) Pack<F32, 4>::store(p.dz, m * p.N + n, left, d);
         }
     }
     if (!p.sums) return;
 #pragma unroll
-    for (int e = 0; e < V; ++e) part[rl][cl * V + e] = sum[e];
+    for (int e = 0; e < 4; ++e) part[rl][cl * 4 + e] = sum[e];
     __syncthreads();
-    for (int c = threadIdx.x; c < 32 * V; c += 256) {
-        const int col = blockIdx.x * 32 * V + c;
-        if (col >= p.N) continue;
-        float s = 0.0f;
-#pragma unroll
-        for (int r = 0; r < 8; ++r) s += part[r][c];
-        p.sums[(int64_t)blockIdx.y * p.N + col] = s;
-    }
-}
-
-template <bool F32> __global__ __launch_bounds__(64) void db_kernel(const float *sums, int blocks, int N, void *db) {
-    const int n = blockIdx.x * 64 + threadIdx.x;
-    if (n >= N) return;
+    const int col = blockIdx.x * 128 + threadIdx.x;
+    if (threadIdx.x >= 128 || col >= p.N) return;
     float s = 0.0f;
-    for (int b = 0; b < blocks; ++b) s += sums[(int64_t)b * N + n];
-    store1<F32>(db, n, s);
+#pragma unroll
+    for (int r = 0; r < 8; ++r) s += part[r][threadIdx.x];
+    p.sums[(int64_t)blockIdx.y * p.N + col] = s;
 }
 
 // ---- host --------------------------------------------------------------------------------
 
 constexpr int kRowsMost = 32;  // rows of x up to which rows_kernel is taken
 
+template <bool F32> using Small = Shape<F32, 2, 2, 4, 4, 2>;  // 128 x 128 tiles, 4 waves, two workgroups a unit
+template <bool F32> using Deep = Shape<F32, 2, 2, 4, 4, 4>;    // the same, three steps ahead, one workgroup a unit
+using Large = Shape<false, 2, 4, 8, 4, 2>;                    // 256 x 256 tiles, 8 waves
+
+// Products that run in one launch.
 struct Plan {
-    bool large;  // 256 x 256 tiles (else 128 x 128)
-    int tiles_m, tiles_n, splits, c_per_split;
+    bool large, deep;
+    int tiles_m[2], tiles_n[2], splits[2], c_per_split[2];
+    int64_t blocks[2], partial[2];  // workgroups; bytes of partial sums
+};
+struct Size {
+    int64_t M, N, C;
 };
 
+constexpr int64_t kLeastSteps = 8;  // of a split: below, its partial sums cost more than they save
+
 // 256 x 256 tiles where they fill the card's 256 units about as well as 128 x
-// 128 ones; c is split where there are too few tiles for all units.
-Plan plan_of(int64_t M, int64_t N, int64_t C, bool f32, bool direct) {
-    const int64_t t128 = ceil_div(M, 128) * ceil_div(N, 128), t256 = ceil_div(M, 256) * ceil_div(N, 256);
+// 128 ones.  c is split where a workgroup would walk much more than its share
+// of all steps.  Sharers: the 256 units, or, for a pair of products in small
+// tiles, 512, two a unit.  (Backward at M = 256, N = K = 4096 bf16: 52 us with
+// 512, 74 us with 256; forward there 23.5 us with 256, 25.7 us with 512.)
+// Where there is one workgroup a unit or less, it runs three steps ahead
+// instead of one (forward at M = 1024, N = K = 4096: 43 against 49 us).
+Plan plan_of(const Size *sz, int n, bool f32, bool direct) {
+    int64_t t128 = 0, t256 = 0;
     const int64_t bk = f32 ? 32 : 64;
-    Plan p;
+    for (int g = 0; g < n; ++g) {
+        t128 += ceil_div(sz[g].M, 128) * ceil_div(sz[g].N, 128);
+        t256 += ceil_div(sz[g].M, 256) * ceil_div(sz[g].N, 256);
+    }
+    Plan p = {};
     p.large = !f32 && direct && t256 >= 128 && 4 * ceil_div(t256, 256) <= ceil_div(t128, 256) * 5 / 4;
-    const int64_t edge = p.large ? 256 : 128, tiles = p.large ? t256 : t128;
-    p.tiles_m = (int)ceil_div(M, edge);
-    p.tiles_n = (int)ceil_div(N, edge);
-    int64_t splits = tiles >= 192 ? 1 : 256 / tiles;
-    const int64_t most = ceil_div(C, 4 * bk);
-    splits = splits < most ? splits : most;
-    if (splits < 1) splits = 1;
-    const int64_t steps = ceil_div(ceil_div(C, bk), splits);
-    p.c_per_split = (int)(steps * bk);
-    p.splits = C > 0 ? (int)ceil_div(C, steps * bk) : 1;
-    if (C == 0) p.c_per_split = (int)bk;
+    const int64_t edge = p.large ? 256 : 128;
+    int64_t work = 0;
+    for (int g = 0; g < n; ++g)
+        work += ceil_div(sz[g].M, edge) * ceil_div(sz[g].N, edge) * (ceil_div(sz[g].C, bk) + 4);
+    int64_t share = ceil_div(work, p.large || n == 1 ? 256 : 512);
+    if (share < kLeastSteps) share = kLeastSteps;
+    for (int g = 0; g < n; ++g) {
+        p.tiles_m[g] = (int)ceil_div(sz[g].M, edge);
+        p.tiles_n[g] = (int)ceil_div(sz[g].N, edge);
+        const int64_t all = ceil_div(sz[g].C, bk);
+        const int64_t splits = all * 2 > share * 3 ? ceil_div(all, share) : 1;
+        const int64_t steps = all > 0 ? ceil_div(all, splits) : 1;
+        p.c_per_split[g] = (int)(steps * bk);
+        p.splits[g] = all > 0 ? (int)ceil_div(all, steps) : 1;
+        p.blocks[g] = (int64_t)p.tiles_m[g] * p.tiles_n[g] * p.splits[g];
+        if (p.splits[g] > 1) p.partial[g] = (p.splits[g] * sz[g].M * sz[g].N * 4 + 15) / 16 * 16;
+    }
+    p.deep = !p.large && direct && p.blocks[0] + p.blocks[1] <= 256;
     return p;
 }
 
-int64_t partial_bytes(int64_t M, int64_t N, int64_t C, bool f32) {
-    int64_t most = 0;
-    for (int direct = 0; direct < 2; ++direct) {
-        const Plan p = plan_of(M, N, C, f32, direct);
-        if (p.splits > 1 && p.splits * M * N * 4 > most) most = p.splits * M * N * 4;
-    }
-    return (most + 15) / 16 * 16;
+// Workspace for the partial sums, whatever the operands' alignment.
+int64_t partial_bytes(const Size *sz, int n, bool f32) {
+    const Plan a = plan_of(sz, n, f32, false), b = plan_of(sz, n, f32, true);
+    const int64_t x = a.partial[0] + a.partial[1], y = b.partial[0] + b.partial[1];
+    return x > y ? x : y;
 }
 
-bool epilogue_vec(const Epilogue &e, int64_t eb) {
-    const int64_t b = 4 * eb;
-    return e.N % 4 == 0 && e.ldy % 4 == 0 && aligned(e.y, b) && aligned(e.preact, b) && aligned(e.bias, b) &&
-           (!e.residual || (e.ldr % 4 == 0 && aligned(e.residual, b)));
+// Whether an operand can be fetched straight into LDS: aligned 16-byte chunks,
+// none across its edge, offsets inside a tile below 2^31.
+bool direct_ok(const void *p, int64_t ld, int64_t row, int64_t eb) {
+    return aligned(p, 16) && (ld * eb) % 16 == 0 && (row * eb) % 16 == 0 && ld < (int64_t)1 << 21;
 }
 
-// C = A B^T with the epilogue, `partial` at least partial_bytes.
-template <bool F32, bool TALL_A, bool TALL_B>
-int gemm(const void *a, int64_t lda, const void *b, int64_t ldb, int64_t M, int64_t N, int64_t C, Epilogue e,
-         float *partial, hipStream_t stream) {
-    if (M == 0 || N == 0) return HYENA_OK;
-    const int64_t eb = F32 ? 4 : 2, ce = 16 / eb;
+GemmParams gemm_params(const Plan &pl, int g, const Size &sz, const void *a, int64_t lda, const void *b, int64_t ldb,
+                       Epilogue e, char *&ws) {
     GemmParams p = {};
-    p.a = a, p.b = b, p.lda = lda, p.ldb = ldb, p.M = (int)M, p.N = (int)N, p.C = (int)C;
+    p.a = a, p.b = b, p.lda = lda, p.ldb = ldb, p.M = (int)sz.M, p.N = (int)sz.N, p.C = (int)sz.C;
+    p.tiles_m = pl.tiles_m[g], p.tiles_n = pl.tiles_n[g], p.splits = pl.splits[g], p.c_per_split = pl.c_per_split[g];
     p.e = e;
-    p.e.N = (int)N;
-    p.e.vec = epilogue_vec(p.e, eb);
-    // 16-byte chunks: aligned, none across an operand's edge, offsets in a tile below 2^31
-    const bool direct = aligned(a, 16) && aligned(b, 16) && lda % ce == 0 && ldb % ce == 0 &&
-                        (TALL_A ? M : C) % ce == 0 && (TALL_B ? N : C) % ce == 0 &&
-                        lda < (int64_t)1 << 21 && ldb < (int64_t)1 << 21;
-    const Plan pl = plan_of(M, N, C, F32, direct);
-    p.tiles_m = pl.tiles_m, p.tiles_n = pl.tiles_n, p.splits = pl.splits, p.c_per_split = pl.c_per_split;
-    p.partial = pl.splits > 1 ? partial : nullptr;
-    const int64_t blocks = (int64_t)pl.tiles_m * pl.tiles_n * pl.splits;
+    p.e.M = p.M, p.e.N = p.N;
+    if (pl.splits[g] > 1) {
+        p.partial = (float *)ws;
+        ws += pl.partial[g];
+    }
+    return p;
+}
+
+template <bool F32> int launch_finish(const GemmParams *g, int n, const float *sums, int n_sums, int N, void *db,
+                                      hipStream_t stream) {
+    FinishParams p = {};
+    int64_t blocks = 0;
+    for (int i = 0; i < n; ++i)
+        if (g[i].partial) {
+            p.g[i] = g[i];
+            p.blocks[i] = ceil_div((int64_t)g[i].M * ceil_div(g[i].N, 4), 256);
+            blocks += p.blocks[i];
+        }
+    if (db) {
+        p.sums = sums, p.n_sums = n_sums, p.N = N, p.db = db;
+        blocks += ceil_div(N, 64);
+    }
+    if (blocks == 0) return HYENA_OK;
     if (blocks > 0x7fffffff) return HYENA_ERR_UNSUPPORTED;
-    const dim3 grid((unsigned)blocks);
-    if (pl.large) {
-        if constexpr (!F32)
-            hipLaunchKernelGGL((gemm_kernel<F32, TALL_A, TALL_B, true, 2, 4, 8, 4>), grid, dim3(512), 0, stream, p);
-    } else if (direct) {
-        hipLaunchKernelGGL((gemm_kernel<F32, TALL_A, TALL_B, true, 2, 2, 4, 4>), grid, dim3(256), 0, stream, p);
-    } else {
-        hipLaunchKernelGGL((gemm_kernel<F32, TALL_A, TALL_B, false, 2, 2, 4, 4>), grid, dim3(256), 0, stream, p);
-    }
-    if (p.partial) {
-        const int64_t n = ceil_div(M * ceil_div(N, 4), 256);
-        if (n > 0x7fffffff) return HYENA_ERR_UNSUPPORTED;
-        hipLaunchKernelGGL(split_kernel<F32>, dim3((unsigned)n), dim3(256), 0, stream, p);
-    }
+    hipLaunchKernelGGL(finish_kernel<F32>, dim3((unsigned)blocks), dim3(256), 0, stream, p);
     return launch_status();
 }
 
 template <bool F32>
-int rows_product(const void *x, int64_t ldx, const void *w, int64_t M, int64_t N, int64_t K, Epilogue e,
-                 hipStream_t stream) {
+int linear_fwd(const void *x, int64_t ldx, const void *w, int64_t M, int64_t N, int64_t K, Epilogue e, void *ws,
+               hipStream_t stream) {
     const int64_t eb = F32 ? 4 : 2;
-    RowsParams p = {};
-    p.x = x, p.w = w, p.ldx = ldx, p.M = (int)M, p.N = (int)N, p.K = (int)K;
-    p.e = e;
-    p.e.N = (int)N;
-    p.e.vec = epilogue_vec(p.e, eb);
-    const bool wide = aligned(x, 16) && aligned(w, 16) && (ldx * eb) % 16 == 0 && (K * eb) % 16 == 0;
-    const dim3 grid((unsigned)ceil_div(N, 16), 1), block(64 * kRowWaves);
-    if (M <= 16)
-        hipLaunchKernelGGL((wide ? rows_kernel<F32, true, 1> : rows_kernel<F32, false, 1>), grid, block, 0, stream, p);
-    else
-        hipLaunchKernelGGL((wide ? rows_kernel<F32, true, 2> : rows_kernel<F32, false, 2>), grid, block, 0, stream, p);
-    return launch_status();
+    if (M <= kRowsMost) {
+        RowsParams p = {};
+        p.x = x, p.w = w, p.ldx = ldx, p.M = (int)M, p.N = (int)N, p.K = (int)K;
+        p.e = e;
+        p.e.M = p.M, p.e.N = p.N;
+        hipLaunchKernelGGL((M <= 16 ? rows_kernel<F32, 1> : rows_kernel<F32, 2>), dim3((unsigned)ceil_div(N, 16)),
+                           dim3(64 * kRowWaves), 0, stream, p);
+        return launch_status();
+    }
+    const Size sz = {M, N, K};
+    const bool direct = direct_ok(x, ldx, K, eb) && direct_ok(w, K, K, eb);
+    const Plan pl = plan_of(&sz, 1, F32, direct);
+    if (pl.blocks[0] > 0x7fffffff) return HYENA_ERR_UNSUPPORTED;
+    char *at = (char *)ws;
+    const GemmParams p = gemm_params(pl, 0, sz, x, ldx, w, K, e, at);
+    const dim3 grid((unsigned)pl.blocks[0]);
+    if (pl.large) {
+        if constexpr (!F32) hipLaunchKernelGGL((fwd_kernel<F32, true, Large>), grid, dim3(Large::NT), 0, stream, p);
+    } else if (pl.deep) {
+        hipLaunchKernelGGL((fwd_kernel<F32, true, Deep<F32>>), grid, dim3(Deep<F32>::NT), 0, stream, p);
+    } else if (direct) {
+        hipLaunchKernelGGL((fwd_kernel<F32, true, Small<F32>>), grid, dim3(Small<F32>::NT), 0, stream, p);
+    } else {
+        hipLaunchKernelGGL((fwd_kernel<F32, false, Small<F32>>), grid, dim3(Small<F32>::NT), 0, stream, p);
+    }
+    const int st = launch_status();
+    return st != HYENA_OK ? st : launch_finish<F32>(&p, 1, nullptr, 0, 0, nullptr, stream);
 }
 
 // Row blocks of dz_kernel.
 int64_t dz_blocks(int64_t M, int64_t N) {
-    const int64_t cols = ceil_div(N, 128);
-    int64_t blocks = ceil_div(1024, cols);
-    const int64_t most = ceil_div(M, 32);
+    const int64_t blocks = ceil_div(1024, ceil_div(N, 128)), most = ceil_div(M, 32);
     return blocks < most ? blocks : most;
 }
 
+// Workspace of the backward: dz, the column sums, the products' partial sums.
+struct BwdSpace {
+    int64_t dz, sums, partial;
+};
+BwdSpace bwd_space(int64_t M, int64_t N, int64_t K, int act, int dtype) {
+    const bool f32 = dtype == HYENA_DTYPE_F32;
+    BwdSpace s = {};
+    if (act != HYENA_ACT_NONE) s.dz = (M * N * (f32 ? 4 : 2) + 15) / 16 * 16;
+    if (M == 0 || N == 0) return s;
+    s.sums = (dz_blocks(M, N) * N * 4 + 15) / 16 * 16;
+    if (K == 0) return s;
+    // one product alone splits as much as both together, or more
+    const Size both[2] = {{M, K, N}, {N, K, M}};
+    for (int64_t b : {partial_bytes(both, 2, f32), partial_bytes(both, 1, f32), partial_bytes(both + 1, 1, f32)})
+        if (b > s.partial) s.partial = b;
+    return s;
+}
+
 template <bool F32>
-int dz_and_db(const void *dy, int64_t lddy, const void *z, int act, int64_t M, int64_t N, void *dz, float *sums,
-              void *db, hipStream_t stream) {
-    if (N == 0) return HYENA_OK;
+int linear_bwd(const void *x, const void *w, const void *z, const void *dy, int64_t M, int64_t N, int64_t K,
+               int64_t ldx, int64_t lddy, int64_t lddx, int act, void *dx, void *dw, void *db, char *ws,
+               const BwdSpace &sp, hipStream_t stream) {
     const int64_t eb = F32 ? 4 : 2;
-    const int64_t blocks = dz_blocks(M, N);
-    if (M > 0) {
+    if (M == 0 || K == 0) dx = nullptr;
+    if (N == 0 || K == 0) dw = nullptr;
+    if (N == 0) db = nullptr;
+    const void *dz = dy;
+    int64_t lddz = lddy;
+    void *made = nullptr;
+    if (act != HYENA_ACT_NONE && (dx || dw) && M > 0 && N > 0) {
+        dz = made = ws;
+        lddz = N;
+    }
+    const int64_t row_blocks = M > 0 && N > 0 ? dz_blocks(M, N) : 0;
+    float *sums = (float *)(ws + sp.dz);
+    int st = HYENA_OK;
+    if ((made || db) && row_blocks > 0) {
         DzParams p = {};
-        p.dy = dy, p.z = z, p.dz = dz, p.sums = db ? sums : nullptr, p.M = M, p.lddy = lddy, p.N = (int)N;
-        p.rows = (int)ceil_div(M, blocks);
-        const bool vec = N % 4 == 0 && lddy % 4 == 0 && aligned(dy, 4 * eb) && aligned(z, 4 * eb);
-        const dim3 grid((unsigned)ceil_div(N, vec ? 128 : 32), (unsigned)blocks);
-#define DZ(ACT)                                                                                                    \
-    hipLaunchKernelGGL((vec ? dz_kernel<F32, ACT, 4> : dz_kernel<F32, ACT, 1>), grid, dim3(256), 0, stream, p);
+        p.dy = dy, p.z = z, p.dz = made, p.sums = db ? sums : nullptr, p.M = M, p.lddy = lddy, p.N = (int)N;
+        p.rows = (int)ceil_div(M, row_blocks);
+        const dim3 grid((unsigned)ceil_div(N, 128), (unsigned)row_blocks);
+#define DZ(ACT) hipLaunchKernelGGL((dz_kernel<F32, ACT>), grid, dim3(256), 0, stream, p);
         FOR_ACT(act, DZ)
 #undef DZ
+        if ((st = launch_status()) != HYENA_OK) return st;
     }
-    if (db)
-        hipLaunchKernelGGL(db_kernel<F32>, dim3((unsigned)ceil_div(N, 64)), dim3(64), 0, stream, sums,
-                           M > 0 ? (int)blocks : 0, (int)N, db);
-    return launch_status();
+    Size sz[2];
+    GemmParams g[2] = {};
+    int n = 0;
+    if (dw) sz[n++] = Size{N, K, M};
+    if (dx) sz[n++] = Size{M, K, N};
+    if (n > 0) {
+        const bool direct = direct_ok(dz, lddz, N, eb) && (!dx || direct_ok(w, K, K, eb)) &&
+                            (!dw || direct_ok(x, ldx, K, eb));
+        const Plan pl = plan_of(sz, n, F32, direct);
+        const int64_t blocks = pl.blocks[0] + pl.blocks[1];
+        if (blocks > 0x7fffffff) return HYENA_ERR_UNSUPPORTED;
+        char *at = ws + sp.dz + sp.sums;
+        Epilogue e = {};
+        int i = 0;
+        if (dw) {
+            e.y = dw, e.ldy = K;
+            g[i] = gemm_params(pl, i, sz[i], dz, lddz, x, ldx, e, at);
+            ++i;
+        }
+        if (dx) {
+            e.y = dx, e.ldy = lddx;
+            g[i] = gemm_params(pl, i, sz[i], dz, lddz, w, K, e, at);
+        }
+        const int first = dw ? (int)pl.blocks[0] : 0;
+        const GemmParams &second = g[n - 1];
+        const dim3 grid((unsigned)blocks);
+        if (pl.large) {
+            if constexpr (!F32) {
+                if (dw) hipLaunchKernelGGL((large_kernel<true, Large>), dim3((unsigned)first), dim3(Large::NT), 0, stream, g[0]);
+                if (dx)
+                    hipLaunchKernelGGL((large_kernel<false, Large>), dim3((unsigned)(blocks - first)), dim3(Large::NT), 0,
+                                       stream, second);
+            }
+        } else if (pl.deep) {
+            hipLaunchKernelGGL((bwd_kernel<F32, true, Deep<F32>>), grid, dim3(Deep<F32>::NT), 0, stream, g[0], second, first);
+        } else if (direct) {
+            hipLaunchKernelGGL((bwd_kernel<F32, true, Small<F32>>), grid, dim3(Small<F32>::NT), 0, stream, g[0], second,
+                               first);
+        } else {
+            hipLaunchKernelGGL((bwd_kernel<F32, false, Small<F32>>), grid, dim3(Small<F32>::NT), 0, stream, g[0],
+                               second, first);
+        }
+        if ((st = launch_status()) != HYENA_OK) return st;
+    }
+    return launch_finish<F32>(g, n, sums, (int)row_blocks, (int)N, db, stream);
 }
 
 int check_linear(int64_t M, int64_t N, int64_t K, int act, int dtype) {
@@ -699,48 +1006,6 @@ int check_linear(int64_t M, int64_t N, int64_t K, int act, int dtype) {
     const int64_t most = ((int64_t)1 << 31) - 1024;  // tile coordinates are 32 bits
     if (M > most || N > most || K > most) return HYENA_ERR_SHAPE;
     return HYENA_OK;
-}
-
-// Workspace of the backward: dz, the column sums, then a product's partials.
-struct BwdSpace {
-    int64_t dz, sums, partial;
-};
-BwdSpace bwd_space(int64_t M, int64_t N, int64_t K, int act, int dtype) {
-    const bool f32 = dtype == HYENA_DTYPE_F32;
-    BwdSpace s = {};
-    if (act != HYENA_ACT_NONE) s.dz = (M * N * (f32 ? 4 : 2) + 15) / 16 * 16;
-    if (M > 0 && N > 0) s.sums = (dz_blocks(M, N) * N * 4 + 15) / 16 * 16;
-    if (M > 0 && N > 0 && K > 0) {
-        const int64_t a = partial_bytes(M, K, N, f32), b = partial_bytes(N, K, M, f32);
-        s.partial = a > b ? a : b;
-    }
-    return s;
-}
-
-template <bool F32>
-int linear_bwd(const void *x, const void *w, const void *z, const void *dy, int64_t M, int64_t N, int64_t K,
-               int64_t ldx, int64_t lddy, int64_t lddx, int act, void *dx, void *dw, void *db, char *ws,
-               const BwdSpace &sp, hipStream_t stream) {
-    const void *dz = dy;
-    int64_t lddz = lddy;
-    void *made = nullptr;
-    if (act != HYENA_ACT_NONE && (dx || dw)) {
-        dz = made = ws;
-        lddz = N;
-    }
-    int st = HYENA_OK;
-    if (made || db) st = dz_and_db<F32>(dy, lddy, z, act, M, N, made, (float *)(ws + sp.dz), db, stream);
-    float *partial = (float *)(ws + sp.dz + sp.sums);
-    Epilogue e = {};
-    if (dx && st == HYENA_OK) {
-        e.y = dx, e.ldy = lddx;
-        st = gemm<F32, false, true>(dz, lddz, w, K, M, K, N, e, partial, stream);
-    }
-    if (dw && st == HYENA_OK) {
-        e.y = dw, e.ldy = K;
-        st = gemm<F32, true, true>(dz, lddz, x, ldx, N, K, M, e, partial, stream);
-    }
-    return st;
 }
 
 }  // namespace
@@ -758,7 +1023,8 @@ int hyena_linear_workspace(int64_t M, int64_t N, int64_t K, int act, int dtype, 
         const BwdSpace s = bwd_space(M, N, K, act, dtype);
         *bytes_out = s.dz + s.sums + s.partial;
     } else {
-        *bytes_out = M > kRowsMost && N > 0 ? partial_bytes(M, N, K, dtype == HYENA_DTYPE_F32) : 0;
+        const Size sz = {M, N, K};
+        *bytes_out = M > kRowsMost && N > 0 ? partial_bytes(&sz, 1, dtype == HYENA_DTYPE_F32) : 0;
     }
     return HYENA_OK;
 }
@@ -793,10 +1059,7 @@ int hyena_linear_fwd(const void *x, const void *w, const void *bias, const void 
     e.bias = bias, e.residual = residual, e.ldr = ldr, e.ldy = ldy, e.y = y, e.preact = preact, e.act = act;
     hipStream_t s = (hipStream_t)stream;
     const bool f32 = dtype == HYENA_DTYPE_F32;
-    if (M <= kRowsMost)
-        return f32 ? rows_product<true>(x, ldx, w, M, N, K, e, s) : rows_product<false>(x, ldx, w, M, N, K, e, s);
-    return f32 ? gemm<true, false, false>(x, ldx, w, K, M, N, K, e, (float *)workspace, s)
-               : gemm<false, false, false>(x, ldx, w, K, M, N, K, e, (float *)workspace, s);
+    return f32 ? linear_fwd<true>(x, ldx, w, M, N, K, e, workspace, s) : linear_fwd<false>(x, ldx, w, M, N, K, e, workspace, s);
 }
 
 int hyena_linear_bwd(const void *x, const void *w, const void *preact, const void *dy, int64_t M, int64_t N,

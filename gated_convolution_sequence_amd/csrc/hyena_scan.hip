@@ -219,9 +219,6 @@ template <typename G> struct Place {
     }
 };
 
-// Whether any lane of the wave says so.
-__device__ inline bool any_lane(bool x) { return __builtin_amdgcn_ballot_w64(x) != 0; }
-
 // s -> a s + x; RESETS: where a may be 0 and must drop s.
 template <bool RESETS> __device__ inline float walk(float a, float x, float s) {
     if constexpr (RESETS) return apply(a, x, s);

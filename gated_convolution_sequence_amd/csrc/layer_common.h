@@ -40,6 +40,9 @@ template <bool F32> __device__ inline void store1(void *p, size_t i, float x) {
     else ((bf16_t *)p)[i] = (bf16_t)x;
 }
 
+// Whether any lane of the wave says so.
+__device__ inline bool any_lane(bool x) { return __builtin_amdgcn_ballot_w64(x) != 0; }
+
 // The decay a of a gate, and da/dg.  With e = exp(-g), sigmoid(g) = 1 / (1 + e)
 // and its slope is e a^2, which keeps 1 - a exact to rounding where a is near
 // 1.  a is 0 for g = -inf and for a finite g whose e overflows (g < -88); the
