@@ -371,7 +371,7 @@ template <bool F32, int WM, int WN, int MT, int NTL, int ST> struct Shape {
     static constexpr int NT = 64 * WM * WN, BM = WM * MT * 16, BN = WN * NTL * 16;
     static constexpr int CE = El<F32>::CE, BK = 8 * CE;
     static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128, STAGES = ST;
-    static constexpr int WAVES = ST * (A_BYTES + B_BYTES) > 80 * 1024 ? NT / 256 : NT / 128;  // a SIMD, by LDS
+    static constexpr int WAVES = ST * (A_BYTES + B_BYTES) > 80 * 1024 ? NT / 256 : ST * (A_BYTES + B_BYTES) > 53 * 1024 ? NT / 128 : 3;  // a SIMD, by LDS
 
     // The workgroup's tile of one product; la and lb are the operands' buffers.
     template <bool TALL_A, bool TALL_B, bool DIRECT>
@@ -477,17 +477,18 @@ template <bool F32, int WM, int WN, int MT, int NTL, int ST> struct Shape {
             }
         }
 
-        // The sums go through LDS, 64 rows by 64 columns a wave at a time in
-        // its own 16 KB, so that 8 lanes write a row's 64 columns: 16 bytes a
+        // The sums go through LDS, up to 64 rows by 64 columns a wave at a time in
+        // a piece of its own, so that 8 lanes write a row's 64 columns: 16 bytes a
         // lane in bf16, whole 128-byte lines.  Rows are 256 bytes, their
         // 16-byte chunks XOR-ed with the row: no bank conflicts either way.
-        static_assert(NTL == 4 && MT % 4 == 0 && A_BYTES == B_BYTES, "64 x 64 pieces of a wave");
-        constexpr int PER = A_BYTES / 16384;  // waves a buffer holds
+        constexpr int G = MT < 4 ? MT : 4, PIECE = G * 16 * 256;
+        static_assert(NTL == 4 && MT % G == 0 && A_BYTES == B_BYTES && WM * WN * PIECE <= 4 * A_BYTES, "pieces of 64 columns");
+        constexpr int PER = A_BYTES / PIECE;  // waves a buffer holds
         unsigned char *const buf[4] = {la[0], la[1], lb[0], lb[1]};
         lds piece = (lds)la[0];
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-            if (wave / PER == q) piece = (lds)buf[q] + wave % PER * 16384;
+            if (wave / PER == q) piece = (lds)buf[q] + wave % PER * PIECE;
         const int c8 = threadIdx.x & 7, r8 = (threadIdx.x >> 3) & 7;
         const int n = n0 + wn + c8 * 8;
         const Epilogue &ep = p.e;
@@ -495,21 +496,21 @@ template <bool F32, int WM, int WN, int MT, int NTL, int ST> struct Shape {
         const auto bias = partial ? Pack<F32, 8>::zero() : bias_of<F32, 8>(ep, n);
         __syncthreads();  // every wave is done with the operands
 #pragma unroll
-        for (int g = 0; g < MT; g += 4) {
+        for (int g = 0; g < MT; g += G) {
             const int m = m0 + wm + g * 16 + r8;
-            Pack<F32, 8> res[8];
+            Pack<F32, 8> res[2 * G];
             if (!partial) {  // all fetched before the first store (y may be the residual)
 #pragma unroll
-                for (int r = 0; r < 8; ++r) res[r] = residual_of<F32, 8>(ep, m + 8 * r, n);
+                for (int r = 0; r < 2 * G; ++r) res[r] = residual_of<F32, 8>(ep, m + 8 * r, n);
             }
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
+            for (int t = 0; t < G; ++t)
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
                     *(LDS_PTR f32x4_t *)(piece + (t * 16 + i) * 256 + (((u * 4 + j) ^ i) << 4)) = acc[g + t][u];
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the piece is this wave's own
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
+            for (int r = 0; r < 2 * G; ++r) {
                 const int row = r * 8 + r8;
                 const f32x4_t lo = *(LDS_PTR f32x4_t *)(piece + row * 256 + (((c8 * 2) ^ (row & 15)) << 4));
                 const f32x4_t hi = *(LDS_PTR f32x4_t *)(piece + row * 256 + (((c8 * 2 + 1) ^ (row & 15)) << 4));
@@ -768,11 +769,13 @@ constexpr int kRowsMost = 32;  // rows of x up to which rows_kernel is taken
 
 template <bool F32> using Small = Shape<F32, 2, 2, 4, 4, 2>;  // 128 x 128 tiles, 4 waves, two workgroups a unit
 template <bool F32> using Deep = Shape<F32, 2, 2, 4, 4, 4>;    // the same, three steps ahead, one workgroup a unit
+template <bool F32> using Fine = Shape<F32, 4, 1, 1, 4, 2>;     // 64 x 64 tiles, 4 waves, up to five workgroups a unit
+using FineDeep = Shape<false, 4, 1, 1, 4, 4>;                  // the same, three steps ahead, two workgroups a unit
 using Large = Shape<false, 2, 4, 8, 4, 2>;                    // 256 x 256 tiles, 8 waves
 
 // Products that run in one launch.
 struct Plan {
-    bool large, deep;
+    bool large, deep, fine;
     int tiles_m[2], tiles_n[2], splits[2], c_per_split[2];
     int64_t blocks[2], partial[2];  // workgroups; bytes of partial sums
 };
@@ -782,13 +785,16 @@ struct Size {
 
 constexpr int64_t kLeastSteps = 8;  // of a split: below, its partial sums cost more than they save
 
-// 256 x 256 tiles where they fill the card's 256 units about as well as 128 x
-// 128 ones.  c is split where a workgroup would walk much more than its share
-// of all steps.  Sharers: the 256 units, or, for a pair of products in small
-// tiles, 512, two a unit.  (Backward at M = 256, N = K = 4096 bf16: 52 us with
-// 512, 74 us with 256; forward there 23.5 us with 256, 25.7 us with 512.)
-// Where there is one workgroup a unit or less, it runs three steps ahead
-// instead of one (forward at M = 1024, N = K = 4096: 43 against 49 us).
+// Tiles: 256 x 256 where they fill the card's 256 units about as well as 128 x
+// 128 ones, 64 x 64 where there are fewer than 192 of 128 x 128 (at M = 1000,
+// N = K = 1024 bf16 forward 15 us, with split tiles of 128 x 128 20 us; at
+// 1021 x 777 x 521 fp32 24 against 31 us).
+// Splits: c is cut where a workgroup would walk much more than its share of
+// all steps.  One bf16 product is shared between 256 workgroups, each three
+// steps ahead of its products where a unit has one; two products between 512;
+// fp32, where a step's products are 16 times as long, between twice as many.
+// (Backward at M = 256, N = K = 4096 bf16: 48 us with 512, 74 us with 256;
+// forward 19 us with 256, 23 us with 512.)
 Plan plan_of(const Size *sz, int n, bool f32, bool direct) {
     int64_t t128 = 0, t256 = 0;
     const int64_t bk = f32 ? 32 : 64;
@@ -798,11 +804,12 @@ Plan plan_of(const Size *sz, int n, bool f32, bool direct) {
     }
     Plan p = {};
     p.large = !f32 && direct && t256 >= 128 && 4 * ceil_div(t256, 256) <= ceil_div(t128, 256) * 5 / 4;
-    const int64_t edge = p.large ? 256 : 128;
+    p.fine = !p.large && t128 < 192;
+    const int64_t edge = p.large ? 256 : p.fine ? 64 : 128;
     int64_t work = 0;
     for (int g = 0; g < n; ++g)
         work += ceil_div(sz[g].M, edge) * ceil_div(sz[g].N, edge) * (ceil_div(sz[g].C, bk) + 4);
-    int64_t share = ceil_div(work, p.large || n == 1 ? 256 : 512);
+    int64_t share = ceil_div(work, p.large ? 256 : (f32 ? 512 : 256) * n);
     if (share < kLeastSteps) share = kLeastSteps;
     for (int g = 0; g < n; ++g) {
         p.tiles_m[g] = (int)ceil_div(sz[g].M, edge);
@@ -815,7 +822,7 @@ Plan plan_of(const Size *sz, int n, bool f32, bool direct) {
         p.blocks[g] = (int64_t)p.tiles_m[g] * p.tiles_n[g] * p.splits[g];
         if (p.splits[g] > 1) p.partial[g] = (p.splits[g] * sz[g].M * sz[g].N * 4 + 15) / 16 * 16;
     }
-    p.deep = !p.large && direct && p.blocks[0] + p.blocks[1] <= 256;
+    p.deep = direct && (p.fine ? !f32 && n == 1 : !p.large && p.blocks[0] + p.blocks[1] <= 256);
     return p;
 }
 
@@ -888,6 +895,12 @@ int linear_fwd(const void *x, int64_t ldx, const void *w, int64_t M, int64_t N, 
     const dim3 grid((unsigned)pl.blocks[0]);
     if (pl.large) {
         if constexpr (!F32) hipLaunchKernelGGL((fwd_kernel<F32, true, Large>), grid, dim3(Large::NT), 0, stream, p);
+    } else if (pl.fine && pl.deep) {
+        if constexpr (!F32)
+            hipLaunchKernelGGL((fwd_kernel<F32, true, FineDeep>), grid, dim3(FineDeep::NT), 0, stream, p);
+    } else if (pl.fine) {
+        hipLaunchKernelGGL((direct ? fwd_kernel<F32, true, Fine<F32>> : fwd_kernel<F32, false, Fine<F32>>), grid,
+                           dim3(Fine<F32>::NT), 0, stream, p);
     } else if (pl.deep) {
         hipLaunchKernelGGL((fwd_kernel<F32, true, Deep<F32>>), grid, dim3(Deep<F32>::NT), 0, stream, p);
     } else if (direct) {
@@ -984,6 +997,13 @@ int linear_bwd(const void *x, const void *w, const void *z, const void *dy, int6
                     hipLaunchKernelGGL((large_kernel<false, Large>), dim3((unsigned)(blocks - first)), dim3(Large::NT), 0,
                                        stream, second);
             }
+        } else if (pl.fine && pl.deep) {
+            if constexpr (!F32)
+                hipLaunchKernelGGL((bwd_kernel<F32, true, FineDeep>), grid, dim3(FineDeep::NT), 0, stream, g[0], second,
+                                   first);
+        } else if (pl.fine) {
+            hipLaunchKernelGGL((direct ? bwd_kernel<F32, true, Fine<F32>> : bwd_kernel<F32, false, Fine<F32>>), grid,
+                               dim3(Fine<F32>::NT), 0, stream, g[0], second, first);
         } else if (pl.deep) {
             hipLaunchKernelGGL((bwd_kernel<F32, true, Deep<F32>>), grid, dim3(Deep<F32>::NT), 0, stream, g[0], second, first);
         } else if (direct) {

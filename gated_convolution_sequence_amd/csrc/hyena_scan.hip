@@ -113,55 +113,6 @@ __global__ __launch_bounds__(256) void scan_none_kernel(const float *from, float
     if (i < n) to[i] = from ? from[i] : 0.0f;
 }
 
-// What one lane reads and writes at a time: 16 bytes at any element's address
-// (the hardware takes global accesses of any alignment), or the first n
-// channels of them at the right edge of D.
-template <bool F32> struct Lane;
-template <> struct Lane<false> {
-    static constexpr int VEC = 8;
-    typedef u32x4_t raw;
-    typedef u32x4_t raw_any __attribute__((aligned(2)));
-    __device__ static raw load(const void *p, size_t e) {
-        return __builtin_nontemporal_load((const raw_any *)((const bf16_t *)p + e));
-    }
-    __device__ static raw load_part(const void *p, size_t e, int n) {
-        float x[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = i < n ? load1<false>(p, e + i) : 0.0f;
-        return pack(x);
-    }
-    __device__ static float get(const raw &r, int i) { return i & 1 ? bf_hi(r[i >> 1]) : bf_lo(r[i >> 1]); }
-    __device__ static raw pack(const float (&x)[8]) {
-        return raw{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])};
-    }
-    __device__ static void store(void *p, size_t e, const float (&x)[8]) {
-        __builtin_nontemporal_store(pack(x), (raw_any *)((bf16_t *)p + e));
-    }
-};
-template <> struct Lane<true> {
-    static constexpr int VEC = 4;
-    typedef f32x4_t raw;
-    typedef f32x4_t raw_any __attribute__((aligned(4)));
-    __device__ static raw load(const void *p, size_t e) {
-        return __builtin_nontemporal_load((const raw_any *)((const float *)p + e));
-    }
-    __device__ static raw load_part(const void *p, size_t e, int n) {
-        raw r;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) r[i] = i < n ? load1<true>(p, e + i) : 0.0f;
-        return r;
-    }
-    __device__ static float get(const raw &r, int i) { return r[i]; }
-    __device__ static void store(void *p, size_t e, const float (&x)[4]) {
-        __builtin_nontemporal_store(raw{x[0], x[1], x[2], x[3]}, (raw_any *)((float *)p + e));
-    }
-};
-template <bool F32> __device__ inline void store_part(void *p, size_t e, const float (&x)[Lane<F32>::VEC], int n) {
-#pragma unroll
-    for (int i = 0; i < Lane<F32>::VEC; ++i)
-        if (i < n) store1<F32>(p, e + i, x[i]);
-}
-
 // Geometry of a tile: R rows a lane, NS slices of them, LANES lanes a row.
 template <bool F32, int THREADS, int ROWS, int LANES_> struct Tile {
     static constexpr int VEC = Lane<F32>::VEC, LANES = LANES_, NT = THREADS;

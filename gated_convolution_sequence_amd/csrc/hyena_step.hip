@@ -7,6 +7,8 @@
 namespace layer {
 namespace {
 
+// A lane takes 16 bytes of a row (Lane), blockIdx.y counts sequences (or rows).
+
 struct StepParams {
     const void *q, *k, *v, *g, *h;
     const float *state;
@@ -17,65 +19,182 @@ struct StepParams {
     int64_t B, L, D, ld, S, R, group_size, l_h;
 };
 
+// a / b and a % b for a >= 0, b > 0; the 64-bit division only where one is wanted.
+__device__ inline int64_t quotient(int64_t a, int64_t b) {
+    return a >> 32 | b >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+__device__ inline int64_t remainder_of(int64_t a, int64_t b) { return a < b ? a : a - quotient(a, b) * b; }
+
 __device__ inline int64_t slot_of(const StepParams &p, int64_t b) { return p.slots ? p.slots[b] : b; }
 
+// The lane's n channels at element e (n may be less than VEC at the right edge).
+template <bool F32> __device__ inline typename Lane<F32>::raw load_row(const void *p, size_t e, int n) {
+    return n == Lane<F32>::VEC ? Lane<F32>::load(p, e) : Lane<F32>::load_part(p, e, n);
+}
+template <bool F32>
+__device__ inline void store_row(void *p, size_t e, const float (&x)[Lane<F32>::VEC], int n) {
+    if (n == Lane<F32>::VEC) Lane<F32>::store(p, e, x);
+    else store_part<F32>(p, e, x, n);
+}
+
+constexpr int kScanThreads = 64;
+
 template <bool F32, bool LOG>
-__global__ __launch_bounds__(256) void scan_step_kernel(StepParams p) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= p.B * p.D) return;
-    const int64_t b = i / p.D, d = i % p.D, e = b * p.ld + d;
-    const int64_t slot = slot_of(p, b);
-    float y = 0.0f;
-    if (slot >= 0 && slot < p.S) {
-        const float a = decay<LOG>(load1<F32>(p.g, e));
-        const float s = (a == 0.0f ? 0.0f : a * p.state[slot * p.D + d]) + load1<F32>(p.k, e) * load1<F32>(p.v, e);
-        p.state_out[slot * p.D + d] = s;
-        y = load1<F32>(p.q, e) * s;
+__global__ __launch_bounds__(kScanThreads) void scan_step_kernel(StepParams p) {
+    using Ln = Lane<F32>;
+    constexpr int VEC = Ln::VEC;
+    const int64_t d0 = ((int64_t)blockIdx.x * kScanThreads + threadIdx.x) * VEC;
+    const int n = (int)min((int64_t)VEC, p.D - d0);
+    if (n <= 0) return;
+    for (int64_t b = blockIdx.y; b < p.B; b += gridDim.y) {
+        const int64_t slot = slot_of(p, b);
+        float y[VEC] = {};
+        if (slot >= 0 && slot < p.S) {
+            const size_t e = b * p.ld + d0, at = slot * p.D + d0;
+            const auto q = load_row<F32>(p.q, e, n), k = load_row<F32>(p.k, e, n), v = load_row<F32>(p.v, e, n),
+                       g = load_row<F32>(p.g, e, n);
+            f32x4_t s[VEC / 4];
+#pragma unroll
+            for (int i = 0; i < VEC / 4; ++i) s[i] = load_row<true>(p.state, at + 4 * i, max(0, min(4, n - 4 * i)));
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                const float a = decay<LOG>(Ln::get(g, i)), old = s[i / 4][i % 4];
+                const float now = fmaf(a, a == 0.0f ? 0.0f : old, Ln::get(k, i) * Ln::get(v, i));
+                s[i / 4][i % 4] = now;
+                y[i] = Ln::get(q, i) * now;
+            }
+#pragma unroll
+            for (int i = 0; i < VEC / 4; ++i) {
+                const float x[4] = {s[i][0], s[i][1], s[i][2], s[i][3]};
+                store_row<true>(p.state_out, at + 4 * i, x, max(0, min(4, n - 4 * i)));
+            }
+        }
+        store_row<F32>(p.y, b * p.D + d0, y, n);
     }
-    store1<F32>(p.y, i, y);
 }
 
-template <bool F32>
-__global__ __launch_bounds__(256) void conv_step_kernel(StepParams p) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= p.B * p.D) return;
-    const int64_t b = i / p.D, d = i % p.D, e = b * p.ld + d;
-    const int64_t slot = slot_of(p, b), pos = p.pos[b];
-    float y = 0.0f;
-    if (slot >= 0 && slot < p.S && pos >= 0) {
-        const int64_t f = d / p.group_size * p.l_h;
-        const float x = load1<F32>(p.k, e) * load1<F32>(p.v, e);
-        float acc = load1<F32>(p.h, f) * x;
-        for (int64_t s = 1; s < p.l_h && s <= pos; ++s)
-            acc += load1<F32>(p.h, f + s) * load1<F32>(p.cache, (slot * p.R + (pos - s) % p.R) * p.D + d);
-        store1<F32>(p.cache, (slot * p.R + pos % p.R) * p.D + d, x);
-        y = load1<F32>(p.q, e) * acc;
+// The convolution's token: 8 lanes take 128 bytes of channels, and the taps of
+// one sequence are cut between 8 W slices of such lanes (W waves), kTaps
+// consecutive taps each, all rows of the ring in flight at once; the slices'
+// sums meet by shuffles and, over the waves, in LDS.  Bound by the ring's rows
+// from memory (l_h - 1 of them a sequence), or by latency for few sequences.
+constexpr int kTaps = 4;
+
+template <bool F32, int W> __global__ __launch_bounds__(256) void conv_step_kernel(StepParams p) {
+    using Ln = Lane<F32>;
+    constexpr int VEC = Ln::VEC, ITEMS = 4 / W;
+    __shared__ float part[ITEMS][W][8 * VEC];
+    const int wave = threadIdx.x >> 6, item = wave / W, c8 = threadIdx.x & 7;
+    const int slice = (wave % W) * 8 + (threadIdx.x >> 3 & 7);
+    const int64_t d0 = (((int64_t)blockIdx.x * ITEMS + item) * 8 + c8) * VEC;
+    const int n = (int)min((int64_t)VEC, p.D - d0);
+    // channels of one group share their taps
+    const bool one = p.group_size % VEC == 0;
+    for (int64_t b = blockIdx.y; b < p.B; b += gridDim.y) {
+        const int64_t slot = slot_of(p, b), pos = p.pos[b];
+        const bool live = slot >= 0 && slot < p.S && pos >= 0;
+        float acc[VEC] = {}, x0[VEC] = {};
+        typename Ln::raw q = {};
+        if (live && n > 0) {
+            const int64_t now = remainder_of(pos, p.R);
+            const size_t ring = (size_t)slot * p.R * p.D + d0;
+            typename Ln::raw k = {}, v = {}, x[kTaps] = {};
+            if (slice == 0) {
+                const size_t e = b * p.ld + d0;
+                q = load_row<F32>(p.q, e, n), k = load_row<F32>(p.k, e, n), v = load_row<F32>(p.v, e, n);
+            }
+            const int first = slice * kTaps;
+            const int64_t most = min(p.l_h - 1, pos);  // the longest lag there is
+#pragma unroll
+            for (int i = 0; i < kTaps; ++i) {
+                const int s = first + i;
+                const int64_t row = now - s + (s > now ? p.R : 0);
+                if (s >= 1 && s <= most) x[i] = load_row<F32>(p.cache, ring + row * p.D, n);
+            }
+            float h[kTaps][VEC];
+#pragma unroll
+            for (int i = 0; i < kTaps; ++i) {
+                const bool in = first + i <= most;
+                const float h0 = in && one ? load1<F32>(p.h, quotient(d0, p.group_size) * p.l_h + first + i) : 0.0f;
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) {
+                    h[i][c] = h0;
+                    if (in && !one && c < n) h[i][c] = load1<F32>(p.h, quotient(d0 + c, p.group_size) * p.l_h + first + i);
+                }
+            }
+            if (slice == 0) {
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) x0[c] = Ln::get(k, c) * Ln::get(v, c);
+                store_row<F32>(p.cache, ring + now * p.D, x0, n);
+            }
+#pragma unroll
+            for (int i = 0; i < kTaps; ++i)
+#pragma unroll
+                for (int c = 0; c < VEC; ++c)
+                    if (first + i <= most) acc[c] = fmaf(h[i][c], first + i == 0 ? x0[c] : Ln::get(x[i], c), acc[c]);
+        }
+#pragma unroll
+        for (int c = 0; c < VEC; ++c)
+#pragma unroll
+            for (int o = 8; o < 64; o *= 2) acc[c] += __shfl_xor(acc[c], o);
+        if constexpr (W > 1) {
+            __syncthreads();  // the sums before are taken
+            if ((threadIdx.x & 63) < 8) {
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) part[item][wave % W][c8 * VEC + c] = acc[c];
+            }
+            __syncthreads();
+        }
+        if (slice == 0 && n > 0) {
+            float y[VEC];
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) {
+                float sum = acc[c];
+                if constexpr (W > 1) {
+#pragma unroll
+                    for (int w = 1; w < W; ++w) sum += part[item][w][c8 * VEC + c];
+                }
+                y[c] = live ? Ln::get(q, c) * sum : 0.0f;
+            }
+            store_row<F32>(p.y, b * p.D + d0, y, n);
+        }
     }
-    store1<F32>(p.y, i, y);
 }
 
-// One thread per channel of each of the R last rows.
-template <bool F32>
-__global__ __launch_bounds__(256) void cache_fill_kernel(StepParams p) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+// blockIdx.y counts the last rows of each prompt, blockIdx.z the sequences.
+template <bool F32> __global__ __launch_bounds__(kScanThreads) void cache_fill_kernel(StepParams p) {
+    using Ln = Lane<F32>;
+    constexpr int VEC = Ln::VEC;
+    const int64_t d0 = ((int64_t)blockIdx.x * kScanThreads + threadIdx.x) * VEC;
+    const int n = (int)min((int64_t)VEC, p.D - d0);
+    if (n <= 0) return;
     const int64_t rows = min(p.R, p.L);
-    if (i >= p.B * rows * p.D) return;
-    const int64_t d = i % p.D, r = i / p.D % rows, b = i / p.D / rows;
-    const int64_t slot = slot_of(p, b);
-    int64_t len = p.pos ? p.pos[b] : p.L;
-    len = len < 0 ? 0 : len > p.L ? p.L : len;
-    const int64_t t = len - 1 - r;
-    if (slot < 0 || slot >= p.S || t < 0) return;
-    const int64_t e = (b * p.L + t) * p.ld + d;
-    store1<F32>(p.cache, (slot * p.R + t % p.R) * p.D + d, load1<F32>(p.k, e) * load1<F32>(p.v, e));
+    for (int64_t b = blockIdx.z; b < p.B; b += gridDim.z) {
+        const int64_t slot = slot_of(p, b);
+        if (slot < 0 || slot >= p.S) continue;
+        int64_t len = p.pos ? p.pos[b] : p.L;
+        len = len < 0 ? 0 : len > p.L ? p.L : len;
+        for (int64_t r = blockIdx.y; r < rows && r < len; r += gridDim.y) {
+            const int64_t t = len - 1 - r;
+            const size_t e = (size_t)(b * p.L + t) * p.ld + d0;
+            const auto k = load_row<F32>(p.k, e, n), v = load_row<F32>(p.v, e, n);
+            float x[VEC];
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) x[c] = Ln::get(k, c) * Ln::get(v, c);
+            store_row<F32>(p.cache, ((size_t)slot * p.R + remainder_of(t, p.R)) * p.D + d0, x, n);
+        }
+    }
 }
 
-template <typename K> int launch(K kernel, const StepParams &p, int64_t threads, void *stream) {
-    const int64_t blocks = ceil_div(threads, 256);
-    if (blocks > 0x7fffffff) return HYENA_ERR_UNSUPPORTED;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(256), 0, (hipStream_t)stream, p);
+unsigned at_most(int64_t n, int64_t most) { return (unsigned)(n < most ? n : most); }
+
+template <typename K> int launch(K kernel, const StepParams &p, dim3 grid, int threads, void *stream) {
+    hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, (hipStream_t)stream, p);
     return launch_status();
 }
+
+// Blocks of `lanes` lanes over a row's channels.
+int64_t row_blocks(int64_t D, bool f32, int64_t lanes) { return ceil_div(ceil_div(D, f32 ? 4 : 8), lanes); }
 
 int check_dtype(int dtype) {
     return dtype == HYENA_DTYPE_BF16 || dtype == HYENA_DTYPE_F32 ? HYENA_OK : HYENA_ERR_DTYPE;
@@ -114,8 +233,11 @@ int hyena_scan_step(const void *q, const void *k, const void *v, const void *g, 
     p.q = q, p.k = k, p.v = v, p.g = g, p.state = state, p.state_out = state_out, p.slots = slots, p.y = y;
     p.B = B, p.D = D, p.ld = ld, p.S = S;
     const bool f32 = dtype == HYENA_DTYPE_F32, lg = gate == HYENA_GATE_LOG;
+    const int64_t x = row_blocks(D, f32, kScanThreads);
+    if (x > 0x7fffffff) return HYENA_ERR_UNSUPPORTED;
     return launch(f32 ? (lg ? scan_step_kernel<true, true> : scan_step_kernel<true, false>)
-                      : (lg ? scan_step_kernel<false, true> : scan_step_kernel<false, false>), p, B * D, stream);
+                      : (lg ? scan_step_kernel<false, true> : scan_step_kernel<false, false>),
+                  p, dim3((unsigned)x, at_most(B, 65535)), kScanThreads, stream);
 }
 
 int hyena_conv_step(const void *q, const void *k, const void *v, const void *h, int64_t B, int64_t D, int64_t ld,
@@ -144,7 +266,12 @@ int hyena_conv_step(const void *q, const void *k, const void *v, const void *h, 
     StepParams p = {};
     p.q = q, p.k = k, p.v = v, p.h = h, p.cache = cache, p.pos = pos, p.slots = slots, p.y = y;
     p.B = B, p.D = D, p.ld = ld, p.S = S, p.R = R, p.group_size = group_size, p.l_h = l_h;
-    return launch(dtype == HYENA_DTYPE_F32 ? conv_step_kernel<true> : conv_step_kernel<false>, p, B * D, stream);
+    const bool f32 = dtype == HYENA_DTYPE_F32, few = l_h <= 8 * kTaps;  // taps that one wave's slices take
+    const int64_t x = row_blocks(D, f32, few ? 32 : 8);
+    if (x > 0x7fffffff) return HYENA_ERR_UNSUPPORTED;
+    return launch(f32 ? (few ? conv_step_kernel<true, 1> : conv_step_kernel<true, 4>)
+                      : (few ? conv_step_kernel<false, 1> : conv_step_kernel<false, 4>),
+                  p, dim3((unsigned)x, at_most(B, 65535)), 256, stream);
 }
 
 int hyena_conv_cache_fill(const void *k, const void *v, int64_t B, int64_t L, int64_t D, int64_t ld, void *cache,
@@ -168,8 +295,11 @@ int hyena_conv_cache_fill(const void *k, const void *v, int64_t B, int64_t L, in
     StepParams p = {};
     p.k = k, p.v = v, p.cache = cache, p.pos = lens, p.slots = slots;
     p.B = B, p.L = L, p.D = D, p.ld = ld, p.S = S, p.R = R;
-    return launch(dtype == HYENA_DTYPE_F32 ? cache_fill_kernel<true> : cache_fill_kernel<false>, p,
-                  B * (R < L ? R : L) * D, stream);
+    const bool f32 = dtype == HYENA_DTYPE_F32;
+    const int64_t x = row_blocks(D, f32, kScanThreads);
+    if (x > 0x7fffffff) return HYENA_ERR_UNSUPPORTED;
+    return launch(f32 ? cache_fill_kernel<true> : cache_fill_kernel<false>, p,
+                  dim3((unsigned)x, at_most(R < L ? R : L, 65535), at_most(B, 65535)), kScanThreads, stream);
 }
 
 const char *hyena_layer_strerror(int status) {

@@ -99,7 +99,7 @@ def _row_stride(t: torch.Tensor, name: str) -> Optional[int]:
     if shape[-1] > 1 and stride[-1] != 1:
         raise ValueError("%s must have contiguous rows" % name)
     ld, rows = None, 1
-    for n, s in zip(reversed(shape[:-1]), reversed(stride[:-1])):
+    for n, s in zip(shape[-2::-1], stride[-2::-1]):
         if n == 0:
             return None
         if n == 1:
@@ -115,18 +115,17 @@ def _row_stride(t: torch.Tensor, name: str) -> Optional[int]:
 
 
 def _shared_stride(ts, names, n: int) -> int:
-    """The row stride that all of ts share (n where none has a second row)."""
-    ld = None
-    for t, name in zip(ts, names):
-        s = _row_stride(t, name)
-        if s is not None and ld is not None and s != ld:
-            raise ValueError("%s must have one row stride, got %d and %d" % (", ".join(names), ld, s))
-        ld = s if ld is None else ld
+    """The row stride that all of ts, of one shape, share (n where none has a second row)."""
+    ld = _row_stride(ts[0], names[0])
+    first = ts[0].stride()
+    for t, name in zip(ts[1:], names[1:]):
+        if t.stride() != first and _row_stride(t, name) != ld:
+            raise ValueError("%s must have one row stride" % ", ".join(names))
     return n if ld is None else ld
 
 
 def _like(t: torch.Tensor, name: str, shape, dtype, dev) -> None:
-    if t.shape != shape or t.dtype != dtype or t.device != dev:
+    if t.shape != shape or t.dtype is not dtype or t.device != dev:
         raise ValueError("%s must be %s %s on %s" % (name, tuple(shape), dtype, dev))
 
 
@@ -143,12 +142,10 @@ def _ptr(t: Optional[torch.Tensor]):
 
 def _call(name: str, dev: torch.device, stream, *args) -> None:
     """name(*args, stream) on dev; raises LayerError for a status other than HYENA_OK."""
-    if stream is None:
-        handle = torch.cuda.current_stream(dev).cuda_stream
-    else:
-        handle = stream.cuda_stream
-    fn = getattr(layer_lib(), name)
-    if dev.index == torch.cuda.current_device():
+    fn = getattr(_lib or layer_lib(), name)
+    # the current stream's handle, without the Stream object torch.cuda.current_stream makes
+    handle = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+    if dev.index == torch._C._cuda_getDevice():
         st = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
