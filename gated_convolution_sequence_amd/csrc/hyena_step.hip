@@ -73,65 +73,105 @@ __global__ __launch_bounds__(kScanThreads) void scan_step_kernel(StepParams p) {
     }
 }
 
-// The convolution's token: 8 lanes take 128 bytes of channels, and the taps of
-// one sequence are cut between 8 W slices of such lanes (W waves), kTaps
-// consecutive taps each, all rows of the ring in flight at once; the slices'
-// sums meet by shuffles and, over the waves, in LDS.  Bound by the ring's rows
-// from memory (l_h - 1 of them a sequence), or by latency for few sequences.
-constexpr int kTaps = 4;
+// N consecutive taps from element e on, `left` of them in the filter (the rest
+// zero).
+template <bool F32, int N> __device__ inline void load_taps(const void *h, size_t e, int left, float (&x)[N]) {
+    if (left >= N) {
+        constexpr int WORDS = F32 ? N : N / 2;
+        typedef u32x2_t pair_any __attribute__((aligned(2)));
+        u32x2_t r[WORDS / 2];
+#pragma unroll
+        for (int i = 0; i < WORDS / 2; ++i) r[i] = ((const pair_any *)((const char *)h + e * (F32 ? 4 : 2)))[i];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if constexpr (F32) x[i] = __uint_as_float(r[i / 2][i % 2]);
+            else x[i] = i & 1 ? bf_hi(r[i / 4][i / 2 % 2]) : bf_lo(r[i / 4][i / 2 % 2]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = i < left ? load1<F32>(h, e + i) : 0.0f;
+    }
+}
 
-template <bool F32, int W> __global__ __launch_bounds__(256) void conv_step_kernel(StepParams p) {
+// The convolution's token: 8 lanes take 128 bytes of channels, and the taps of
+// one sequence are cut between 8 W slices of such lanes (W waves), TAPS
+// consecutive taps each, all their rows of the ring in flight at once; the
+// slices' sums meet by shuffles and, over the waves, in LDS.  Bound by the
+// ring's rows from memory (l_h - 1 of them a sequence), or by latency for few
+// sequences.  ONE: a lane's channels share a filter.
+template <bool F32, int W, int TAPS, bool ONE> __global__ __launch_bounds__(256) void conv_step_kernel(StepParams p) {
     using Ln = Lane<F32>;
-    constexpr int VEC = Ln::VEC, ITEMS = 4 / W;
+    constexpr int VEC = Ln::VEC, EB = F32 ? 4 : 2, ITEMS = 4 / W;
     __shared__ float part[ITEMS][W][8 * VEC];
     const int wave = threadIdx.x >> 6, item = wave / W, c8 = threadIdx.x & 7;
     const int slice = (wave % W) * 8 + (threadIdx.x >> 3 & 7);
+    const int first = slice * TAPS;
     const int64_t d0 = (((int64_t)blockIdx.x * ITEMS + item) * 8 + c8) * VEC;
     const int n = (int)min((int64_t)VEC, p.D - d0);
-    // channels of one group share their taps
-    const bool one = p.group_size % VEC == 0;
     for (int64_t b = blockIdx.y; b < p.B; b += gridDim.y) {
-        const int64_t slot = slot_of(p, b), pos = p.pos[b];
-        const bool live = slot >= 0 && slot < p.S && pos >= 0;
+        const int slot = __builtin_amdgcn_readfirstlane(slot_of(p, b) < p.S ? (int)slot_of(p, b) : -1);
+        const int64_t pos = p.pos[b];
+        const bool live = slot >= 0 && pos >= 0;
         float acc[VEC] = {}, x0[VEC] = {};
         typename Ln::raw q = {};
         if (live && n > 0) {
-            const int64_t now = remainder_of(pos, p.R);
-            const size_t ring = (size_t)slot * p.R * p.D + d0;
-            typename Ln::raw k = {}, v = {}, x[kTaps] = {};
+            const int now = (int)remainder_of(pos, p.R);           // R D elements of a ring are below 2^31 bytes
+            const int most = (int)min(p.l_h - 1, pos);             // the longest lag there is
+            const size_t ring = (size_t)slot * p.R * p.D;
+            const uint32_t pitch = (uint32_t)p.D * EB;
+            typename Ln::raw k = {}, v = {}, x[TAPS] = {};
             if (slice == 0) {
                 const size_t e = b * p.ld + d0;
                 q = load_row<F32>(p.q, e, n), k = load_row<F32>(p.k, e, n), v = load_row<F32>(p.v, e, n);
             }
-            const int first = slice * kTaps;
-            const int64_t most = min(p.l_h - 1, pos);  // the longest lag there is
+            if (n == VEC) {
+                // lags there are none of read past the ring's range: zero
+                const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+                    (char *)p.cache + ring * EB, (short)0, (int)((uint32_t)p.R * pitch), 0x00020000);
 #pragma unroll
-            for (int i = 0; i < kTaps; ++i) {
-                const int s = first + i;
-                const int64_t row = now - s + (s > now ? p.R : 0);
-                if (s >= 1 && s <= most) x[i] = load_row<F32>(p.cache, ring + row * p.D, n);
-            }
-            float h[kTaps][VEC];
+                for (int i = 0; i < TAPS; ++i) {
+                    const int s = first + i, row = now - s + (s > now ? (int)p.R : 0);
+                    const uint32_t off = s >= 1 && s <= most ? row * pitch + (uint32_t)d0 * EB : 0x80000000u;
+                    x[i] = __builtin_bit_cast(typename Ln::raw, __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 2));
+                }
+            } else {
 #pragma unroll
-            for (int i = 0; i < kTaps; ++i) {
-                const bool in = first + i <= most;
-                const float h0 = in && one ? load1<F32>(p.h, quotient(d0, p.group_size) * p.l_h + first + i) : 0.0f;
-#pragma unroll
-                for (int c = 0; c < VEC; ++c) {
-                    h[i][c] = h0;
-                    if (in && !one && c < n) h[i][c] = load1<F32>(p.h, quotient(d0 + c, p.group_size) * p.l_h + first + i);
+                for (int i = 0; i < TAPS; ++i) {
+                    const int s = first + i, row = now - s + (s > now ? (int)p.R : 0);
+                    if (s >= 1 && s <= most) x[i] = Ln::load_part(p.cache, ring + (size_t)row * p.D + d0, n);
                 }
             }
             if (slice == 0) {
 #pragma unroll
                 for (int c = 0; c < VEC; ++c) x0[c] = Ln::get(k, c) * Ln::get(v, c);
-                store_row<F32>(p.cache, ring + now * p.D, x0, n);
+                store_row<F32>(p.cache, ring + (size_t)now * p.D + d0, x0, n);
             }
+            // (a tap past the last lag may be anything: its x does not count)
+            auto add = [&](int i, int c, float tap) {
+                const float xi = i == 0 && first == 0 ? x0[c] : Ln::get(x[i], c);
+                if (first + i <= most) acc[c] = fmaf(tap, xi, acc[c]);
+            };
+            float h[TAPS];
+            // the scheduling barriers keep one tap's (channel's) values in
+            // registers at a time, not all of them
+            if constexpr (ONE) {
+                load_taps<F32, TAPS>(p.h, quotient(d0, p.group_size) * p.l_h + first, (int)p.l_h - first, h);
 #pragma unroll
-            for (int i = 0; i < kTaps; ++i)
+                for (int i = 0; i < TAPS; ++i) {
+                    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int c = 0; c < VEC; ++c)
-                    if (first + i <= most) acc[c] = fmaf(h[i][c], first + i == 0 ? x0[c] : Ln::get(x[i], c), acc[c]);
+                    for (int c = 0; c < VEC; ++c) add(i, c, h[i]);
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    if (c < n)
+                        load_taps<F32, TAPS>(p.h, quotient(d0 + c, p.group_size) * p.l_h + first, (int)p.l_h - first, h);
+#pragma unroll
+                    for (int i = 0; i < TAPS; ++i) add(i, c, h[i]);
+                }
+            }
         }
 #pragma unroll
         for (int c = 0; c < VEC; ++c)
@@ -253,6 +293,8 @@ int hyena_conv_step(const void *q, const void *k, const void *v, const void *h, 
     if (R < l_h || !mul_fits(S, R, 1, &n) || !mul_fits(n, D, eb, &n)) return HYENA_ERR_SHAPE;
     if (!slots && S < B) return HYENA_ERR_SHAPE;
     if (B == 0 || D == 0) return HYENA_OK;
+    // offsets in a ring are 31 bits, rings are counted in 32
+    if (R * D * eb > 0x7fffffff || S > 0x7fffffff) return HYENA_ERR_UNSUPPORTED;
     if (!q || !k || !v || !h || !y || !pos || (!cache && S > 0)) return HYENA_ERR_NULL;
     if (!aligned(q, eb) || !aligned(k, eb) || !aligned(v, eb) || !aligned(h, eb) || !aligned(y, eb) ||
         !aligned(cache, eb) || !aligned(pos, 8) || !aligned(slots, 4))
@@ -266,12 +308,23 @@ int hyena_conv_step(const void *q, const void *k, const void *v, const void *h, 
     StepParams p = {};
     p.q = q, p.k = k, p.v = v, p.h = h, p.cache = cache, p.pos = pos, p.slots = slots, p.y = y;
     p.B = B, p.D = D, p.ld = ld, p.S = S, p.R = R, p.group_size = group_size, p.l_h = l_h;
-    const bool f32 = dtype == HYENA_DTYPE_F32, few = l_h <= 8 * kTaps;  // taps that one wave's slices take
-    const int64_t x = row_blocks(D, f32, few ? 32 : 8);
+    // The cut of the taps.  Filters of up to 32 taps: one wave, 4 taps a lane.
+    // Few sequences: as many lanes as there can be (B = 1, l_h = 128, D = 4096
+    // bf16, one filter for 16 channels: 6 us).  Once that is more waves than the
+    // card holds, 16 taps a lane (B = 64: 15.5 us against 19.0 with 4 and 17.7
+    // with 8); 8 where a lane's channels have filters of their own, whose taps
+    // take registers too (27.5 us against 33.1 with 16).
+    const bool f32 = dtype == HYENA_DTYPE_F32, single = l_h <= 32;
+    const bool one = group_size % (f32 ? 4 : 8) == 0;
+    const bool many = !single && ceil_div(D, f32 ? 32 : 64) * B > 1024;
+    const int64_t x = row_blocks(D, f32, single || (many && one) ? 32 : many ? 16 : 8);
     if (x > 0x7fffffff) return HYENA_ERR_UNSUPPORTED;
-    return launch(f32 ? (few ? conv_step_kernel<true, 1> : conv_step_kernel<true, 4>)
-                      : (few ? conv_step_kernel<false, 1> : conv_step_kernel<false, 4>),
-                  p, dim3((unsigned)x, at_most(B, 65535)), 256, stream);
+    const dim3 grid((unsigned)x, at_most(B, 65535));
+#define CONV_STEP(W, TAPS, ONE) \
+    launch(f32 ? conv_step_kernel<true, W, TAPS, ONE> : conv_step_kernel<false, W, TAPS, ONE>, p, grid, 256, stream)
+    if (one) return single ? CONV_STEP(1, 4, true) : many ? CONV_STEP(1, 16, true) : CONV_STEP(4, 4, true);
+    return single ? CONV_STEP(1, 4, false) : many ? CONV_STEP(2, 8, false) : CONV_STEP(4, 4, false);
+#undef CONV_STEP
 }
 
 int hyena_conv_cache_fill(const void *k, const void *v, int64_t B, int64_t L, int64_t D, int64_t ld, void *cache,
@@ -311,7 +364,7 @@ const char *hyena_layer_strerror(int status) {
     case HYENA_ERR_FILTER_LEN: return "l_h must be in [1, 128]";
     case HYENA_ERR_ALIGN: return "a pointer is not aligned to its elements (workspaces: 16 bytes)";
     case HYENA_ERR_ALIAS: return "an output overlaps an input or another output";
-    case HYENA_ERR_UNSUPPORTED: return "unknown gate or activation code, or a grid too large to launch";
+    case HYENA_ERR_UNSUPPORTED: return "unknown gate or activation code, a ring of 2 GiB or more, or a grid too large to launch";
     case HYENA_ERR_LAUNCH: return "kernel launch failed";
     case HYENA_ERR_DTYPE: return "unknown dtype code";
     case HYENA_ERR_WORKSPACE: return "workspace missing or smaller than the operator's workspace call reports";

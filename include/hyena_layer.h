@@ -109,7 +109,8 @@ int hyena_scan_step(const void *q, const void *k, const void *v, const void *g,
  * [B, D] with row stride ld; h is [D / group_size, l_h], l_h <= 128; y [B, D]
  * contiguous.  A slot outside [0, S) or pos < 0 marks an inactive entry: its
  * y row is zero and its ring is left alone.  slots NULL: ring b, S >= B.
- * Active slots must differ.  x_pos itself enters the sum in fp32. */
+ * Active slots must differ.  x_pos itself enters the sum in fp32.  A ring must
+ * be below 2 GiB (else HYENA_ERR_UNSUPPORTED). */
 int hyena_conv_step(const void *q, const void *k, const void *v, const void *h,
                     int64_t B, int64_t D, int64_t ld, int64_t group_size,
                     int64_t l_h, void *cache, int64_t S, int64_t R,
