@@ -12,6 +12,7 @@ conv_step, conv_cache_fill      the gated convolution for one token at a time
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Sequence
 
@@ -129,6 +130,20 @@ def _like(t: torch.Tensor, name: str, shape, dtype, dev) -> None:
         raise ValueError("%s must be %s %s on %s" % (name, tuple(shape), dtype, dev))
 
 
+def _rows_like(ts, names, shape, dtype, dev) -> int:
+    """The one row stride of ts, which must all be ``shape``, ``dtype`` and on ``dev``."""
+    first = ts[0].stride()
+    for t in ts:
+        if t.shape != shape or t.dtype is not dtype or t.device != dev or t.stride() != first:
+            break
+    else:  # alike, as they nearly always are
+        if len(shape) == 2 and first[1] == 1 and first[0] >= shape[1]:
+            return first[0] if shape[0] > 1 else shape[1]
+    for t, name in zip(ts, names):
+        _like(t, name, shape, dtype, dev)
+    return _shared_stride(ts, names, shape[-1])
+
+
 def _contiguous(t: Optional[torch.Tensor], name: str, shape, dtype, dev) -> None:
     if t is not None:
         _like(t, name, shape, dtype, dev)
@@ -168,6 +183,7 @@ def _ws_args(ws: Optional[torch.Tensor]):
 
 # ---- gated linear recurrence ------------------------------------------------------
 
+@functools.lru_cache(maxsize=1024)
 def scan_workspace_bytes(B: int, L: int, D: int, dtype: int = 0) -> int:
     """Workspace bytes scan_fwd and scan_bwd need."""
     n = ctypes.c_int64()
@@ -182,9 +198,7 @@ def _scan_inputs(ts, names):
     code = _code(q)
     if q.dim() != 3:
         raise ValueError("q, k, v, g must be [B, L, D]")
-    for t, name in zip(ts, names):
-        _like(t, name, q.shape, q.dtype, q.device)
-    return code, _shared_stride(ts, names, q.shape[2])
+    return code, _rows_like(ts, names, q.shape, q.dtype, q.device)
 
 
 def scan_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, gate: str = "sigmoid",
@@ -243,9 +257,7 @@ def scan_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
         names = ("dq", "dk", "dv", "dg")
         if len(grads) != 4:
             raise ValueError("grads must be the four tensors dq, dk, dv, dg")
-        for t, name in zip(grads, names):
-            _like(t, name, q.shape, q.dtype, dev)
-        ldd = _shared_stride(grads, names, D)
+        ldd = _rows_like(grads, names, q.shape, q.dtype, dev)
     ds0 = torch.empty((B, D), dtype=torch.float32, device=dev)
     ws = _workspace(scan_workspace_bytes(B, L, D, code), workspace, dev)
     _call("hyena_scan_bwd", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), dy.data_ptr(),
@@ -270,10 +282,7 @@ def scan_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor
     if q.dim() != 2 or state.dim() != 2:
         raise ValueError("q, k, v, g must be [B, D] and state [S, D]")
     B, D = q.shape
-    ts, names = (q, k, v, g), ("q", "k", "v", "g")
-    for t, name in zip(ts, names):
-        _like(t, name, q.shape, q.dtype, dev)
-    ld = _shared_stride(ts, names, D)
+    ld = _rows_like((q, k, v, g), ("q", "k", "v", "g"), q.shape, q.dtype, dev)
     S = state.shape[0]
     _contiguous(state, "state", (S, D), torch.float32, dev)
     _contiguous(state_out, "state_out", (S, D), torch.float32, dev)
@@ -303,8 +312,8 @@ class GatedScan(torch.autograd.Function):
         need = ctx.needs_input_grad
         dq, dk, dv, dg, ds0 = scan_bwd(q, k, v, g, dy.contiguous(), states, gate=ctx.gate,
                                        ds_last=ds_last.contiguous())
-        return (dq if need[0] else None, dk if need[1] else None, dv if need[2] else None, dg if need[3] else None,
-                None, ds0 if need[5] else None)
+        grads = (dq, dk, dv, dg, None, ds0)
+        return tuple(t if n else None for t, n in zip(grads, need))  # as many as apply was given
 
 
 # ---- the gated convolution, one token at a time --------------------------------------
@@ -331,10 +340,7 @@ def conv_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, h: torch.Tensor
     if q.dim() != 2 or h.dim() != 2:
         raise ValueError("q, k, v must be [B, D]; h [D // group_size, l_h]")
     B, D = q.shape
-    ts, names = (q, k, v), ("q", "k", "v")
-    for t, name in zip(ts, names):
-        _like(t, name, q.shape, q.dtype, dev)
-    ld = _shared_stride(ts, names, D)
+    ld = _rows_like((q, k, v), ("q", "k", "v"), q.shape, q.dtype, dev)
     G, l_h = h.shape
     if group_size < 1 or D % group_size != 0 or G != D // group_size:
         raise ValueError("h has %d filters; D=%d, group_size=%d" % (G, D, group_size))
@@ -363,8 +369,7 @@ def conv_cache_fill(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, lens:
     if k.dim() != 3:
         raise ValueError("k, v must be [B, L, D]")
     B, L, D = k.shape
-    _like(v, "v", k.shape, k.dtype, dev)
-    ld = _shared_stride((k, v), ("k", "v"), D)
+    ld = _rows_like((k, v), ("k", "v"), k.shape, k.dtype, dev)
     S, R = _cache_sizes(cache, D, k.dtype, dev)
     _contiguous(lens, "lens", (B,), torch.int64, dev)
     _contiguous(slots, "slots", (B,), torch.int32, dev)
@@ -374,6 +379,7 @@ def conv_cache_fill(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, lens:
 
 # ---- matrix product with an epilogue --------------------------------------------------
 
+@functools.lru_cache(maxsize=1024)
 def linear_workspace_bytes(M: int, N: int, K: int, act: str = "none", dtype: int = 0, backward: bool = False) -> int:
     """Workspace bytes linear_fwd (or linear_bwd) needs."""
     n = ctypes.c_int64()
@@ -488,5 +494,6 @@ class LinearAct(torch.autograd.Function):
         x, w, z = ctx.saved_tensors
         need = ctx.needs_input_grad
         dx, dw, db = linear_bwd(x, w, dy.contiguous(), preact=z, act=ctx.act, need_dx=need[0], need_dw=need[1],
-                                need_db=need[2])
-        return dx, dw, db, dy if need[3] else None, None
+                                need_db=len(need) > 2 and need[2])
+        grads = (dx, dw, db, dy, None)
+        return tuple(t if n else None for t, n in zip(grads, need))  # as many as apply was given
