@@ -616,9 +616,8 @@ template <bool F32> __global__ __launch_bounds__(256) void finish_kernel(FinishP
 // For a few rows of x the weights stream through once and bound the time.  A
 // workgroup owns 16 rows of w (16 columns of y) and MT x 16 rows of x; its
 // waves cut c between them, and each loads its fragments of w and x straight
-// from memory into the matrix cores' layout: lane (i, j) takes 32 bytes of row i
-// at 128-byte steps, two chunks which serve two products (c is permuted alike
-// for x and w).  The waves' sums meet in LDS.
+// from memory into the matrix cores' layout: lane (i, j) takes two 16-byte chunks
+// of row i at 128-byte steps, one of each 64 bytes, which serve two products.  The waves' sums meet in LDS.
 struct RowsParams {
     const void *x, *w;
     int64_t ldx;
@@ -627,7 +626,7 @@ struct RowsParams {
 };
 
 constexpr int kRowWaves = 8;
-constexpr int kRowSteps = 4;  // steps of c in flight a wave
+constexpr int kRowSteps = 2;  // steps of c in flight a wave
 
 template <bool F32, int MT>
 __global__ __launch_bounds__(64 * kRowWaves) void rows_kernel(RowsParams p) {
@@ -638,10 +637,10 @@ __global__ __launch_bounds__(64 * kRowWaves) void rows_kernel(RowsParams p) {
     __shared__ __attribute__((aligned(16))) float sums[kRowWaves][MT][16][16];
     const int wave = threadIdx.x >> 6, i = threadIdx.x & 15, j = (threadIdx.x >> 4) & 3;
     const int n0 = blockIdx.x * 16;
-    const T *w = (const T *)p.w + (int64_t)(n0 + i) * p.K + j * 2 * CE;
+    const T *w = (const T *)p.w + (int64_t)(n0 + i) * p.K + j * CE;
     const T *x[MT];
 #pragma unroll
-    for (int t = 0; t < MT; ++t) x[t] = (const T *)p.x + (int64_t)(t * 16 + i) * p.ldx + j * 2 * CE;
+    for (int t = 0; t < MT; ++t) x[t] = (const T *)p.x + (int64_t)(t * 16 + i) * p.ldx + j * CE;
 
     f32x4_t acc[MT] = {};
     auto multiply = [&](const u32x4_t (&fw)[kRowSteps][2], const u32x4_t (&fx)[MT][kRowSteps][2]) {
@@ -663,7 +662,7 @@ __global__ __launch_bounds__(64 * kRowWaves) void rows_kernel(RowsParams p) {
             for (int s = 0; s < kRowSteps; ++s)
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    fw[s][h] = __builtin_nontemporal_load((const typename E::chunk_any *)(w + c + s * BK + h * CE));
+                    fw[s][h] = __builtin_nontemporal_load((const typename E::chunk_any *)(w + c + s * BK + h * 4 * CE));
         }
 #pragma unroll
         for (int t = 0; t < MT; ++t)
@@ -671,14 +670,14 @@ __global__ __launch_bounds__(64 * kRowWaves) void rows_kernel(RowsParams p) {
 #pragma unroll
                 for (int s = 0; s < kRowSteps; ++s)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) fx[t][s][h] = *(const typename E::chunk_any *)(x[t] + c + s * BK + h * CE);
+                    for (int h = 0; h < 2; ++h) fx[t][s][h] = *(const typename E::chunk_any *)(x[t] + c + s * BK + h * 4 * CE);
             }
         multiply(fw, fx);
     }
     if (c < p.K) {  // the last span, cut short
         u32x4_t fw[kRowSteps][2] = {}, fx[MT][kRowSteps][2] = {};
         auto edge = [&](const T *row, int at) {
-            const int left = p.K - at - j * 2 * CE;
+            const int left = p.K - at - j * CE;
             if (left >= CE) return (u32x4_t)*(const typename E::chunk_any *)(row + at);
             T v[CE];
 #pragma unroll
@@ -689,7 +688,7 @@ __global__ __launch_bounds__(64 * kRowWaves) void rows_kernel(RowsParams p) {
         for (int s = 0; s < kRowSteps; ++s)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int at = c + s * BK + h * CE;
+                const int at = c + s * BK + h * 4 * CE;
                 if (n0 + i < p.N) fw[s][h] = edge(w, at);
 #pragma unroll
                 for (int t = 0; t < MT; ++t)

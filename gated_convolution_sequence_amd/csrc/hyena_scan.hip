@@ -170,13 +170,20 @@ template <typename G> struct Place {
     }
 };
 
+// Rows past the end: a gate of exactly 1 and products of 0, so that they pass
+// the state on unchanged.
+template <bool F32, bool LOG> __device__ inline typename Lane<F32>::raw open_gate() {
+    constexpr uint32_t one = LOG ? 0u : F32 ? 0x7f800000u : 0x7f807f80u;  // exp(0) or sigmoid(+inf)
+    return __builtin_bit_cast(typename Lane<F32>::raw, u32x4_t{one, one, one, one});
+}
+
 // s -> a s + x; RESETS: where a may be 0 and must drop s.
 template <bool RESETS> __device__ inline float walk(float a, float x, float s) {
     if constexpr (RESETS) return apply(a, x, s);
     else return fmaf(a, s, x);
 }
 
-template <bool F32, bool LOG>
+template <bool F32, bool LOG, bool PART>
 __global__ __launch_bounds__(FwdTile<F32>::NT, 2) void scan_fwd_kernel(ScanParams p) {
     using G = FwdTile<F32>;
     using Ln = Lane<F32>;
@@ -202,7 +209,7 @@ __global__ __launch_bounds__(FwdTile<F32>::NT, 2) void scan_fwd_kernel(ScanParam
                 k[r] = Ln::load(p.k, e);
                 v[r] = Ln::load(p.v, e);
             }
-        } else if (at.n_ch > 0) {
+        } else if (PART && at.n_ch > 0) {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 const size_t e = at.row(p, r) * p.ld + at.d0;
@@ -231,7 +238,7 @@ __global__ __launch_bounds__(FwdTile<F32>::NT, 2) void scan_fwd_kernel(ScanParam
     if (p.y && at.n_ch == VEC) {
 #pragma unroll
         for (int r = 0; r < R; ++r) q[r] = Ln::load(p.q, at.row(p, r) * p.ld + at.d0);
-    } else if (p.y && at.n_ch > 0) {
+    } else if (PART && p.y && at.n_ch > 0) {
 #pragma unroll
         for (int r = 0; r < R; ++r) q[r] = Ln::load_part(p.q, at.row(p, r) * p.ld + at.d0, at.n_ch);
     }
@@ -303,7 +310,7 @@ __global__ __launch_bounds__(FwdTile<F32>::NT, 2) void scan_fwd_kernel(ScanParam
         float *to = p.states + (at.b * chunks + at.t0 / kStateRows) * p.D + at.d0;
 #pragma unroll
         for (int i = 0; i < VEC; ++i)
-            if (i < at.n_ch) to[i] = s[i];
+            if (!PART || i < at.n_ch) to[i] = s[i];
     }
     if (!p.y) return;
     auto outputs = [&](auto sel) {
@@ -317,8 +324,8 @@ __global__ __launch_bounds__(FwdTile<F32>::NT, 2) void scan_fwd_kernel(ScanParam
                 y[i] = Ln::get(q[r], i) * s[i];
             }
             if (at.t0 + r >= p.L) continue;
-            if (at.n_ch == VEC) Ln::store(p.y, first + (size_t)r * p.D, y);
-            else store_part<F32>(p.y, first + (size_t)r * p.D, y, at.n_ch);
+            if (!PART || at.n_ch == VEC) Ln::store(p.y, first + (size_t)r * p.D, Ln::pack(y));
+            else Ln::store_part(p.y, first + (size_t)r * p.D, Ln::pack(y), at.n_ch);
         }
     };
     if (resets) outputs(std::true_type());
@@ -328,8 +335,8 @@ __global__ __launch_bounds__(FwdTile<F32>::NT, 2) void scan_fwd_kernel(ScanParam
 // The backward walks chains from the end of time: c -> a (q dy + c) maps the
 // gradient of a row's state to that of the row before, with the same decays.
 // The states inside a tile are walked again from the saved state at its start.
-template <bool F32, bool LOG>
-__global__ __launch_bounds__(BwdTile<F32>::NT, 2) void scan_bwd_kernel(ScanParams p) {
+template <bool F32, bool LOG, bool PART>
+__global__ __launch_bounds__(BwdTile<F32>::NT, PART ? 2 : 3) void scan_bwd_kernel(ScanParams p) {
     using G = BwdTile<F32>;
     using Ln = Lane<F32>;
     constexpr int VEC = G::VEC, R = G::R, NS = G::NS, C = G::C;
@@ -343,71 +350,52 @@ __global__ __launch_bounds__(BwdTile<F32>::NT, 2) void scan_bwd_kernel(ScanParam
     const int64_t n = p.n_tiles - 1 - at.m;  // the tile, counted in time
     const int lane = threadIdx.x % G::LANES, slice = threadIdx.x / G::LANES;
 
+    // The inputs stay as they were loaded, and each channel's decays are
+    // computed where they are wanted: twice, for a third of the registers.
     typename Ln::raw g[R] = {}, k[R] = {}, v[R] = {}, q[R] = {}, dy[R] = {};
-    float a[R][VEC];
-    {
-        if (at.n_ch == VEC) {
+    if (at.n_ch == VEC) {
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const size_t row = at.row(p, r), e = row * p.ld + at.d0;
-                g[r] = Ln::load(p.g, e);
-                k[r] = Ln::load(p.k, e);
-                v[r] = Ln::load(p.v, e);
-                q[r] = Ln::load(p.q, e);
-                dy[r] = Ln::load(p.dy, row * p.D + at.d0);
-            }
-        } else if (at.n_ch > 0) {
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const size_t row = at.row(p, r), e = row * p.ld + at.d0;
-                g[r] = Ln::load_part(p.g, e, at.n_ch);
-                k[r] = Ln::load_part(p.k, e, at.n_ch);
-                v[r] = Ln::load_part(p.v, e, at.n_ch);
-                q[r] = Ln::load_part(p.q, e, at.n_ch);
-                dy[r] = Ln::load_part(p.dy, row * p.D + at.d0, at.n_ch);
-            }
+        for (int r = 0; r < R; ++r) {
+            const size_t row = at.row(p, r), e = row * p.ld + at.d0;
+            g[r] = Ln::load(p.g, e);
+            k[r] = Ln::load(p.k, e);
+            v[r] = Ln::load(p.v, e);
+            q[r] = Ln::load(p.q, e);
+            dy[r] = Ln::load(p.dy, row * p.D + at.d0);
         }
+    } else if (PART && at.n_ch > 0) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const size_t row = at.row(p, r), e = row * p.ld + at.d0;
+            g[r] = Ln::load_part(p.g, e, at.n_ch);
+            k[r] = Ln::load_part(p.k, e, at.n_ch);
+            v[r] = Ln::load_part(p.v, e, at.n_ch);
+            q[r] = Ln::load_part(p.q, e, at.n_ch);
+            dy[r] = Ln::load_part(p.dy, row * p.D + at.d0, at.n_ch);
+        }
+    }
+    if (at.t0 + R > p.L) {
 #pragma unroll
         for (int r = 0; r < R; ++r)
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) a[r][i] = decay<LOG>(Ln::get(g[r], i));
-        if (at.t0 + R > p.L) {  // rows past the end pass the gradient on
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                if (at.t0 + r < p.L) continue;
+            if (at.t0 + r >= p.L) {
+                g[r] = open_gate<F32, LOG>();
                 k[r] = q[r] = typename Ln::raw{};
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) a[r][i] = 1.0f;
             }
+    }
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+        float a[R], P, least, S = 0.0f, c = 0.0f;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            a[r] = decay<LOG>(Ln::get(g[r], i));
+            P = r == 0 ? a[0] : P * a[r];
+            least = r == 0 ? a[0] : fminf(least, a[r]);
         }
-    }
-    float least_of_all = 1.0f;
-    auto compose = [&](auto sel, int i, float &S, float &c) {
-        constexpr bool RESETS = decltype(sel)::value;
-        S = c = 0.0f;
 #pragma unroll
-        for (int r = 0; r < R; ++r) S = walk<RESETS>(a[r][i], Ln::get(k[r], i) * Ln::get(v[r], i), S);
+        for (int r = 0; r < R; ++r) S = apply(a[r], Ln::get(k[r], i) * Ln::get(v[r], i), S);
 #pragma unroll
-        for (int r = R - 1; r >= 0; --r)
-            c = walk<RESETS>(a[r][i], 0.0f, fmaf(Ln::get(q[r], i), Ln::get(dy[r], i), c));
-    };
-    float least[VEC];
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-        least[i] = a[0][i];
-#pragma unroll
-        for (int r = 1; r < R; ++r) least[i] = fminf(least[i], a[r][i]);
-        least_of_all = fminf(least_of_all, least[i]);
-    }
-    const bool resets = any_lane(least_of_all == 0.0f);
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-        float P = a[0][i], S, c;
-#pragma unroll
-        for (int r = 1; r < R; ++r) P *= a[r][i];
-        if (resets) compose(std::true_type(), i, S, c);
-        else compose(std::false_type(), i, S, c);
-        sP[slice][lane * VEC + i] = keep_off_zero(P, least[i]);
+        for (int r = R - 1; r >= 0; --r) c = apply(a[r], 0.0f, fmaf(Ln::get(q[r], i), Ln::get(dy[r], i), c));
+        sP[slice][lane * VEC + i] = keep_off_zero(P, least);
         sS[slice][lane * VEC + i] = S;
         sC[slice][lane * VEC + i] = c;
     }
@@ -448,50 +436,65 @@ __global__ __launch_bounds__(BwdTile<F32>::NT, 2) void scan_bwd_kernel(ScanParam
     lds_barrier();
     if (at.n_ch <= 0) return;
 
-    auto outputs = [&](auto sel) {
-        constexpr bool RESETS = decltype(sel)::value;
-        float s[R + 1][VEC], c[VEC];  // s[r]: before row r
+    // Or the compiler would keep what it computed from them above in registers.
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            const int ch = lane * VEC + i;
-            s[0][i] = sS[slice][ch];
-            c[i] = apply(sP[slice][ch], sC[slice][ch], sIn[ch]);
+    for (int r = 0; r < R; ++r) asm volatile("" : "+v"(g[r]), "+v"(k[r]), "+v"(v[r]), "+v"(q[r]), "+v"(dy[r]));
+    // Two channels at a time (one, in fp32): their gradients take the place of
+    // their inputs, dq of q, dk of k, dv of v and dg of g.
+    constexpr int PAIR = F32 ? 1 : 2;
 #pragma unroll
-            for (int r = 0; r < R; ++r)
-                s[r + 1][i] = walk<RESETS>(a[r][i], Ln::get(k[r], i) * Ln::get(v[r], i), s[r][i]);
-        }
-        const size_t first = ((size_t)at.b * p.L + at.t0) * p.ldd + at.d0;
+    for (int h = 0; h < VEC / PAIR; ++h) {
+                float dq[R][PAIR], dk[R][PAIR], dv[R][PAIR], dg[R][PAIR];
 #pragma unroll
-        for (int r = R - 1; r >= 0; --r) {
-            float dq[VEC], dk[VEC], dv[VEC], dg[VEC];
+            for (int w = 0; w < PAIR; ++w) {
+                const int i = h * PAIR + w, ch = lane * VEC + i;
+                float a[R], s[R + 1];  // s[r]: before row r
+                s[0] = sS[slice][ch];
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const float dyi = Ln::get(dy[r], i);
-                const float ds = fmaf(Ln::get(q[r], i), dyi, c[i]);
-                dq[i] = dyi * s[r + 1][i];
-                dk[i] = ds * Ln::get(v[r], i);
-                dv[i] = ds * Ln::get(k[r], i);
-                dg[i] = ds * s[r][i] * decay_slope<LOG>(Ln::get(g[r], i), a[r][i]);
-                c[i] = a[r][i] * ds;
-                if (RESETS && a[r][i] == 0.0f) dg[i] = c[i] = 0.0f;
+                for (int r = 0; r < R; ++r) {
+                    a[r] = decay<LOG>(Ln::get(g[r], i));
+                    s[r + 1] = apply(a[r], Ln::get(k[r], i) * Ln::get(v[r], i), s[r]);
+                }
+                float c = apply(sP[slice][ch], sC[slice][ch], sIn[ch]);
+#pragma unroll
+                for (int r = R - 1; r >= 0; --r) {
+                    const float dyi = Ln::get(dy[r], i), ds = fmaf(Ln::get(q[r], i), dyi, c);
+                    dq[r][w] = dyi * s[r + 1];
+                    dk[r][w] = ds * Ln::get(v[r], i);
+                    dv[r][w] = ds * Ln::get(k[r], i);
+                    dg[r][w] = ds * s[r] * decay_slope<LOG>(Ln::get(g[r], i), a[r]);
+                    c = a[r] * ds;
+                    if (a[r] == 0.0f) dg[r][w] = c = 0.0f;
+                }
             }
-            if (at.t0 + r >= p.L) continue;
-            const size_t o = first + (size_t)r * p.ldd;
-            if (at.n_ch == VEC) {
-                if (p.dq) Ln::store(p.dq, o, dq);
-                if (p.dk) Ln::store(p.dk, o, dk);
-                if (p.dv) Ln::store(p.dv, o, dv);
-                if (p.dg) Ln::store(p.dg, o, dg);
-            } else {
-                if (p.dq) store_part<F32>(p.dq, o, dq, at.n_ch);
-                if (p.dk) store_part<F32>(p.dk, o, dk, at.n_ch);
-                if (p.dv) store_part<F32>(p.dv, o, dv, at.n_ch);
-                if (p.dg) store_part<F32>(p.dg, o, dg, at.n_ch);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                Ln::put(q[r], h, dq[r]);
+                Ln::put(k[r], h, dk[r]);
+                Ln::put(v[r], h, dv[r]);
+                Ln::put(g[r], h, dg[r]);
             }
         }
-    };
-    if (resets) outputs(std::true_type());
-    else outputs(std::false_type());
+    // Computed here, not sunk into the branches of the stores with all it takes.
+#pragma unroll
+    for (int r = 0; r < R; ++r) asm volatile("" : "+v"(g[r]), "+v"(k[r]), "+v"(v[r]), "+v"(q[r]));
+    const size_t to = ((size_t)at.b * p.L + at.t0) * p.ldd + at.d0;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        if (at.t0 + r >= p.L) break;
+        const size_t o = to + (size_t)r * p.ldd;
+        if (!PART || at.n_ch == VEC) {
+            if (p.dq) Ln::store(p.dq, o, q[r]);
+            if (p.dk) Ln::store(p.dk, o, k[r]);
+            if (p.dv) Ln::store(p.dv, o, v[r]);
+            if (p.dg) Ln::store(p.dg, o, g[r]);
+        } else {
+            if (p.dq) Ln::store_part(p.dq, o, q[r], at.n_ch);
+            if (p.dk) Ln::store_part(p.dk, o, k[r], at.n_ch);
+            if (p.dv) Ln::store_part(p.dv, o, v[r], at.n_ch);
+            if (p.dg) Ln::store_part(p.dg, o, g[r], at.n_ch);
+        }
+    }
 }
 
 int check_sizes(int64_t B, int64_t L, int64_t D, int gate, int dtype) {
@@ -546,11 +549,14 @@ int launch_none(const float *from, float *to, int64_t n, void *stream) {
     return launch_status();
 }
 
+// PART: some lane at the right edge of D has less than its channels.
 template <bool F32, bool LOG> int launch_fwd(const ScanParams &p, void *ws, void *stream) {
-    return launch<FwdTile<F32>>(scan_fwd_kernel<F32, LOG>, p, ws, stream);
+    const bool part = p.D % Lane<F32>::VEC != 0;
+    return launch<FwdTile<F32>>(part ? scan_fwd_kernel<F32, LOG, true> : scan_fwd_kernel<F32, LOG, false>, p, ws, stream);
 }
 template <bool F32, bool LOG> int launch_bwd(const ScanParams &p, void *ws, void *stream) {
-    return launch<BwdTile<F32>>(scan_bwd_kernel<F32, LOG>, p, ws, stream);
+    const bool part = p.D % Lane<F32>::VEC != 0;
+    return launch<BwdTile<F32>>(part ? scan_bwd_kernel<F32, LOG, true> : scan_bwd_kernel<F32, LOG, false>, p, ws, stream);
 }
 
 }  // namespace

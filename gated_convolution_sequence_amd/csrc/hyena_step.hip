@@ -33,8 +33,8 @@ template <bool F32> __device__ inline typename Lane<F32>::raw load_row(const voi
 }
 template <bool F32>
 __device__ inline void store_row(void *p, size_t e, const float (&x)[Lane<F32>::VEC], int n) {
-    if (n == Lane<F32>::VEC) Lane<F32>::store(p, e, x);
-    else store_part<F32>(p, e, x, n);
+    if (n == Lane<F32>::VEC) Lane<F32>::store(p, e, Lane<F32>::pack(x));
+    else Lane<F32>::store_part(p, e, Lane<F32>::pack(x), n);
 }
 
 constexpr int kScanThreads = 64;

@@ -77,8 +77,14 @@ template <> struct Lane<false> {
     __device__ static raw pack(const float (&x)[8]) {
         return raw{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])};
     }
-    __device__ static void store(void *p, size_t e, const float (&x)[8]) {
-        __builtin_nontemporal_store(pack(x), (raw_any *)((bf16_t *)p + e));
+    __device__ static void put(raw &r, int h, const float (&x)[2]) { r[h] = pack_bf16(x[0], x[1]); }  // channels 2 h, 2 h + 1
+    __device__ static void store(void *p, size_t e, const raw &r) {
+        __builtin_nontemporal_store(r, (raw_any *)((bf16_t *)p + e));
+    }
+    __device__ static void store_part(void *p, size_t e, const raw &r, int n) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) ((uint16_t *)p)[e + i] = (uint16_t)(r[i >> 1] >> (i & 1 ? 16 : 0));
     }
 };
 template <> struct Lane<true> {
@@ -95,15 +101,17 @@ template <> struct Lane<true> {
         return r;
     }
     __device__ static float get(const raw &r, int i) { return r[i]; }
-    __device__ static void store(void *p, size_t e, const float (&x)[4]) {
-        __builtin_nontemporal_store(raw{x[0], x[1], x[2], x[3]}, (raw_any *)((float *)p + e));
+    __device__ static raw pack(const float (&x)[4]) { return raw{x[0], x[1], x[2], x[3]}; }
+    __device__ static void put(raw &r, int h, const float (&x)[1]) { r[h] = x[0]; }
+    __device__ static void store(void *p, size_t e, const raw &r) {
+        __builtin_nontemporal_store(r, (raw_any *)((float *)p + e));
+    }
+    __device__ static void store_part(void *p, size_t e, const raw &r, int n) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n) ((float *)p)[e + i] = r[i];
     }
 };
-template <bool F32> __device__ inline void store_part(void *p, size_t e, const float (&x)[Lane<F32>::VEC], int n) {
-#pragma unroll
-    for (int i = 0; i < Lane<F32>::VEC; ++i)
-        if (i < n) store1<F32>(p, e + i, x[i]);
-}
 
 // ---- host -------------------------------------------------------------------
 
