@@ -290,11 +290,12 @@ int hyena_conv_step(const void *q, const void *k, const void *v, const void *h, 
     if (B < 0 || D < 0 || S < 0 || ld < D || !mul_fits(B, ld, eb, &n)) return HYENA_ERR_SHAPE;
     if (group_size < 1 || D % group_size != 0) return HYENA_ERR_GROUP;
     if (l_h < 1 || l_h > 128) return HYENA_ERR_FILTER_LEN;
-    if (R < l_h || !mul_fits(S, R, 1, &n) || !mul_fits(n, D, eb, &n)) return HYENA_ERR_SHAPE;
+    int64_t ring;
+    if (R < l_h || !mul_fits(R, D, eb, &ring) || !mul_fits(S, ring, 1, &n)) return HYENA_ERR_SHAPE;
     if (!slots && S < B) return HYENA_ERR_SHAPE;
     if (B == 0 || D == 0) return HYENA_OK;
     // offsets in a ring are 31 bits, rings are counted in 32
-    if (R * D * eb > 0x7fffffff || S > 0x7fffffff) return HYENA_ERR_UNSUPPORTED;
+    if (ring > 0x7fffffff || S > 0x7fffffff) return HYENA_ERR_UNSUPPORTED;
     if (!q || !k || !v || !h || !y || !pos || (!cache && S > 0)) return HYENA_ERR_NULL;
     if (!aligned(q, eb) || !aligned(k, eb) || !aligned(v, eb) || !aligned(h, eb) || !aligned(y, eb) ||
         !aligned(cache, eb) || !aligned(pos, 8) || !aligned(slots, 4))

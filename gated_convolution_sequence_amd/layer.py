@@ -155,11 +155,26 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-def _call(name: str, dev: torch.device, stream, *args) -> None:
-    """name(*args, stream) on dev; raises LayerError for a status other than HYENA_OK."""
+def _on_stream(fn):
+    """Runs fn with its ``stream`` as the current one.
+
+    What fn allocates (outputs, workspaces it does not return) then belongs to
+    that stream, so that the allocator hands none of it on before its work there is done.
+    """
+    @functools.wraps(fn)
+    def run(*args, stream: Optional[torch.cuda.Stream] = None, **kwargs):
+        if stream is None:
+            return fn(*args, **kwargs)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kwargs)
+    return run
+
+
+def _call(name: str, dev: torch.device, *args) -> None:
+    """name(*args, current stream) on dev; raises LayerError for a status other than HYENA_OK."""
     fn = getattr(_lib or layer_lib(), name)
     # the current stream's handle, without the Stream object torch.cuda.current_stream makes
-    handle = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+    handle = torch._C._cuda_getCurrentRawStream(dev.index)
     if dev.index == torch._C._cuda_getDevice():
         st = fn(*args, handle)
     else:
@@ -201,6 +216,7 @@ def _scan_inputs(ts, names):
     return code, _rows_like(ts, names, q.shape, q.dtype, q.device)
 
 
+@_on_stream
 def scan_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, gate: str = "sigmoid",
              s0: Optional[torch.Tensor] = None, save_states: bool = False, out: Optional[torch.Tensor] = None,
              workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
@@ -228,11 +244,12 @@ def scan_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
     if save_states:
         states = torch.empty((B, -(-L // STATE_ROWS), D), dtype=torch.float32, device=dev)
     ws = _workspace(scan_workspace_bytes(B, L, D, code), workspace, dev)
-    _call("hyena_scan_fwd", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), B, L, D, ld, gcode,
+    _call("hyena_scan_fwd", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), B, L, D, ld, gcode,
           _ptr(s0), out.data_ptr(), s_last.data_ptr(), _ptr(states), *_ws_args(ws), code)
     return out, s_last, states
 
 
+@_on_stream
 def scan_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, dy: torch.Tensor,
              states: torch.Tensor, gate: str = "sigmoid", ds_last: Optional[torch.Tensor] = None,
              grads: Optional[Sequence[torch.Tensor]] = None, workspace: Optional[torch.Tensor] = None,
@@ -260,12 +277,13 @@ def scan_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
         ldd = _rows_like(grads, names, q.shape, q.dtype, dev)
     ds0 = torch.empty((B, D), dtype=torch.float32, device=dev)
     ws = _workspace(scan_workspace_bytes(B, L, D, code), workspace, dev)
-    _call("hyena_scan_bwd", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), dy.data_ptr(),
+    _call("hyena_scan_bwd", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), dy.data_ptr(),
           states.data_ptr(), _ptr(ds_last), B, L, D, ld, ldd, gcode, *(t.data_ptr() for t in grads), ds0.data_ptr(),
           *_ws_args(ws), code)
     return (*grads, ds0)
 
 
+@_on_stream
 def scan_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, state: torch.Tensor,
               slots: Optional[torch.Tensor] = None, gate: str = "sigmoid",
               state_out: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
@@ -291,7 +309,7 @@ def scan_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor
         out = torch.empty((B, D), dtype=q.dtype, device=dev)
     else:
         _contiguous(out, "out", (B, D), q.dtype, dev)
-    _call("hyena_scan_step", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), B, D, ld, gcode,
+    _call("hyena_scan_step", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), B, D, ld, gcode,
           state.data_ptr(), _ptr(state_out), S, _ptr(slots), out.data_ptr(), code)
     return out
 
@@ -326,6 +344,7 @@ def _cache_sizes(cache: torch.Tensor, D: int, dtype, dev):
     return S, R
 
 
+@_on_stream
 def conv_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, h: torch.Tensor, cache: torch.Tensor,
               pos: torch.Tensor, group_size: int, slots: Optional[torch.Tensor] = None,
               out: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
@@ -352,11 +371,12 @@ def conv_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, h: torch.Tensor
         out = torch.empty((B, D), dtype=q.dtype, device=dev)
     else:
         _contiguous(out, "out", (B, D), q.dtype, dev)
-    _call("hyena_conv_step", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), h.data_ptr(), B, D, ld,
+    _call("hyena_conv_step", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), h.data_ptr(), B, D, ld,
           group_size, l_h, cache.data_ptr(), S, R, pos.data_ptr(), _ptr(slots), out.data_ptr(), code)
     return out
 
 
+@_on_stream
 def conv_cache_fill(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, lens: Optional[torch.Tensor] = None,
                     slots: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> None:
     """The last rows of a prompt's k v into the ring cache, for conv_step from pos = lens on.
@@ -373,7 +393,7 @@ def conv_cache_fill(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, lens:
     S, R = _cache_sizes(cache, D, k.dtype, dev)
     _contiguous(lens, "lens", (B,), torch.int64, dev)
     _contiguous(slots, "slots", (B,), torch.int32, dev)
-    _call("hyena_conv_cache_fill", dev, stream, k.data_ptr(), v.data_ptr(), B, L, D, ld, cache.data_ptr(), S, R,
+    _call("hyena_conv_cache_fill", dev, k.data_ptr(), v.data_ptr(), B, L, D, ld, cache.data_ptr(), S, R,
           _ptr(lens), _ptr(slots), code)
 
 
@@ -396,6 +416,7 @@ def _rows_of(t: torch.Tensor) -> int:
     return n
 
 
+@_on_stream
 def linear_fwd(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None,
                residual: Optional[torch.Tensor] = None, act: str = "none", save_preact: bool = False,
                out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
@@ -429,11 +450,12 @@ def linear_fwd(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = 
         ldy = _shared_stride((out,), ("out",), N)
     preact = torch.empty(shape, dtype=dt, device=dev) if save_preact else None
     ws = _workspace(linear_workspace_bytes(M, N, K, act, code), workspace, dev)
-    _call("hyena_linear_fwd", dev, stream, x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(residual), M, N, K, ldx, ldr,
+    _call("hyena_linear_fwd", dev, x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(residual), M, N, K, ldx, ldr,
           ldy, acode, out.data_ptr(), _ptr(preact), *_ws_args(ws), code)
     return out, preact
 
 
+@_on_stream
 def linear_bwd(x: torch.Tensor, w: torch.Tensor, dy: torch.Tensor, preact: Optional[torch.Tensor] = None,
                act: str = "none", need_dx: bool = True, need_dw: bool = True, need_db: bool = True,
                dx: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
@@ -474,7 +496,7 @@ def linear_bwd(x: torch.Tensor, w: torch.Tensor, dy: torch.Tensor, preact: Optio
     if dx is None and dw is None and db is None:
         return None, None, None
     ws = _workspace(linear_workspace_bytes(M, N, K, act, code, backward=True), workspace, dev)
-    _call("hyena_linear_bwd", dev, stream, x.data_ptr(), w.data_ptr(), _ptr(preact) if acode else None,
+    _call("hyena_linear_bwd", dev, x.data_ptr(), w.data_ptr(), _ptr(preact) if acode else None,
           dy.data_ptr(), M, N, K, ldx, lddy, lddx, acode, _ptr(dx), _ptr(dw), _ptr(db), *_ws_args(ws), code)
     return dx, dw, db
 

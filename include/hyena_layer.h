@@ -20,9 +20,8 @@
  * so every call can be captured into a HIP graph.
  *
  * Alignment: data pointers need the alignment of their elements (else
- * HYENA_ERR_ALIGN).  Pointers and row strides that are multiples of 16 bytes
- * (and feature counts to match) take the wide kernels; any other takes the
- * same arithmetic in narrower accesses.
+ * HYENA_ERR_ALIGN), and sizes and row strides are free.  Multiples of 16 bytes
+ * are fastest.
  */
 #ifndef HYENA_LAYER_H
 #define HYENA_LAYER_H

@@ -122,6 +122,7 @@ def conv_step(q=P[0], k=P[1], v=P[2], h=P[3], B=2, D=64, ld=64, gs=16, l_h=7, ca
     (dict(h=None), -1), (dict(cache=None), -1), (dict(pos=None), -1),
     (dict(ld=1), -2), (dict(R=6), -2), (dict(slots=None, S=1), -2), (dict(S=1 << 50, R=1 << 20), -2),
     (dict(gs=0), -3), (dict(gs=48), -3), (dict(l_h=0), -4), (dict(l_h=129, R=200), -4),
+    (dict(R=1 << 25), -7), (dict(S=1 << 31), -7), (dict(S=0, R=1 << 60), -2),
     (dict(pos=P[5] + 4), -5), (dict(cache=P[4] + 1), -5),
     (dict(y=P[4]), -6), (dict(cache=P[3]), -6), (dict(y=P[5]), -6), (dict(dtype=7), -9),
 ])

@@ -158,8 +158,9 @@ def test_non_finite_values_stay_in_their_rows(bad, M):
 def test_empty_sizes():
     e = lambda *s: torch.empty(*s, dtype=BF16, device=DEV)
     b = torch.randn(6, device=DEV).to(BF16)
-    y, _ = hc.linear_fwd(e(4, 0), e(6, 0), bias=b)
-    assert torch.equal(y, b.expand(4, 6))
+    for M in (4, 200):
+        y, _ = hc.linear_fwd(e(M, 0), e(6, 0), bias=b)
+        assert torch.equal(y, b.expand(M, 6))
     y, _ = hc.linear_fwd(e(0, 8), e(6, 8), bias=b)
     assert y.shape == (0, 6)
     dx, dw, db = hc.linear_bwd(e(0, 8), e(6, 8), e(0, 6))
@@ -258,6 +259,24 @@ def test_autograd_against_differences(act):
                     vals.append(loss(*[moved if m == i else o.detach() for m, o in enumerate(args)]))
             num.view(-1)[j] = (vals[0] - vals[1]) / (2 * h)
         assert (num - a.grad).abs().max() <= 2.0 ** -8 * a.grad.abs().max(), i
+
+
+def test_memory_of_another_stream_is_not_reused_early():
+    """A call queued behind long work on a side stream: what it allocated stays its own meanwhile."""
+    t = inputs(300, 256, 2048, F32, 60)
+    dz = torch.randn(300, 256, device=DEV)
+    want = hc.linear_bwd(t["x"], t["w"], t["dy"], preact=dz, act="gelu")
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)  # some milliseconds
+    got = hc.linear_bwd(t["x"], t["w"], t["dy"], preact=dz, act="gelu", stream=side)
+    n = hc.linear_workspace_bytes(300, 256, 2048, "gelu", 1, backward=True)
+    filled = [torch.full((n,), 255, dtype=torch.uint8, device=DEV) for _ in range(4)]
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    assert all(bool((f == 255).all()) for f in filled)
 
 
 def test_refusals():
