@@ -29,7 +29,8 @@
 //
 // A gate of exactly 0 drops the state, whatever it holds.  P is therefore kept
 // at 0 exactly where a run holds such a gate, and off 0 (at the least positive
-// fp32) where a product of small gates underflows.
+// fp32) where a product of small gates underflows.  A gate of NaN is not kept in
+// P, which fmaxf would lose: S is NaN then, also where the run starts with it.
 
 #include <type_traits>
 
@@ -65,6 +66,9 @@ __device__ inline float apply(float P, float S, float s) { return P == 0.0f ? S 
 __device__ inline float join(float P1, float P2) {
     return P1 == 0.0f || P2 == 0.0f ? 0.0f : fmaxf(P1 * P2, __uint_as_float(1u));
 }
+
+// The state after a run's first row, taken from 0: x, or NaN where the gate is.
+__device__ inline float from_zero(float a, float x) { return a == a ? x : a; }
 
 __device__ inline void put_word(uint64_t *w, uint32_t hi, float lo) {
     __hip_atomic_store(w, ((uint64_t)hi << 32) | __float_as_uint(lo), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -257,7 +261,7 @@ __global__ __launch_bounds__(FwdTile<F32>::NT, 2) void scan_fwd_kernel(ScanParam
     auto compose = [&](auto sel) {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-            S[i] = x[0][i];
+            S[i] = from_zero(a[0][i], x[0][i]);
 #pragma unroll
             for (int r = 1; r < R; ++r) S[i] = walk<decltype(sel)::value>(a[r][i], x[r][i], S[i]);
         }
@@ -384,7 +388,7 @@ __global__ __launch_bounds__(BwdTile<F32>::NT, PART ? 2 : 3) void scan_bwd_kerne
     }
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
-        float a[R], P, least, S = 0.0f, c = 0.0f;
+        float a[R], P, least, S, c = 0.0f;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             a[r] = decay<LOG>(Ln::get(g[r], i));
@@ -392,7 +396,10 @@ __global__ __launch_bounds__(BwdTile<F32>::NT, PART ? 2 : 3) void scan_bwd_kerne
             least = r == 0 ? a[0] : fminf(least, a[r]);
         }
 #pragma unroll
-        for (int r = 0; r < R; ++r) S = apply(a[r], Ln::get(k[r], i) * Ln::get(v[r], i), S);
+        for (int r = 0; r < R; ++r) {
+            const float x = Ln::get(k[r], i) * Ln::get(v[r], i);
+            S = r == 0 ? from_zero(a[0], x) : apply(a[r], x, S);
+        }
 #pragma unroll
         for (int r = R - 1; r >= 0; --r) c = apply(a[r], 0.0f, fmaf(Ln::get(q[r], i), Ln::get(dy[r], i), c));
         sP[slice][lane * VEC + i] = keep_off_zero(P, least);
@@ -444,37 +451,37 @@ __global__ __launch_bounds__(BwdTile<F32>::NT, PART ? 2 : 3) void scan_bwd_kerne
     constexpr int PAIR = F32 ? 1 : 2;
 #pragma unroll
     for (int h = 0; h < VEC / PAIR; ++h) {
-                float dq[R][PAIR], dk[R][PAIR], dv[R][PAIR], dg[R][PAIR];
+        float dq[R][PAIR], dk[R][PAIR], dv[R][PAIR], dg[R][PAIR];
 #pragma unroll
-            for (int w = 0; w < PAIR; ++w) {
-                const int i = h * PAIR + w, ch = lane * VEC + i;
-                float a[R], s[R + 1];  // s[r]: before row r
-                s[0] = sS[slice][ch];
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    a[r] = decay<LOG>(Ln::get(g[r], i));
-                    s[r + 1] = apply(a[r], Ln::get(k[r], i) * Ln::get(v[r], i), s[r]);
-                }
-                float c = apply(sP[slice][ch], sC[slice][ch], sIn[ch]);
-#pragma unroll
-                for (int r = R - 1; r >= 0; --r) {
-                    const float dyi = Ln::get(dy[r], i), ds = fmaf(Ln::get(q[r], i), dyi, c);
-                    dq[r][w] = dyi * s[r + 1];
-                    dk[r][w] = ds * Ln::get(v[r], i);
-                    dv[r][w] = ds * Ln::get(k[r], i);
-                    dg[r][w] = ds * s[r] * decay_slope<LOG>(Ln::get(g[r], i), a[r]);
-                    c = a[r] * ds;
-                    if (a[r] == 0.0f) dg[r][w] = c = 0.0f;
-                }
-            }
+        for (int w = 0; w < PAIR; ++w) {
+            const int i = h * PAIR + w, ch = lane * VEC + i;
+            float a[R], s[R + 1];  // s[r]: before row r
+            s[0] = sS[slice][ch];
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                Ln::put(q[r], h, dq[r]);
-                Ln::put(k[r], h, dk[r]);
-                Ln::put(v[r], h, dv[r]);
-                Ln::put(g[r], h, dg[r]);
+                a[r] = decay<LOG>(Ln::get(g[r], i));
+                s[r + 1] = apply(a[r], Ln::get(k[r], i) * Ln::get(v[r], i), s[r]);
+            }
+            float c = apply(sP[slice][ch], sC[slice][ch], sIn[ch]);
+#pragma unroll
+            for (int r = R - 1; r >= 0; --r) {
+                const float dyi = Ln::get(dy[r], i), ds = fmaf(Ln::get(q[r], i), dyi, c);
+                dq[r][w] = dyi * s[r + 1];
+                dk[r][w] = ds * Ln::get(v[r], i);
+                dv[r][w] = ds * Ln::get(k[r], i);
+                dg[r][w] = ds * s[r] * decay_slope<LOG>(Ln::get(g[r], i), a[r]);
+                c = a[r] * ds;
+                if (a[r] == 0.0f) dg[r][w] = c = 0.0f;
             }
         }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            Ln::put(q[r], h, dq[r]);
+            Ln::put(k[r], h, dk[r]);
+            Ln::put(v[r], h, dv[r]);
+            Ln::put(g[r], h, dg[r]);
+        }
+    }
     // Computed here, not sunk into the branches of the stores with all it takes.
 #pragma unroll
     for (int r = 0; r < R; ++r) asm volatile("" : "+v"(g[r]), "+v"(k[r]), "+v"(v[r]), "+v"(q[r]));
@@ -497,19 +504,19 @@ __global__ __launch_bounds__(BwdTile<F32>::NT, PART ? 2 : 3) void scan_bwd_kerne
     }
 }
 
+// Rows and channels of the smallest tile of any variant bound the words.
+constexpr int64_t kLeastRows = 64, kMostChannels = 128;
+constexpr int64_t kHeader = kMostCounters * kCounterGap * 4;
+
 int check_sizes(int64_t B, int64_t L, int64_t D, int gate, int dtype) {
     if (dtype != HYENA_DTYPE_BF16 && dtype != HYENA_DTYPE_F32) return HYENA_ERR_DTYPE;
     if (gate != HYENA_GATE_SIGMOID && gate != HYENA_GATE_LOG) return HYENA_ERR_UNSUPPORTED;
     int64_t n;
     if (B < 0 || L < 0 || D < 0) return HYENA_ERR_SHAPE;
-    if (!mul_fits(B, L, 1, &n) || !mul_fits(n, D, 4, &n) || !mul_fits(B, D, 4, &n)) return HYENA_ERR_SHAPE;
     if (L > (int64_t)1 << 40 || D > (int64_t)1 << 30 || B > (int64_t)1 << 30) return HYENA_ERR_SHAPE;
+    if (!mul_fits(B, L, 1, &n) || !mul_fits(n, D + kMostChannels, 4, &n)) return HYENA_ERR_SHAPE;
     return HYENA_OK;
 }
-
-// Rows and channels of the smallest tile of any variant bound the words.
-constexpr int64_t kLeastRows = 64, kMostChannels = 128;
-constexpr int64_t kHeader = kMostCounters * kCounterGap * 4;
 
 int64_t workspace_bytes(int64_t B, int64_t L, int64_t D) {
     if (L <= kLeastRows || B == 0 || D == 0) return 0;

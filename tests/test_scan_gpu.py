@@ -125,6 +125,21 @@ def test_a_reset_drops_what_is_not_finite(bad, D):
     assert torch.isfinite(got[3][:, 150]).all()
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("gate", ["sigmoid", "log"])
+@pytest.mark.parametrize("D", [64, 37])
+def test_a_gate_of_nan_is_not_lost(dtype, gate, D):
+    """A gate of NaN in any row of a tile reaches every later state of its channel, up to a reset."""
+    ts = inputs(1, 400, D, dtype, gate, 15)
+    for d in range(32):
+        ts[3][0, 130 + d, d] = math.nan
+    ts[3][0, 300, 9:14] = -math.inf
+    s0, ds_last = states_of(1, D, 6)
+    y, last, states = check_fwd(ts, gate, s0, "fwd")
+    assert torch.isnan(y[0, 299, :32]).all() and torch.isfinite(y[0, 300:, 9:14]).all()
+    check_bwd(ts, gate, s0, ds_last, states, "bwd")
+
+
 def test_an_infinite_state_lives_on_without_a_reset():
     """Only a gate of exactly 0 drops the state: small gates whose product underflows do not."""
     ts = inputs(1, 600, 64, F32, "log", 12)
