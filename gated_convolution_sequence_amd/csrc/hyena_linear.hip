@@ -185,7 +185,7 @@ struct GemmParams {
     int M, N, C;
     int tiles_m, tiles_n;
     int splits, c_per_split;  // c is cut into splits (a multiple of the step each, but the last)
-    float *partial;           // splits > 1: [splits][M][N] sums for split_kernel; else null
+    float *partial;           // splits > 1: [splits][M][N] sums for finish_kernel; else null
     Epilogue e;
 };
 
@@ -367,11 +367,15 @@ template <int N> __device__ __forceinline__ void step_barrier() {
 
 // A workgroup of WM x WN waves, each MT x NTL tiles of 16 x 16, with ST
 // operand buffers: ST - 1 steps of c are on their way while one is multiplied.
+// Bound by the matrix cores and the reads of LDS that feed them: at M = 8192, N
+// = K = 4096 bf16 the forward's product takes 230 us (1.2 PFLOP/s), dx = dz w 242
+// us (1.14) and dw = dz^T x 224 us (1.23), 256 x 256 tiles.
 template <bool F32, int WM, int WN, int MT, int NTL, int ST> struct Shape {
     static constexpr int NT = 64 * WM * WN, BM = WM * MT * 16, BN = WN * NTL * 16;
     static constexpr int CE = El<F32>::CE, BK = 8 * CE;
     static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128, STAGES = ST;
-    static constexpr int WAVES = ST * (A_BYTES + B_BYTES) > 80 * 1024 ? NT / 256 : ST * (A_BYTES + B_BYTES) > 53 * 1024 ? NT / 128 : 3;  // a SIMD, by LDS
+    static constexpr int LDS = ST * (A_BYTES + B_BYTES);
+    static constexpr int WAVES = LDS > 80 * 1024 ? NT / 256 : LDS > 53 * 1024 ? NT / 128 : 3;  // a SIMD, by LDS
 
     // The workgroup's tile of one product; la and lb are the operands' buffers.
     template <bool TALL_A, bool TALL_B, bool DIRECT>
@@ -565,7 +569,9 @@ template <bool TALL_A, typename S> __global__ __launch_bounds__(S::NT, S::WAVES)
 }
 
 // What remains after the products: the sums of the splits with their epilogue
-// (four columns a thread), and db from the row blocks' column sums.
+// (four columns a thread), and db from the row blocks' column sums.  Bound by its
+// launch (4 to 5 us at N = 4096).  Atomics in the products would spare it and make
+// the bits depend on their order.
 struct FinishParams {
     GemmParams g[2];
     int64_t blocks[2];   // workgroups of each
@@ -617,7 +623,12 @@ template <bool F32> __global__ __launch_bounds__(256) void finish_kernel(FinishP
 // workgroup owns 16 rows of w (16 columns of y) and MT x 16 rows of x; its
 // waves cut c between them, and each loads its fragments of w and x straight
 // from memory into the matrix cores' layout: lane (i, j) takes two 16-byte chunks
-// of row i at 128-byte steps, one of each 64 bytes, which serve two products.  The waves' sums meet in LDS.
+// of row i at 128-byte steps, one of each 64 bytes, which serve two products.
+// The waves' sums meet in LDS.  8 rows against 4096 x 4096 bf16 weights: 10.5 us
+// (33.6 MB at 3.2 TB/s; a launch and one trip to memory are about 4.5 us of it).
+// 8 waves with 2 steps each in flight: 9.4 / 10.8 / 17.6 us for 1 row, 8 rows and
+// 8 rows in fp32; 4 waves 11.2 / 11.2 / 20.3, 16 waves 10.1 / 11.1 / 19.1, 1 step
+// 10.2 / 10.9 / 19.3, 4 steps 10.5 / 11.4 / 20.2.
 struct RowsParams {
     const void *x, *w;
     int64_t ldx;
@@ -717,8 +728,11 @@ __global__ __launch_bounds__(64 * kRowWaves) void rows_kernel(RowsParams p) {
 
 // ---- dz and db -----------------------------------------------------------------------
 
-// dz = dy act'(z) (rounded once) and each block's column sums of the unrounded
-// dz.  A block takes 32 lanes of four columns by `rows` rows.
+// dz = dy act'(z) (rounded once, to the type the matrix cores take) and each
+// block's column sums of the unrounded dz.  A block takes 32 lanes of four
+// columns by `rows` rows.  Bound by memory: 8192 x 4096 bf16 in 41 us (201 MB,
+// 4.9 TB/s).  Formed in the products' loads instead, dy and z would be read anew
+// by every tile of a row and column of tiles, and straight loads into LDS lost.
 struct DzParams {
     const void *dy, *z;
     void *dz;         // null: only the sums
@@ -764,7 +778,17 @@ template <bool F32, int ACT> __global__ __launch_bounds__(256) void dz_kernel(Dz
 
 // ---- host --------------------------------------------------------------------------------
 
-constexpr int kRowsMost = 32;  // rows of x up to which rows_kernel is taken
+// Whether rows_kernel takes the forward.  It cuts no c between workgroups, so long
+// rows want enough columns, and every workgroup reads all of x, so more rows want
+// short ones (us in bf16, rows_kernel and tiles):
+//   M = 16: N x K = 1024 x 1024 5.3 / 8.0, 512 x 2048 6.6 / 7.3, 4096 x 4096
+//           11.7 / 12.2, 4096 x 8192 20.1 / 21.3; but 1024 x 4096 10.6 / 9.2, 2048 x
+//           8192 18.6 / 13.2
+//   M = 32: 1024 x 1024 5.4 / 7.4, 4096 x 1024 6.2 / 8.6, 8192 x 1024 9.2 / 10.1;
+//           but 16384 x 1024 15.1 / 10.0, 1024 x 4096 13.9 / 9.2, 4096 x 4096 15.0 / 12.8
+bool few_rows(int64_t M, int64_t N, int64_t K) {
+    return M <= 16 ? K <= 2048 || N >= 4096 : M <= 32 && K <= 1024 && N <= 8192;
+}
 
 template <bool F32> using Small = Shape<F32, 2, 2, 4, 4, 2>;  // 128 x 128 tiles, 4 waves, two workgroups a unit
 template <bool F32> using Deep = Shape<F32, 2, 2, 4, 4, 4>;    // the same, three steps ahead, one workgroup a unit
@@ -876,7 +900,7 @@ template <bool F32>
 int linear_fwd(const void *x, int64_t ldx, const void *w, int64_t M, int64_t N, int64_t K, Epilogue e, void *ws,
                hipStream_t stream) {
     const int64_t eb = F32 ? 4 : 2;
-    if (M <= kRowsMost) {
+    if (few_rows(M, N, K)) {
         RowsParams p = {};
         p.x = x, p.w = w, p.ldx = ldx, p.M = (int)M, p.N = (int)N, p.K = (int)K;
         p.e = e;
@@ -1043,7 +1067,7 @@ int hyena_linear_workspace(int64_t M, int64_t N, int64_t K, int act, int dtype, 
         *bytes_out = s.dz + s.sums + s.partial;
     } else {
         const Size sz = {M, N, K};
-        *bytes_out = M > kRowsMost && N > 0 ? partial_bytes(&sz, 1, dtype == HYENA_DTYPE_F32) : 0;
+        *bytes_out = N > 0 && !few_rows(M, N, K) ? partial_bytes(&sz, 1, dtype == HYENA_DTYPE_F32) : 0;
     }
     return HYENA_OK;
 }

@@ -51,7 +51,8 @@ def check_bwd(t, z, act, what, **need):
 SHAPES = [(1, 1, 1), (1, 64, 64), (1, 4096, 512), (2, 17, 33), (3, 100, 8), (5, 129, 70), (8, 256, 1024), (9, 24, 2048),
           (15, 48, 40), (16, 64, 96), (17, 80, 72), (33, 130, 264), (48, 512, 520), (64, 64, 64), (65, 72, 136),
           (100, 200, 300), (127, 129, 131), (128, 128, 128), (200, 264, 1032), (256, 256, 64), (257, 520, 200),
-          (300, 1, 50), (1000, 72, 24), (513, 385, 96)]
+          (300, 1, 50), (1000, 72, 24), (513, 385, 96), (4, 72, 2056), (16, 100, 4100), (8, 4100, 2056),
+          (24, 64, 1032), (31, 8200, 40), (32, 128, 1024)]
 
 
 @pytest.mark.parametrize("shape", SHAPES, ids=str)
