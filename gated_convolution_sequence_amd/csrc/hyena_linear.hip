@@ -21,8 +21,10 @@
 //   * The products are formed as B A^T, so a lane ends up with 4 consecutive n
 //     of one m, and the epilogue's way through LDS is in 16-byte accesses.
 // Operands whose 16-byte chunks are not aligned (odd sizes, strides or
-// pointers) cannot be fetched straight into LDS: the same kernels take them
-// through registers, a step ahead, with unaligned 16-byte loads.
+// pointers) cannot be fetched straight into LDS.  Where their sizes are odd and
+// the product is long enough, they are copied to padded rows first; otherwise the
+// same kernels take them through registers, a step ahead, with unaligned 16-byte
+// loads.
 
 #include <initializer_list>
 
@@ -726,28 +728,70 @@ __global__ __launch_bounds__(64 * kRowWaves) void rows_kernel(RowsParams p) {
     }
 }
 
-// ---- dz and db -----------------------------------------------------------------------
+// ---- dz, db and padded rows ------------------------------------------------------------
 
 // dz = dy act'(z) (rounded once, to the type the matrix cores take) and each
 // block's column sums of the unrounded dz.  A block takes 32 lanes of four
 // columns by `rows` rows.  Bound by memory: 8192 x 4096 bf16 in 41 us (201 MB,
 // 4.9 TB/s).  Formed in the products' loads instead, dy and z would be read anew
 // by every tile of a row and column of tiles, and straight loads into LDS lost.
+//
+// Where rows are no whole number of 16 bytes, x and w are copied to rows that
+// are, zeros behind them, by further blocks of the same launch (and dz is written
+// so), for the products to fetch straight into LDS: one pass over the operands
+// instead of registers and element-wise edges in every tile.
+struct Pads {
+    const void *from[2];  // null: none
+    void *to[2];          // rows of `chunks` 16-byte chunks
+    int64_t ld[2];
+    uint32_t rows[2];     // rows * chunks is below 2^31
+    uint32_t n, chunks;
+};
 struct DzParams {
     const void *dy, *z;
     void *dz;         // null: only the sums
     float *sums;      // [row blocks][N], or null
-    int64_t M, lddy;
+    int64_t M, lddy, lddz;  // lddz: whole 16 bytes
     int N, rows;
+    unsigned row_blocks;  // blockIdx.y from there on: padded rows
+    Pads pads;
 };
+
+template <bool F32> __device__ inline void copy_rows(const Pads &p, uint32_t block, uint32_t blocks) {
+    using T = typename El<F32>::type;
+    constexpr int CE = El<F32>::CE;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+        if (!p.from[g]) continue;
+        const uint32_t total = p.rows[g] * p.chunks;
+        for (uint32_t id = block * 256 + threadIdx.x; id < total; id += blocks * 256) {
+            const uint32_t row = id / p.chunks, c = (id - row * p.chunks) * CE, left = p.n - c;
+            const T *from = (const T *)p.from[g] + (int64_t)row * p.ld[g] + c;
+            u32x4_t v;
+            if (left >= CE) {
+                v = *(const typename El<F32>::chunk_any *)from;
+            } else {
+                T x[CE];
+#pragma unroll
+                for (int e = 0; e < CE; ++e) x[e] = e < (int)left ? from[e] : (T)0.0f;
+                v = __builtin_bit_cast(u32x4_t, x);
+            }
+            ((u32x4_t *)p.to[g])[id] = v;
+        }
+    }
+}
 
 template <bool F32, int ACT> __global__ __launch_bounds__(256) void dz_kernel(DzParams p) {
     __shared__ float part[8][128];
+    if (blockIdx.y >= p.row_blocks)
+        return copy_rows<F32>(p.pads, (blockIdx.y - p.row_blocks) * gridDim.x + blockIdx.x,
+                              (gridDim.y - p.row_blocks) * gridDim.x);
     const int cl = threadIdx.x & 31, rl = threadIdx.x >> 5;
     const int n = (blockIdx.x * 32 + cl) * 4, left = p.N - n;
     const int64_t first = (int64_t)blockIdx.y * p.rows, last = min(p.M, first + p.rows);
     float sum[4] = {};
-    if (left > 0) {
+    const int wide = p.dz ? (int)(p.lddz - n) : left;  // dz has zeros behind its columns
+    if (wide > 0) {
 #pragma unroll 4
         for (int64_t m = first + rl; m < last; m += 8) {
             const auto rd = Pack<F32, 4>::load(p.dy, m * p.lddy + n, left);
@@ -761,7 +805,7 @@ template <bool F32, int ACT> __global__ __launch_bounds__(256) void dz_kernel(Dz
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) sum[e] += d[e];
-            if (p.dz) Pack<F32, 4>::store(p.dz, m * p.N + n, left, d);
+            if (p.dz) Pack<F32, 4>::store(p.dz, m * p.lddz + n, 4, d);
         }
     }
     if (!p.sums) return;
@@ -806,18 +850,24 @@ struct Size {
     int64_t M, N, C;
 };
 
-constexpr int64_t kLeastSteps = 8;  // of a split: below, its partial sums cost more than they save
+// Steps of a split, and three times as many for c to be cut at all: the launch
+// that adds the sums costs about as much as four.  (64 x 1024 x 1024, us in fp32
+// and bf16: 9.2 / 7.1, with splits of 8 steps 10.7 / 7.8; cutting the 8 steps of
+// 200 x 512 x 512 bf16 in two 7.0, uncut 5.2.)
+constexpr int64_t kLeastSteps = 4;
 
 // Tiles: 256 x 256 where they fill the card's 256 units about as well as 128 x
 // 128 ones, 64 x 64 where there are fewer than 192 of 128 x 128 (at M = 1000,
 // N = K = 1024 bf16 forward 15 us, with split tiles of 128 x 128 20 us; at
 // 1021 x 777 x 521 fp32 24 against 31 us).
 // Splits: c is cut where a workgroup would walk much more than its share of
-// all steps.  One bf16 product is shared between 256 workgroups, each three
-// steps ahead of its products where a unit has one; two products between 512;
-// fp32, where a step's products are 16 times as long, between twice as many.
-// (Backward at M = 256, N = K = 4096 bf16: 48 us with 512, 74 us with 256;
-// forward 19 us with 256, 23 us with 512.)
+// all steps.  One product is shared between 256 workgroups (in bf16 three steps
+// ahead of its products where a unit has one); two products between 512, but two
+// in fp32 of 64 x 64 tiles, whose blocks are of unlike length and few, between
+// 1024.  (Backward at M = 256, N = K = 4096 bf16: 48 us with 512, 74 us with 256;
+// forward 19 us with 256, 23 us with 512.  fp32 forward at 2048 x 2048 x 512 45 us
+// with 256, 56 with 512; backward at 1300 x 1288 x 1288 115 us with 512, 131 with
+// 1024, at 1021 x 777 x 521 46 with 512, 42 with 1024.)
 Plan plan_of(const Size *sz, int n, bool f32, bool direct) {
     int64_t t128 = 0, t256 = 0;
     const int64_t bk = f32 ? 32 : 64;
@@ -832,13 +882,13 @@ Plan plan_of(const Size *sz, int n, bool f32, bool direct) {
     int64_t work = 0;
     for (int g = 0; g < n; ++g)
         work += ceil_div(sz[g].M, edge) * ceil_div(sz[g].N, edge) * (ceil_div(sz[g].C, bk) + 4);
-    int64_t share = ceil_div(work, p.large ? 256 : (f32 ? 512 : 256) * n);
+    int64_t share = ceil_div(work, p.large ? 256 : f32 && p.fine && n == 2 ? 1024 : 256 * n);
     if (share < kLeastSteps) share = kLeastSteps;
     for (int g = 0; g < n; ++g) {
         p.tiles_m[g] = (int)ceil_div(sz[g].M, edge);
         p.tiles_n[g] = (int)ceil_div(sz[g].N, edge);
         const int64_t all = ceil_div(sz[g].C, bk);
-        const int64_t splits = all * 2 > share * 3 ? ceil_div(all, share) : 1;
+        const int64_t splits = all * 2 > share * 3 && all >= 3 * kLeastSteps ? ceil_div(all, share) : 1;
         const int64_t steps = all > 0 ? ceil_div(all, splits) : 1;
         p.c_per_split[g] = (int)(steps * bk);
         p.splits[g] = all > 0 ? (int)ceil_div(all, steps) : 1;
@@ -848,6 +898,15 @@ Plan plan_of(const Size *sz, int n, bool f32, bool direct) {
     p.deep = direct && (p.fine ? !f32 && n == 1 : !p.large && p.blocks[0] + p.blocks[1] <= 256);
     return p;
 }
+
+// Products from which on padded rows are worth a launch (see pad_rows), measured
+// against the way through registers.  Forward: 1300 x 1291 x 1293 (2.2e9) fp32 63
+// against 67 us but bf16 25 against 21, 4091 x 2045 x 2045 (1.7e10) bf16 55 against
+// 64.  Backward: 1300 x 1291 x 1293 bf16 37 against 51 us, 1021 x 777 x 521 (4e8)
+// fp32 40 against 38; in a launch that is there anyway 41 against 45, and bf16 24
+// against 31.
+constexpr double pad_forward(bool f32) { return f32 ? 2e9 : 7e9; }
+constexpr double kPadBackward = 1e9;
 
 // Workspace for the partial sums, whatever the operands' alignment.
 int64_t partial_bytes(const Size *sz, int n, bool f32) {
@@ -860,6 +919,39 @@ int64_t partial_bytes(const Size *sz, int n, bool f32) {
 // none across its edge, offsets inside a tile below 2^31.
 bool direct_ok(const void *p, int64_t ld, int64_t row, int64_t eb) {
     return aligned(p, 16) && (ld * eb) % 16 == 0 && (row * eb) % 16 == 0 && ld < (int64_t)1 << 21;
+}
+
+// Elements of n rounded up to whole 16 bytes.
+int64_t whole(int64_t n, int64_t eb) { return ceil_div(n * eb, 16) * 16 / eb; }
+
+// Whether rows of K values are padded for the products: where they are no whole
+// 16 bytes, and the product is long enough to earn the copies (`least` products).
+bool pad_rows(int64_t M, int64_t N, int64_t K, int64_t eb, double least) {
+    const int64_t pitch = whole(K, eb), rows = M > N ? M : N;
+    return pitch != K && pitch < (int64_t)1 << 21 && rows * (pitch * eb / 16) < (int64_t)1 << 31 &&
+           (double)M * (double)N * (double)K >= least;
+}
+
+// Adds [rows, n] at `from` to the pads: at `at` from now on.
+void add_pad(Pads &p, int g, const void *&from, int64_t &ld, int64_t rows, int64_t n, int64_t eb, char *&at) {
+    p.from[g] = from, p.to[g] = at, p.ld[g] = ld, p.rows[g] = (uint32_t)rows;
+    p.n = (uint32_t)n;
+    ld = whole(n, eb);
+    p.chunks = (uint32_t)(ld * eb / 16);
+    from = at;
+    at += rows * ld * eb;
+}
+
+template <bool F32> int launch_dz(const DzParams &p, int act, hipStream_t stream) {
+    int64_t copies = 0;  // blocks, four chunks a thread or more
+    for (int g = 0; g < 2; ++g)
+        if (p.pads.from[g]) copies += ceil_div((int64_t)p.pads.rows[g] * p.pads.chunks, 1024);
+    const int64_t x = ceil_div(p.N, 128), y = ceil_div(copies < 2048 ? copies : 2048, x);
+    const dim3 grid((unsigned)x, (unsigned)(p.row_blocks + y));
+#define DZ(ACT) hipLaunchKernelGGL((dz_kernel<F32, ACT>), grid, dim3(256), 0, stream, p);
+    FOR_ACT(act, DZ)
+#undef DZ
+    return launch_status();
 }
 
 GemmParams gemm_params(const Plan &pl, int g, const Size &sz, const void *a, int64_t lda, const void *b, int64_t ldb,
@@ -910,11 +1002,21 @@ int linear_fwd(const void *x, int64_t ldx, const void *w, int64_t M, int64_t N, 
         return launch_status();
     }
     const Size sz = {M, N, K};
-    const bool direct = direct_ok(x, ldx, K, eb) && direct_ok(w, K, K, eb);
+    bool direct = direct_ok(x, ldx, K, eb) && direct_ok(w, K, K, eb);
+    int64_t ldw = K;
+    char *at = (char *)ws;
+    if (pad_rows(M, N, K, eb, pad_forward(F32))) {
+        DzParams p = {};
+        p.N = (int)N;
+        add_pad(p.pads, 0, x, ldx, M, K, eb, at);
+        add_pad(p.pads, 1, w, ldw, N, K, eb, at);
+        const int st = launch_dz<F32>(p, HYENA_ACT_NONE, stream);
+        if (st != HYENA_OK) return st;
+        direct = true;
+    }
     const Plan pl = plan_of(&sz, 1, F32, direct);
     if (pl.blocks[0] > 0x7fffffff) return HYENA_ERR_UNSUPPORTED;
-    char *at = (char *)ws;
-    const GemmParams p = gemm_params(pl, 0, sz, x, ldx, w, K, e, at);
+    const GemmParams p = gemm_params(pl, 0, sz, x, ldx, w, ldw, e, at);
     const dim3 grid((unsigned)pl.blocks[0]);
     if (pl.large) {
         if constexpr (!F32) hipLaunchKernelGGL((fwd_kernel<F32, true, Large>), grid, dim3(Large::NT), 0, stream, p);
@@ -941,14 +1043,25 @@ int64_t dz_blocks(int64_t M, int64_t N) {
     return blocks < most ? blocks : most;
 }
 
-// Workspace of the backward: dz, the column sums, the products' partial sums.
+// Workspace of the forward: padded x and w, partial sums.
+int64_t fwd_space(int64_t M, int64_t N, int64_t K, bool f32) {
+    if (N == 0 || few_rows(M, N, K)) return 0;
+    const int64_t eb = f32 ? 4 : 2;
+    const Size sz = {M, N, K};
+    return (pad_rows(M, N, K, eb, pad_forward(f32)) ? (M + N) * whole(K, eb) * eb : 0) + partial_bytes(&sz, 1, f32);
+}
+
+// Workspace of the backward: dz, the column sums, padded x and w, the products'
+// partial sums.
 struct BwdSpace {
-    int64_t dz, sums, partial;
+    int64_t dz, sums, pads, partial;
 };
 BwdSpace bwd_space(int64_t M, int64_t N, int64_t K, int act, int dtype) {
     const bool f32 = dtype == HYENA_DTYPE_F32;
+    const int64_t eb = f32 ? 4 : 2;
     BwdSpace s = {};
-    if (act != HYENA_ACT_NONE) s.dz = (M * N * (f32 ? 4 : 2) + 15) / 16 * 16;
+    if (act != HYENA_ACT_NONE || pad_rows(M, K, N, eb, 0)) s.dz = M * whole(N, eb) * eb;
+    if (pad_rows(M, N, K, eb, 0)) s.pads = (M + N) * whole(K, eb) * eb;
     if (M == 0 || N == 0) return s;
     s.sums = (dz_blocks(M, N) * N * 4 + 15) / 16 * 16;
     if (K == 0) return s;
@@ -967,38 +1080,43 @@ int linear_bwd(const void *x, const void *w, const void *z, const void *dy, int6
     if (M == 0 || K == 0) dx = nullptr;
     if (N == 0 || K == 0) dw = nullptr;
     if (N == 0) db = nullptr;
-    const void *dz = dy;
-    int64_t lddz = lddy;
-    void *made = nullptr;
-    if (act != HYENA_ACT_NONE && (dx || dw) && M > 0 && N > 0) {
-        dz = made = ws;
-        lddz = N;
-    }
+    const bool products = (dx || dw) && M > 0 && N > 0;
+    // Padded rows earn their copies where there is a launch for dz or db anyway.
+    const double least = act != HYENA_ACT_NONE || db ? 0 : kPadBackward;
+    const bool pad = products && pad_rows(M, N, K, eb, least);
+    const bool x_ok = !dw || pad || direct_ok(x, ldx, K, eb), w_ok = !dx || pad || direct_ok(w, K, K, eb);
+    const bool make = products && (act != HYENA_ACT_NONE || (x_ok && w_ok && pad_rows(M, K, N, eb, least)));
+    const bool direct = x_ok && w_ok && (make ? direct_ok(ws, whole(N, eb), whole(N, eb), eb) : direct_ok(dy, lddy, N, eb));
+    const void *dz = make ? ws : dy;
+    const int64_t lddz = make ? whole(N, eb) : lddy;
+    int64_t ldw = K;
     const int64_t row_blocks = M > 0 && N > 0 ? dz_blocks(M, N) : 0;
     float *sums = (float *)(ws + sp.dz);
     int st = HYENA_OK;
-    if ((made || db) && row_blocks > 0) {
-        DzParams p = {};
-        p.dy = dy, p.z = z, p.dz = made, p.sums = db ? sums : nullptr, p.M = M, p.lddy = lddy, p.N = (int)N;
-        p.rows = (int)ceil_div(M, row_blocks);
-        const dim3 grid((unsigned)ceil_div(N, 128), (unsigned)row_blocks);
-#define DZ(ACT) hipLaunchKernelGGL((dz_kernel<F32, ACT>), grid, dim3(256), 0, stream, p);
-        FOR_ACT(act, DZ)
-#undef DZ
-        if ((st = launch_status()) != HYENA_OK) return st;
+    DzParams d = {};
+    d.N = (int)N;
+    if (pad && direct) {
+        char *at = ws + sp.dz + sp.sums;
+        if (dw) add_pad(d.pads, 0, x, ldx, M, K, eb, at);
+        if (dx) add_pad(d.pads, 1, w, ldw, N, K, eb, at);
     }
+    if ((make || db) && row_blocks > 0) {
+        d.dy = dy, d.z = z, d.dz = make ? ws : nullptr, d.sums = db ? sums : nullptr;
+        d.M = M, d.lddy = lddy, d.lddz = lddz;
+        d.rows = (int)ceil_div(M, row_blocks), d.row_blocks = (unsigned)row_blocks;
+    }
+    if ((d.row_blocks > 0 || d.pads.from[0] || d.pads.from[1]) && (st = launch_dz<F32>(d, act, stream)) != HYENA_OK)
+        return st;
     Size sz[2];
     GemmParams g[2] = {};
     int n = 0;
     if (dw) sz[n++] = Size{N, K, M};
     if (dx) sz[n++] = Size{M, K, N};
     if (n > 0) {
-        const bool direct = direct_ok(dz, lddz, N, eb) && (!dx || direct_ok(w, K, K, eb)) &&
-                            (!dw || direct_ok(x, ldx, K, eb));
         const Plan pl = plan_of(sz, n, F32, direct);
         const int64_t blocks = pl.blocks[0] + pl.blocks[1];
         if (blocks > 0x7fffffff) return HYENA_ERR_UNSUPPORTED;
-        char *at = ws + sp.dz + sp.sums;
+        char *at = ws + sp.dz + sp.sums + sp.pads;
         Epilogue e = {};
         int i = 0;
         if (dw) {
@@ -1008,7 +1126,7 @@ int linear_bwd(const void *x, const void *w, const void *z, const void *dy, int6
         }
         if (dx) {
             e.y = dx, e.ldy = lddx;
-            g[i] = gemm_params(pl, i, sz[i], dz, lddz, w, K, e, at);
+            g[i] = gemm_params(pl, i, sz[i], dz, lddz, w, ldw, e, at);
         }
         const int first = dw ? (int)pl.blocks[0] : 0;
         const GemmParams &second = g[n - 1];
@@ -1045,7 +1163,7 @@ int check_linear(int64_t M, int64_t N, int64_t K, int act, int dtype) {
     if (dtype != HYENA_DTYPE_BF16 && dtype != HYENA_DTYPE_F32) return HYENA_ERR_DTYPE;
     if (act < HYENA_ACT_NONE || act > HYENA_ACT_SIGMOID) return HYENA_ERR_UNSUPPORTED;
     int64_t n;
-    if (!mul_fits(M, N, 4, &n) || !mul_fits(M, K, 4, &n) || !mul_fits(N, K, 4, &n)) return HYENA_ERR_SHAPE;
+    if (!mul_fits(M, N, 64, &n) || !mul_fits(M, K, 64, &n) || !mul_fits(N, K, 64, &n)) return HYENA_ERR_SHAPE;
     const int64_t most = ((int64_t)1 << 31) - 1024;  // tile coordinates are 32 bits
     if (M > most || N > most || K > most) return HYENA_ERR_SHAPE;
     return HYENA_OK;
@@ -1064,10 +1182,9 @@ int hyena_linear_workspace(int64_t M, int64_t N, int64_t K, int act, int dtype, 
     if (!bytes_out) return HYENA_ERR_NULL;
     if (backward) {
         const BwdSpace s = bwd_space(M, N, K, act, dtype);
-        *bytes_out = s.dz + s.sums + s.partial;
+        *bytes_out = s.dz + s.sums + s.pads + s.partial;
     } else {
-        const Size sz = {M, N, K};
-        *bytes_out = N > 0 && !few_rows(M, N, K) ? partial_bytes(&sz, 1, dtype == HYENA_DTYPE_F32) : 0;
+        *bytes_out = fwd_space(M, N, K, dtype == HYENA_DTYPE_F32);
     }
     return HYENA_OK;
 }

@@ -52,7 +52,7 @@ SHAPES = [(1, 1, 1), (1, 64, 64), (1, 4096, 512), (2, 17, 33), (3, 100, 8), (5, 
           (15, 48, 40), (16, 64, 96), (17, 80, 72), (33, 130, 264), (48, 512, 520), (64, 64, 64), (65, 72, 136),
           (100, 200, 300), (127, 129, 131), (128, 128, 128), (200, 264, 1032), (256, 256, 64), (257, 520, 200),
           (300, 1, 50), (1000, 72, 24), (513, 385, 96), (4, 72, 2056), (16, 100, 4100), (8, 4100, 2056),
-          (24, 64, 1032), (31, 8200, 40), (32, 128, 1024)]
+          (24, 64, 1032), (31, 8200, 40), (32, 128, 1024), (2100, 1900, 1801)]
 
 
 @pytest.mark.parametrize("shape", SHAPES, ids=str)
@@ -73,6 +73,32 @@ def test_epilogues(act, bias, residual, M):
     t = inputs(M, 136, 72, BF16, 7)
     z = check_fwd(t, act, bias, residual, "fwd")
     check_bwd(t, z, act, "bwd")
+
+
+@pytest.mark.parametrize("N,K", [(451, 463), (451, 464), (456, 463)])
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("act,db", [("none", False), ("none", True), ("gelu", False)])
+def test_odd_rows(N, K, dtype, act, db):
+    """Rows of no whole 16 bytes, inside wider buffers of NaN; workspaces of NaN."""
+    M = 500 if act != "none" or db else 5000  # (copies pay off later where they are a launch of their own)
+    t = inputs(M, N, K, dtype, 9)
+
+    def wide(v):
+        big = torch.full((v.shape[0], v.shape[1] + 13), float("nan"), dtype=dtype, device=DEV)
+        big[:, 5:5 + v.shape[1]] = v
+        return big[:, 5:5 + v.shape[1]]
+
+    z = check_fwd(t, act, True, False, "fwd")
+    ws = torch.full((hc.linear_workspace_bytes(M, N, K, act, 0 if dtype == BF16 else 1, True),), 255,
+                    dtype=torch.uint8, device=DEV)
+    want = check_bwd(t, z, act, "bwd", need_db=db, workspace=ws)
+    for need in ((1, 0), (0, 1)):
+        check_bwd(t, z, act, "bwd", need_dx=bool(need[0]), need_dw=bool(need[1]), need_db=db, workspace=ws.fill_(255))
+    t["x"], t["dy"] = wide(t["x"]), wide(t["dy"])
+    check_fwd(t, act, False, True, "fwd strided")
+    check_bwd(t, z, act, "bwd strided", need_db=db, workspace=ws.fill_(255))
+    for v in want[:2]:
+        assert torch.isfinite(v).all()
 
 
 @pytest.mark.parametrize("need", [(1, 0, 0), (0, 1, 0), (0, 0, 1), (1, 1, 0), (0, 1, 1), (0, 0, 0)])
