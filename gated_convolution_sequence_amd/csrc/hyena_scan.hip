@@ -189,8 +189,9 @@ template <typename G> struct Place {
     }
 };
 
-// Rows past the end: a gate of exactly 1 and products of 0, so that they pass
-// the state on unchanged.
+// The gate of rows past the end, exactly 1.  Both factors of their products are
+// cleared with it (the row they were read from may hold infinities), so that
+// they pass the state and its gradient on unchanged.
 template <bool F32, bool LOG> __device__ inline typename Lane<F32>::raw open_gate() {
     constexpr uint32_t one = LOG ? 0u : F32 ? 0x7f800000u : 0x7f807f80u;  // exp(0) or sigmoid(+inf)
     return __builtin_bit_cast(typename Lane<F32>::raw, u32x4_t{one, one, one, one});
@@ -406,7 +407,7 @@ __global__ __launch_bounds__(BwdTile<F32>::NT, PART ? 2 : 3) void scan_bwd_kerne
         for (int r = 0; r < R; ++r)
             if (at.t0 + r >= p.L) {
                 g[r] = open_gate<F32, LOG>();
-                k[r] = q[r] = typename Ln::raw{};
+                k[r] = v[r] = q[r] = dy[r] = typename Ln::raw{};
             }
     }
 #pragma unroll
