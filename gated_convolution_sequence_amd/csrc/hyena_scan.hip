@@ -27,10 +27,15 @@
 // workgroup only waits for workgroups that have started before it and the
 // first unfinished one waits for none.
 //
-// A gate of exactly 0 drops the state, whatever it holds.  P is therefore kept
-// at 0 exactly where a run holds such a gate, and off 0 (at the least positive
-// fp32) where a product of small gates underflows.  A gate of NaN is not kept in
-// P, which fmaxf would lose: S is NaN then, also where the run starts with it.
+// P is held as m 2^e with an exponent of its own: over a tile it leaves the range
+// of fp32 in ordinary use (128 gates of 0.5), and what it then makes of a large
+// state, or with gates above 1 (gate "log", g > 0) of a small one, still counts.
+//
+// A gate of exactly 0 drops the state, whatever it holds: m is 0 exactly where a
+// run holds such a gate.  A gate of NaN is not kept in m, which fmaxf would lose:
+// S is NaN then, also where the run starts with it.
+
+#include <float.h>
 
 #include <type_traits>
 
@@ -47,7 +52,7 @@ constexpr int kWindow = 8;
 constexpr int kMostCounters = 32;
 constexpr int kCounterGap = 32;  // counters lie on lines of their own
 constexpr uint32_t kEmpty = 0xffffffffu;  // high half of a word not yet written
-constexpr uint32_t kState = 0x80000000u;  // high half of a word that holds a state (a map has P >= 0 there)
+constexpr uint32_t kState = 0xff800000u;  // high half of a word that holds a state (a map's exponent is less)
 
 struct ScanParams {
     const void *q, *k, *v, *g, *dy;
@@ -62,13 +67,41 @@ struct ScanParams {
     uint64_t *words;           // [n_tiles][B][c_tiles * C]
 };
 
-// P of a run that holds no gate of 0 (least = its smallest gate).
-__device__ inline float keep_off_zero(float P, float least) {
-    return least == 0.0f ? 0.0f : fmaxf(P, __uint_as_float(1u));
+// A product of decays.
+struct Decay {
+    float m;  // 0, or finite and positive
+    int e;    // of 2
+};
+
+// A run's gates lie between least and most.  Within these bounds the product P
+// of a lane's rows (at most 8) is exact to rounding as it is.
+__device__ inline bool plain(float least, float most) { return least >= 0x1p-15f && most <= 0x1p+15f; }
+
+// m of a run that holds no gate of 0 (least = its smallest gate).
+__device__ inline float keep_off_zero(float m, float least) {
+    return least == 0.0f ? 0.0f : fminf(fmaxf(m, __uint_as_float(1u)), FLT_MAX);
 }
-__device__ inline float apply(float P, float S, float s) { return P == 0.0f ? S : fmaf(P, s, S); }
-__device__ inline float join(float P1, float P2) {
-    return P1 == 0.0f || P2 == 0.0f ? 0.0f : fmaxf(P1 * P2, __uint_as_float(1u));
+
+// s through a row, and through a run.
+__device__ inline float apply(float a, float x, float s) { return a == 0.0f ? x : fmaf(a, s, x); }
+__device__ inline float apply(Decay P, float S, float s) {
+    return P.m == 0.0f ? S : S + __builtin_amdgcn_ldexpf(P.m * s, P.e);
+}
+
+// P with m in [0.5, 1), or 0.
+__device__ inline Decay normal(Decay P) {
+    return {__builtin_amdgcn_frexp_mantf(P.m), P.e + __builtin_amdgcn_frexp_expf(P.m)};
+}
+
+// P in the high half of a word: 9 bits of exponent (from 2^-254 to 2^254: past
+// them it takes every fp32 to nothing or past the largest) and m's 23 bits.
+__device__ inline uint32_t pack(Decay P) {
+    const Decay n = normal(P);
+    const uint32_t e = (uint32_t)(max(-254, min(254, n.e)) + 256);
+    return n.m == 0.0f ? 0u : e << 23 | (__float_as_uint(n.m) & 0x7fffffu);
+}
+__device__ inline Decay unpack(uint32_t hi) {
+    return {hi == 0 ? 0.0f : __uint_as_float((hi & 0x7fffffu) | 0x3f000000u), (int)(hi >> 23) - 256};
 }
 
 // The state after a run's first row, taken from 0: x, or NaN where the gate is.
@@ -101,7 +134,7 @@ __device__ inline float carry_in(uint64_t *words, int64_t stride, int64_t m, flo
             } else if (hi == kEmpty) {
                 known = false;
             } else {
-                s = apply(__uint_as_float(hi), lo, s);
+                s = apply(unpack(hi), lo, s);
             }
         }
         if (known) return s;
@@ -211,7 +244,8 @@ __global__ __launch_bounds__(FwdTile<F32>::NT, 2) void scan_fwd_kernel(ScanParam
     using G = FwdTile<F32>;
     using Ln = Lane<F32>;
     constexpr int VEC = G::VEC, R = G::R, NS = G::NS, C = G::C;
-    __shared__ float sP[NS][C], sS[NS][C], sIn[C];
+    __shared__ float sM[NS][C], sS[NS][C], sIn[C];
+    __shared__ int sE[NS][C];
     __shared__ int64_t sTicket;
 
     if (threadIdx.x == 0) sTicket = next_ticket(p);
@@ -265,7 +299,8 @@ __global__ __launch_bounds__(FwdTile<F32>::NT, 2) void scan_fwd_kernel(ScanParam
 #pragma unroll
         for (int r = 0; r < R; ++r) q[r] = Ln::load_part(p.q, at.row(p, r) * p.ld + at.d0, at.n_ch);
     }
-    float P[VEC], S[VEC], least[VEC], least_of_all = 1.0f;
+    float P[VEC], S[VEC], least[VEC], least_of_all = 1.0f, most = 1.0f;
+    int e[VEC] = {};
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
         least[i] = P[i] = a[0][i];
@@ -275,8 +310,24 @@ __global__ __launch_bounds__(FwdTile<F32>::NT, 2) void scan_fwd_kernel(ScanParam
             least[i] = fminf(least[i], a[r][i]);
         }
         least_of_all = fminf(least_of_all, least[i]);
+        if constexpr (LOG) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) most = fmaxf(most, a[r][i]);
+        }
     }
-    const bool resets = any_lane(least_of_all == 0.0f);
+    bool resets = false;
+    if (any_lane(!plain(least_of_all, most))) {
+        resets = any_lane(least_of_all == 0.0f);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            P[i] = 1.0f;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                P[i] *= __builtin_amdgcn_frexp_mantf(a[r][i]);
+                e[i] += __builtin_amdgcn_frexp_expf(a[r][i]);
+            }
+        }
+    }
     auto compose = [&](auto sel) {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
@@ -289,7 +340,8 @@ __global__ __launch_bounds__(FwdTile<F32>::NT, 2) void scan_fwd_kernel(ScanParam
     else compose(std::false_type());
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
-        sP[slice][lane * VEC + i] = keep_off_zero(P[i], least[i]);
+        sM[slice][lane * VEC + i] = keep_off_zero(P[i], least[i]);
+        sE[slice][lane * VEC + i] = e[i];
         sS[slice][lane * VEC + i] = S[i];
     }
     lds_barrier();
@@ -298,19 +350,23 @@ __global__ __launch_bounds__(FwdTile<F32>::NT, 2) void scan_fwd_kernel(ScanParam
     if (threadIdx.x < C) {
         const int c = threadIdx.x;
         const int64_t d = at.ct * C + c;
-        float P = 1.0f, S = 0.0f;
+        Decay P = {1.0f, 0};
+        float S = 0.0f;
 #pragma unroll
         for (int j = 0; j < NS; ++j) {
-            const float pj = sP[j][c], sj = sS[j][c];
-            sP[j][c] = P, sS[j][c] = S;
-            P = join(P, pj), S = apply(pj, sj, S);
+            const Decay pj = normal({sM[j][c], sE[j][c]});
+            const float sj = sS[j][c];
+            sM[j][c] = P.m, sE[j][c] = P.e, sS[j][c] = S;
+            P.m *= pj.m, P.e += pj.e, S = apply(pj, sj, S);
         }
+        const uint32_t word = pack(P);
+        P = unpack(word);  // as the tiles after this one see it
         float in = p.s0 && d < p.D ? p.s0[at.b * p.D + d] : 0.0f;
         if (p.counters) {
             const int64_t pitch = p.c_tiles * C, stride = p.B * pitch;
             uint64_t *words = p.words + at.b * pitch + at.ct * C + c;
             if (at.m > 0) {
-                if (at.m + 1 < p.n_tiles) put_word(words + at.m * stride, __float_as_uint(P), S);
+                if (at.m + 1 < p.n_tiles) put_word(words + at.m * stride, word, S);
                 in = carry_in(words, stride, at.m, in);
             }
             if (at.m + 1 < p.n_tiles) put_word(words + at.m * stride, kState, apply(P, S, in));
@@ -326,7 +382,7 @@ __global__ __launch_bounds__(FwdTile<F32>::NT, 2) void scan_fwd_kernel(ScanParam
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
         const int c = lane * VEC + i;
-        s[i] = apply(sP[slice][c], sS[slice][c], sIn[c]);
+        s[i] = apply(Decay{sM[slice][c], sE[slice][c]}, sS[slice][c], sIn[c]);
     }
     if (p.states && at.t0 % kStateRows == 0 && at.t0 < p.L) {
         const int64_t chunks = ceil_div(p.L, kStateRows);
@@ -368,7 +424,8 @@ __global__ __launch_bounds__(BwdTile<F32>::NT, PART ? 2 : 3) void scan_bwd_kerne
     using G = BwdTile<F32>;
     using Ln = Lane<F32>;
     constexpr int VEC = G::VEC, R = G::R, NS = G::NS, C = G::C;
-    __shared__ float sP[NS][C], sS[NS][C], sC[NS][C], sIn[C];
+    __shared__ float sM[NS][C], sS[NS][C], sC[NS][C], sIn[C];
+    __shared__ int sE[NS][C];
     __shared__ int64_t sTicket;
 
     if (threadIdx.x == 0) sTicket = next_ticket(p);
@@ -412,12 +469,22 @@ __global__ __launch_bounds__(BwdTile<F32>::NT, PART ? 2 : 3) void scan_bwd_kerne
     }
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
-        float a[R], P, least, S, c = 0.0f;
+        float a[R], P, least, most = 1.0f, S, c = 0.0f;
+        int e = 0;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             a[r] = decay<LOG>(Ln::get(g[r], i));
             P = r == 0 ? a[0] : P * a[r];
             least = r == 0 ? a[0] : fminf(least, a[r]);
+            if (LOG) most = fmaxf(most, a[r]);
+        }
+        if (any_lane(!plain(least, most))) {
+            P = 1.0f;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                P *= __builtin_amdgcn_frexp_mantf(a[r]);
+                e += __builtin_amdgcn_frexp_expf(a[r]);
+            }
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -426,7 +493,8 @@ __global__ __launch_bounds__(BwdTile<F32>::NT, PART ? 2 : 3) void scan_bwd_kerne
         }
 #pragma unroll
         for (int r = R - 1; r >= 0; --r) c = apply(a[r], 0.0f, fmaf(Ln::get(q[r], i), Ln::get(dy[r], i), c));
-        sP[slice][lane * VEC + i] = keep_off_zero(P, least);
+        sM[slice][lane * VEC + i] = keep_off_zero(P, least);
+        sE[slice][lane * VEC + i] = e;
         sS[slice][lane * VEC + i] = S;
         sC[slice][lane * VEC + i] = c;
     }
@@ -436,17 +504,20 @@ __global__ __launch_bounds__(BwdTile<F32>::NT, PART ? 2 : 3) void scan_bwd_kerne
         const int c = threadIdx.x;
         const int64_t d = at.ct * C + c;
         // the maps from the tile's end back to the end of each slice
-        float P = 1.0f, S = 0.0f, pj[NS];
+        Decay P = {1.0f, 0}, pj[NS];
+        float S = 0.0f;
 #pragma unroll
         for (int j = NS - 1; j >= 0; --j) {
-            pj[j] = sP[j][c];
+            pj[j] = normal({sM[j][c], sE[j][c]});
             const float cj = sC[j][c];
-            sP[j][c] = P, sC[j][c] = S;
-            P = join(P, pj[j]), S = apply(pj[j], cj, S);
+            sM[j][c] = P.m, sE[j][c] = P.e, sC[j][c] = S;
+            P.m *= pj[j].m, P.e += pj[j].e, S = apply(pj[j], cj, S);
         }
+        const uint32_t word = pack(P);
+        P = unpack(word);  // as the tiles after this one see it
         const int64_t pitch = p.c_tiles * C, stride = p.B * pitch;
         uint64_t *words = p.words + at.b * pitch + at.ct * C + c;
-        if (p.counters && at.m > 0 && at.m + 1 < p.n_tiles) put_word(words + at.m * stride, __float_as_uint(P), S);
+        if (p.counters && at.m > 0 && at.m + 1 < p.n_tiles) put_word(words + at.m * stride, word, S);
         // the state that enters each slice
         float s = 0.0f;
         if (d < p.D) s = p.states_in[(at.b * ceil_div(p.L, kStateRows) + n * (G::T / kStateRows)) * p.D + d];
@@ -486,7 +557,7 @@ __global__ __launch_bounds__(BwdTile<F32>::NT, PART ? 2 : 3) void scan_bwd_kerne
                 a[r] = decay<LOG>(Ln::get(g[r], i));
                 s[r + 1] = apply(a[r], Ln::get(k[r], i) * Ln::get(v[r], i), s[r]);
             }
-            float c = apply(sP[slice][ch], sC[slice][ch], sIn[ch]);
+            float c = apply(Decay{sM[slice][ch], sE[slice][ch]}, sC[slice][ch], sIn[ch]);
 #pragma unroll
             for (int r = R - 1; r >= 0; --r) {
                 const float dyi = Ln::get(dy[r], i), ds = fmaf(Ln::get(q[r], i), dyi, c);

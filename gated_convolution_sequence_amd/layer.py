@@ -225,7 +225,8 @@ def scan_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
     q, k, v, g: [B, L, D] (bf16 or fp32, all alike), rows contiguous and at one
     row stride for the four: separate contiguous tensors or column slices of
     one [B, L, 4 D] projection.  gate: "sigmoid" (a = sigmoid(g)) or "log"
-    (a = exp(g)); g = -inf starts afresh from that row.  s0: [B, D] fp32 state
+    (a = exp(g), also above 1; exp(g) and the states have to fit fp32); g = -inf
+    starts afresh from that row.  s0: [B, D] fp32 state
     before row 0 (None: zero).  s_last: [B, D] fp32.  states: with
     ``save_states`` the fp32 states before rows 0, 64, 128, ... that scan_bwd
     takes, else None.  ``workspace`` (uint8) is allocated here if not given.

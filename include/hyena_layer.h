@@ -53,7 +53,8 @@ extern "C" {
  * y is rounded once. */
 enum hyena_gate {
     HYENA_GATE_SIGMOID = 0, /* a = 1 / (1 + exp(-g)) */
-    HYENA_GATE_LOG = 1      /* a = exp(g), g <= 0 for a decay (not checked) */
+    HYENA_GATE_LOG = 1      /* a = exp(g): a decay for g <= 0, growth above; exp(g), the
+                               states and their gradients have to fit fp32 */
 };
 
 /* Forward.  s0 may be NULL (zero).  Any of y, s_last, states may be NULL (not
