@@ -18,6 +18,8 @@ from typing import Optional, Sequence
 
 import torch
 
+from ._autograd import first_order
+
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LAYER_LIB_PATH = os.path.join(_PKG, "libhyena_layer.so")
 
@@ -316,18 +318,19 @@ def scan_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor
 
 
 class GatedScan(torch.autograd.Function):
-    """Autograd wrapper: y, s_last = GatedScan.apply(q, k, v, g, gate, s0)."""
+    """Autograd wrapper: y, s_last = GatedScan.apply(q, k, v, g, gate, s0).  No second derivatives: they raise."""
 
     @staticmethod
     def forward(ctx, q, k, v, g, gate="sigmoid", s0=None):
         y, s_last, states = scan_fwd(q, k, v, g, gate=gate, s0=s0, save_states=True)
-        ctx.save_for_backward(q, k, v, g, states)
+        ctx.save_for_backward(q, k, v, g, states, s0)
         ctx.gate = gate
         return y, s_last
 
     @staticmethod
+    @first_order
     def backward(ctx, dy, ds_last):
-        q, k, v, g, states = ctx.saved_tensors
+        q, k, v, g, states, _ = ctx.saved_tensors
         need = ctx.needs_input_grad
         dq, dk, dv, dg, ds0 = scan_bwd(q, k, v, g, dy.contiguous(), states, gate=ctx.gate,
                                        ds_last=ds_last.contiguous())
@@ -503,18 +506,22 @@ def linear_bwd(x: torch.Tensor, w: torch.Tensor, dy: torch.Tensor, preact: Optio
 
 
 class LinearAct(torch.autograd.Function):
-    """Autograd wrapper: y = LinearAct.apply(x, w, bias, residual, act); bias and residual may be None."""
+    """Autograd wrapper: y = LinearAct.apply(x, w, bias, residual, act); bias and residual may be None.
+
+    No second derivatives: they raise (the residual's gradient is the incoming one and keeps its graph).
+    """
 
     @staticmethod
     def forward(ctx, x, w, bias=None, residual=None, act="none"):
         y, z = linear_fwd(x, w, bias=bias, residual=residual, act=act, save_preact=act != "none")
-        ctx.save_for_backward(x, w, z)
+        ctx.save_for_backward(x, w, z, bias)
         ctx.act = act
         return y
 
     @staticmethod
+    @first_order
     def backward(ctx, dy):
-        x, w, z = ctx.saved_tensors
+        x, w, z, _ = ctx.saved_tensors
         need = ctx.needs_input_grad
         dx, dw, db = linear_bwd(x, w, dy.contiguous(), preact=z, act=ctx.act, need_dx=need[0], need_dw=need[1],
                                 need_db=len(need) > 2 and need[2])
