@@ -14,6 +14,8 @@ from typing import Optional
 
 import torch
 
+from ._autograd import first_order
+
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libhyena_conv.so")
 
@@ -379,7 +381,7 @@ class HyenaConv(torch.autograd.Function):
 
     Filters of up to MAX_DIRECT_TAPS taps run on the chunked kernels; longer
     ones on the FFT path (as HyenaConvLong).  The filter gradient comes back
-    in h's dtype (accumulated in fp32).
+    in h's dtype (accumulated in fp32).  No second derivatives: they raise.
     """
 
     @staticmethod
@@ -393,6 +395,7 @@ class HyenaConv(torch.autograd.Function):
         return conv_fwd(q, k, v, h, group_size)
 
     @staticmethod
+    @first_order
     def backward(ctx, dy):
         if ctx.long:
             return HyenaConvLong.backward(ctx, dy)
@@ -408,6 +411,7 @@ class HyenaConvLong(torch.autograd.Function):
     """Autograd wrapper of the long-filter (FFT) path: y = HyenaConvLong.apply(q, k, v, h, group_size).
 
     Any filter length; the filter gradient comes back in h's dtype (fp32 sums).
+    No second derivatives: they raise.
     The forward runs in a workspace of the backward's size, kept until the
     backward, which then reuses the filter spectra the forward left in it.
     """
@@ -422,6 +426,7 @@ class HyenaConvLong(torch.autograd.Function):
         return conv_fwd_long(q, k, v, h, group_size, workspace=ctx.workspace)
 
     @staticmethod
+    @first_order
     def backward(ctx, dy):
         q, k, v, h = ctx.saved_tensors
         need = ctx.needs_input_grad
