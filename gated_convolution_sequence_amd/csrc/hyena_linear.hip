@@ -1232,7 +1232,8 @@ int hyena_linear_bwd(const void *x, const void *w, const void *preact, const voi
     if (lddy < N || (dw && ldx < K) || (dx && lddx < K) || !mul_fits(M, lddy, eb, &n) ||
         (dw && !mul_fits(M, ldx, eb, &n)) || (dx && !mul_fits(M, lddx, eb, &n)))
         return HYENA_ERR_SHAPE;
-    if (!dx && !dw && !db) return HYENA_ERR_NULL;
+    // an output of no elements may be NULL, also where it is the only one wanted
+    if (!dx && !dw && !db) return M > 0 && N > 0 && K > 0 ? HYENA_ERR_NULL : HYENA_OK;
     const bool rows = M > 0 && N > 0;
     if (rows && (!dy || (act != HYENA_ACT_NONE && !preact) || (dx && K > 0 && !w) || (dw && K > 0 && !x)))
         return HYENA_ERR_NULL;

@@ -685,7 +685,7 @@ int hyena_scan_fwd(const void *q, const void *k, const void *v, const void *g, i
     int64_t n;
     if (ld < D || !mul_fits(B * L, ld, eb, &n)) return HYENA_ERR_SHAPE;
     if (B == 0 || D == 0) return HYENA_OK;
-    if (!y && !s_last && !states) return HYENA_ERR_NULL;
+    if (!y && !s_last && !states) return L > 0 ? HYENA_ERR_NULL : HYENA_OK;
     if (L > 0 && (!k || !v || !g || (y && !q))) return HYENA_ERR_NULL;
     if (!aligned(q, eb) || !aligned(k, eb) || !aligned(v, eb) || !aligned(g, eb) || !aligned(y, eb) ||
         !aligned(s0, 4) || !aligned(s_last, 4) || !aligned(states, 4) || !aligned(workspace, 16))
@@ -724,7 +724,7 @@ int hyena_scan_bwd(const void *q, const void *k, const void *v, const void *g, c
     int64_t n;
     if (ld < D || ldd < D || !mul_fits(B * L, ld, eb, &n) || !mul_fits(B * L, ldd, eb, &n)) return HYENA_ERR_SHAPE;
     if (B == 0 || D == 0) return HYENA_OK;
-    if (!dq && !dk && !dv && !dg && !ds0) return HYENA_ERR_NULL;
+    if (!dq && !dk && !dv && !dg && !ds0) return L > 0 ? HYENA_ERR_NULL : HYENA_OK;
     if (L > 0 && (!q || !k || !v || !g || !dy || !states)) return HYENA_ERR_NULL;
     if (!aligned(q, eb) || !aligned(k, eb) || !aligned(v, eb) || !aligned(g, eb) || !aligned(dy, eb) ||
         !aligned(dq, eb) || !aligned(dk, eb) || !aligned(dv, eb) || !aligned(dg, eb) || !aligned(states, 4) ||

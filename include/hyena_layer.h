@@ -15,9 +15,10 @@
  * default stream) and the call returns without waiting; argument checks run
  * on the host before any HIP call; outputs and workspaces must not overlap
  * inputs or each other (HYENA_ERR_ALIAS) except where a buffer is said to be
- * updated in place.  Calls that may run at the same time need workspaces of
- * their own.  Results are the same run to run.  The launches are kernels only,
- * so every call can be captured into a HIP graph.
+ * updated in place.  A pointer to no elements may be NULL.  Calls that may run
+ * at the same time need workspaces of their own.  Results are the same run to
+ * run.  The launches are kernels only, so every call can be captured into a HIP
+ * graph.
  *
  * Alignment: data pointers need the alignment of their elements (else
  * HYENA_ERR_ALIGN), and sizes and row strides are free.  Multiples of 16 bytes
