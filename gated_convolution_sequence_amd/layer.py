@@ -99,12 +99,12 @@ def _pick(table: dict, key: str, what: str) -> int:
 def _row_stride(t: torch.Tensor, name: str) -> Optional[int]:
     """Elements from one row of t ([..., n]) to the next; None where it has at most one row."""
     shape, stride = t.shape, t.stride()
+    if t.numel() == 0:
+        return None
     if shape[-1] > 1 and stride[-1] != 1:
         raise ValueError("%s must have contiguous rows" % name)
     ld, rows = None, 1
     for n, s in zip(shape[-2::-1], stride[-2::-1]):
-        if n == 0:
-            return None
         if n == 1:
             continue
         if ld is None:

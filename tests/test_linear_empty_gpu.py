@@ -26,3 +26,10 @@ def test_any_gradients_of_any_empty_size(M, N, K, need, act):
         assert torch.all(got[1] == 0)
     if need[2] and M == 0:
         assert torch.all(got[2] == 0)
+
+
+def test_an_empty_batch_with_frozen_weights():
+    x = torch.empty(0, 8, dtype=torch.bfloat16, device=DEV, requires_grad=True)
+    w = torch.randn(6, 8, device=DEV).to(torch.bfloat16)
+    hc.LinearAct.apply(x, w, None, None, "silu").sum().backward()
+    assert x.grad.shape == (0, 8)
