@@ -18,6 +18,7 @@ from typing import Optional, Sequence
 
 import torch
 
+from . import HyenaError  # the package imports this module last
 from ._autograd import first_order
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -36,12 +37,12 @@ _DTYPE_CODES = {torch.bfloat16: 0, torch.float32: 1}
 _lib = None
 
 
-class LayerError(RuntimeError):
-    """A status of the library other than HYENA_OK."""
+class LayerError(HyenaError):
+    """A status of the library other than HYENA_OK, with this library's text for it."""
 
     def __init__(self, status: int, where: str):
         self.status = status
-        super().__init__("%s: %s (%d)" % (where, layer_strerror(status), status))
+        RuntimeError.__init__(self, "%s: %s (%d)" % (where, layer_strerror(status), status))
 
 
 def layer_lib() -> ctypes.CDLL:
