@@ -500,7 +500,9 @@ template <bool F32, int WM, int WN, int MT, int NTL, int ST> struct Shape {
         const Epilogue &ep = p.e;
         float *partial = p.partial ? p.partial + (int64_t)split * p.M * p.N : nullptr;
         const auto bias = partial ? Pack<F32, 8>::zero() : bias_of<F32, 8>(ep, n);
-        __syncthreads();  // every wave is done with the operands
+        // Every wave is done with the operands, and its fills past the end of c have
+        // landed: the pieces lie where they go.
+        step_barrier<0>();
 #pragma unroll
         for (int g = 0; g < MT; g += G) {
             const int m = m0 + wm + g * 16 + r8;
