@@ -53,6 +53,7 @@ constexpr int kMostCounters = 32;
 constexpr int kCounterGap = 32;  // counters lie on lines of their own
 constexpr uint32_t kEmpty = 0xffffffffu;  // high half of a word not yet written
 constexpr uint32_t kState = 0xff800000u;  // high half of a word that holds a state (a map's exponent is less)
+constexpr uint32_t kInfinite = 0xff7fffffu;  // high half of a map whose P is infinite
 
 struct ScanParams {
     const void *q, *k, *v, *g, *dy;
@@ -69,7 +70,7 @@ struct ScanParams {
 
 // A product of decays.
 struct Decay {
-    float m;  // 0, or finite and positive
+    float m;  // 0 or positive; infinite where a gate of the run is
     int e;    // of 2
 };
 
@@ -79,7 +80,7 @@ __device__ inline bool plain(float least, float most) { return least >= 0x1p-15f
 
 // m of a run that holds no gate of 0 (least = its smallest gate).
 __device__ inline float keep_off_zero(float m, float least) {
-    return least == 0.0f ? 0.0f : fminf(fmaxf(m, __uint_as_float(1u)), FLT_MAX);
+    return least == 0.0f ? 0.0f : fmaxf(m, __uint_as_float(1u));
 }
 
 // s through a row, and through a run.
@@ -93,15 +94,24 @@ __device__ inline Decay normal(Decay P) {
     return {__builtin_amdgcn_frexp_mantf(P.m), P.e + __builtin_amdgcn_frexp_expf(P.m)};
 }
 
+// Both runs one after the other; b normal.
+template <bool LOG> __device__ inline Decay join(Decay a, Decay b) {
+    const bool drops = LOG && (a.m == 0.0f || b.m == 0.0f);  // (a gate of 0 and an infinite one)
+    return {drops ? 0.0f : a.m * b.m, a.e + b.e};
+}
+
 // P in the high half of a word: 9 bits of exponent (from 2^-254 to 2^254: past
 // them it takes every fp32 to nothing or past the largest) and m's 23 bits.
-__device__ inline uint32_t pack(Decay P) {
+template <bool LOG> __device__ inline uint32_t pack(Decay P) {
     const Decay n = normal(P);
     const uint32_t e = (uint32_t)(max(-254, min(254, n.e)) + 256);
+    if (LOG && n.m > FLT_MAX) return kInfinite;
     return n.m == 0.0f ? 0u : e << 23 | (__float_as_uint(n.m) & 0x7fffffu);
 }
-__device__ inline Decay unpack(uint32_t hi) {
-    return {hi == 0 ? 0.0f : __uint_as_float((hi & 0x7fffffu) | 0x3f000000u), (int)(hi >> 23) - 256};
+template <bool LOG> __device__ inline Decay unpack(uint32_t hi) {
+    Decay P = {hi == 0 ? 0.0f : __uint_as_float((hi & 0x7fffffu) | 0x3f000000u), (int)(hi >> 23) - 256};
+    if (LOG && hi == kInfinite) P.m = __uint_as_float(0x7f800000u);
+    return P;
 }
 
 // The state after a run's first row, taken from 0: x, or NaN where the gate is.
@@ -113,7 +123,7 @@ __device__ inline void put_word(uint64_t *w, uint32_t hi, float lo) {
 
 // The state that enters tile m of a chain whose words are `stride` apart;
 // `first` enters tile 0.
-__device__ inline float carry_in(uint64_t *words, int64_t stride, int64_t m, float first) {
+template <bool LOG> __device__ inline float carry_in(uint64_t *words, int64_t stride, int64_t m, float first) {
     for (;;) {
         uint64_t w[kWindow];
 #pragma unroll
@@ -134,7 +144,7 @@ __device__ inline float carry_in(uint64_t *words, int64_t stride, int64_t m, flo
             } else if (hi == kEmpty) {
                 known = false;
             } else {
-                s = apply(unpack(hi), lo, s);
+                s = apply(unpack<LOG>(hi), lo, s);
             }
         }
         if (known) return s;
@@ -357,17 +367,17 @@ __global__ __launch_bounds__(FwdTile<F32>::NT, 2) void scan_fwd_kernel(ScanParam
             const Decay pj = normal({sM[j][c], sE[j][c]});
             const float sj = sS[j][c];
             sM[j][c] = P.m, sE[j][c] = P.e, sS[j][c] = S;
-            P.m *= pj.m, P.e += pj.e, S = apply(pj, sj, S);
+            P = join<LOG>(P, pj), S = apply(pj, sj, S);
         }
-        const uint32_t word = pack(P);
-        P = unpack(word);  // as the tiles after this one see it
+        const uint32_t word = pack<LOG>(P);
+        P = unpack<LOG>(word);  // as the tiles after this one see it
         float in = p.s0 && d < p.D ? p.s0[at.b * p.D + d] : 0.0f;
         if (p.counters) {
             const int64_t pitch = p.c_tiles * C, stride = p.B * pitch;
             uint64_t *words = p.words + at.b * pitch + at.ct * C + c;
             if (at.m > 0) {
                 if (at.m + 1 < p.n_tiles) put_word(words + at.m * stride, word, S);
-                in = carry_in(words, stride, at.m, in);
+                in = carry_in<LOG>(words, stride, at.m, in);
             }
             if (at.m + 1 < p.n_tiles) put_word(words + at.m * stride, kState, apply(P, S, in));
         }
@@ -511,10 +521,10 @@ __global__ __launch_bounds__(BwdTile<F32>::NT, PART ? 2 : 3) void scan_bwd_kerne
             pj[j] = normal({sM[j][c], sE[j][c]});
             const float cj = sC[j][c];
             sM[j][c] = P.m, sE[j][c] = P.e, sC[j][c] = S;
-            P.m *= pj[j].m, P.e += pj[j].e, S = apply(pj[j], cj, S);
+            P = join<LOG>(P, pj[j]), S = apply(pj[j], cj, S);
         }
-        const uint32_t word = pack(P);
-        P = unpack(word);  // as the tiles after this one see it
+        const uint32_t word = pack<LOG>(P);
+        P = unpack<LOG>(word);  // as the tiles after this one see it
         const int64_t pitch = p.c_tiles * C, stride = p.B * pitch;
         uint64_t *words = p.words + at.b * pitch + at.ct * C + c;
         if (p.counters && at.m > 0 && at.m + 1 < p.n_tiles) put_word(words + at.m * stride, word, S);
@@ -529,7 +539,7 @@ __global__ __launch_bounds__(BwdTile<F32>::NT, PART ? 2 : 3) void scan_bwd_kerne
         }
         float in = p.ds_last && d < p.D ? p.ds_last[at.b * p.D + d] : 0.0f;
         if (p.counters) {
-            if (at.m > 0) in = carry_in(words, stride, at.m, in);
+            if (at.m > 0) in = carry_in<LOG>(words, stride, at.m, in);
             if (at.m + 1 < p.n_tiles) put_word(words + at.m * stride, kState, apply(P, S, in));
         }
         sIn[c] = in;

@@ -5,6 +5,7 @@ states themselves stay inside the range.  Inputs are scaled so that every output
 representable; the bounds are layer_ref's."""
 import math
 
+import numpy as np
 import pytest
 import torch
 
@@ -130,3 +131,42 @@ def test_a_large_state_under_small_gates(gate, g, dtype):
     s0, ds_last = s0 * 1e30, ds_last * 1e30
     _, _, states = check_fwd(ts, gate, s0, "fwd")
     check_bwd(ts, gate, s0, ds_last, states, "bwd")
+
+
+def check_finite(got, want, bound, dtype, what):
+    """As check, but what is not finite may be an infinity or NaN."""
+    fin = np.isfinite(want)
+    assert np.array_equal(fin, np.isfinite(to_np(got))), "%s: non-finite values differ" % what
+    check(torch.where(torch.from_numpy(fin).to(DEV), got, torch.zeros_like(got)), np.where(fin, want, 0.0), bound, dtype,
+          what)
+
+
+@pytest.mark.parametrize("D", [64, 9])
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("growing", [False, True])
+@pytest.mark.parametrize("with_state", [False, True])
+def test_an_infinite_gate(D, dtype, growing, with_state):
+    """exp(+inf): nothing finite up to a reset, and what does not depend on it is as it should be.
+
+    (Whether an infinity or NaN depends on the order of sums: inf (P s + S) is cut into inf s + inf.)"""
+    log("scan infinite gate D=%d %s" % (D, dtype))
+    ts = inputs(2, 500, D, dtype, "log", 12)
+    if growing:
+        ts[3].copy_(pattern("slow", 500)[0][None, :, None].to(DEV))
+    s0, ds_last = states_of(2, D, 12) if with_state else (None, None)
+    ts[3][0, 0, 1] = math.inf    # on the first state
+    ts[3][0, 128, 2] = math.inf  # in the first row of a tile, of a slice, and inside one
+    ts[3][0, 136, 3] = math.inf
+    ts[3][0, 205, 4] = math.inf
+    ts[3][1, 200, 5], ts[3][1, 203, 5] = math.inf, -math.inf  # a reset in the same lane's rows, and before
+    ts[3][1, 201, 6], ts[3][1, 207, 6] = -math.inf, math.inf
+    ts[3][1, 100, 7], ts[3][1, 300, 7] = math.inf, -math.inf
+    y, last, states = hc.scan_fwd(*ts[:4], gate="log", s0=s0, save_states=True)
+    a = [to_np(t) for t in ts]
+    f = ref.scan_fwd(*a[:4], "log", None if s0 is None else to_np(s0))
+    check_finite(last, f["last"], f["elast"], F32, "s_last")
+    check_finite(states, f["states"], f["estates"], F32, "states")
+    check_finite(y, f["y"], f["ey"], dtype, "y")
+    want = ref.scan_bwd(*a, "log", None if s0 is None else to_np(s0), None if ds_last is None else to_np(ds_last))
+    for name, t in zip(("dq", "dk", "dv", "dg", "ds0"), hc.scan_bwd(*ts, states, gate="log", ds_last=ds_last)):
+        check_finite(t, *want[name], F32 if name == "ds0" else dtype, name)
