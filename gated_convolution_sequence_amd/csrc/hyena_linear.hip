@@ -370,8 +370,10 @@ template <int N> __device__ __forceinline__ void step_barrier() {
 // A workgroup of WM x WN waves, each MT x NTL tiles of 16 x 16, with ST
 // operand buffers: ST - 1 steps of c are on their way while one is multiplied.
 // Bound by the matrix cores and the reads of LDS that feed them: at M = 8192, N
-// = K = 4096 bf16 the forward's product takes 230 us (1.2 PFLOP/s), dx = dz w 242
-// us (1.14) and dw = dz^T x 224 us (1.23), 256 x 256 tiles.
+// = K = 4096 bf16, 256 x 256 tiles, the forward with bias and residual takes 236
+// to 238 us in a row of calls (1.16 PFLOP/s), and in a trace of 30, where the
+// clock falls under load, 243 us at least and 273 on average, dx = dz w 239 and
+// 252, dw = dz^T x 227 and 240.
 template <bool F32, int WM, int WN, int MT, int NTL, int ST> struct Shape {
     static constexpr int NT = 64 * WM * WN, BM = WM * MT * 16, BN = WN * NTL * 16;
     static constexpr int CE = El<F32>::CE, BK = 8 * CE;
@@ -566,7 +568,8 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void bwd_kernel(GemmParams dw, Gem
     if ((int)blockIdx.x < blocks) run_tile<true, true, DIRECT, S>(dw, blockIdx.x, a0, a1, a2, a3, b0, b1, b2, b3);
     else run_tile<false, true, DIRECT, S>(dx, blockIdx.x - blocks, a0, a1, a2, a3, b0, b1, b2, b3);
 }
-// One of them (256 x 256 tiles fill the card alone, and have no registers to spare).
+// One of them (256 x 256 tiles fill the card alone, and have no registers to
+// spare: dw's loads keep 11 of theirs in memory, two 16-byte reloads a step).
 template <bool TALL_A, typename S> __global__ __launch_bounds__(S::NT, S::WAVES) void large_kernel(GemmParams p) {
     TILE_BUFFERS(S)
     run_tile<TALL_A, true, true, S>(p, blockIdx.x, a0, a1, a2, a3, b0, b1, b2, b3);
@@ -629,7 +632,9 @@ template <bool F32> __global__ __launch_bounds__(256) void finish_kernel(FinishP
 // from memory into the matrix cores' layout: lane (i, j) takes two 16-byte chunks
 // of row i at 128-byte steps, one of each 64 bytes, which serve two products.
 // The waves' sums meet in LDS.  8 rows against 4096 x 4096 bf16 weights: 10.5 us
-// (33.6 MB at 3.2 TB/s; a launch and one trip to memory are about 4.5 us of it).
+// (33.6 MB at 3.2 TB/s; a launch and one trip to memory are about 4.5 us of it).  A
+// wave issues the next span's loads after it has multiplied the last one's, so a
+// long row costs a trip to memory a span, four at K = 4096.
 // 8 waves with 2 steps each in flight: 9.4 / 10.8 / 17.6 us for 1 row, 8 rows and
 // 8 rows in fp32; 4 waves 11.2 / 11.2 / 20.3, 16 waves 10.1 / 11.1 / 19.1, 1 step
 // 10.2 / 10.9 / 19.3, 4 steps 10.5 / 11.4 / 20.2.
@@ -859,17 +864,21 @@ struct Size {
 constexpr int64_t kLeastSteps = 4;
 
 // Tiles: 256 x 256 where they fill the card's 256 units about as well as 128 x
-// 128 ones, 64 x 64 where there are fewer than 192 of 128 x 128 (at M = 1000,
-// N = K = 1024 bf16 forward 15 us, with split tiles of 128 x 128 20 us; at
-// 1021 x 777 x 521 fp32 24 against 31 us).
+// 128 ones, 64 x 64 where there are fewer than 192 of 128 x 128 (forward at M =
+// 1000, N = K = 1024 bf16 11 us, with split tiles of 128 x 128 20 us; at 500 x
+// 1000 x 2000 15 against 20; fp32 at 1021 x 777 x 521 21 against 30 us, at 1024 x
+// 768 x 512 14 against 23).
 // Splits: c is cut where a workgroup would walk much more than its share of
 // all steps.  One product is shared between 256 workgroups (in bf16 three steps
 // ahead of its products where a unit has one); two products between 512, but two
 // in fp32 of 64 x 64 tiles, whose blocks are of unlike length and few, between
 // 1024.  (Backward at M = 256, N = K = 4096 bf16: 48 us with 512, 74 us with 256;
 // forward 19 us with 256, 23 us with 512.  fp32 forward at 2048 x 2048 x 512 45 us
-// with 256, 56 with 512; backward at 1300 x 1288 x 1288 115 us with 512, 131 with
-// 1024, at 1021 x 777 x 521 46 with 512, 42 with 1024.)
+// with 256, 56 with 512.  fp32 backward of 64 x 64 tiles, with 512 and with 1024:
+// 904 x 1100 x 600 50 and 40 us, 1021 x 777 x 521 44 and 40, 768 x 768 x 768 40
+// and 35, 200 x 1500 x 1500 39.5 and 39, 300 x 300 x 300 and 640 x 1024 x 256 24
+// and 24, but 500 x 700 x 900 28 and 30, 1500 x 500 x 400 29 and 31, 2000 x 400 x
+// 400 29 and 33; of 128 x 128 tiles, 1300 x 1288 x 1288, 115 and 131.)
 Plan plan_of(const Size *sz, int n, bool f32, bool direct) {
     int64_t t128 = 0, t256 = 0;
     const int64_t bk = f32 ? 32 : 64;
@@ -906,7 +915,9 @@ Plan plan_of(const Size *sz, int n, bool f32, bool direct) {
 // against 67 us but bf16 25 against 21, 4091 x 2045 x 2045 (1.7e10) bf16 55 against
 // 64.  Backward: 1300 x 1291 x 1293 bf16 37 against 51 us, 1021 x 777 x 521 (4e8)
 // fp32 40 against 38; in a launch that is there anyway 41 against 45, and bf16 24
-// against 31.
+// against 31.  That holds for few rows too, though each copy then serves one row
+// of tiles: N = K = 4095 with M = 8, 64 and 256 bf16 46, 48 and 63 us against 58,
+// 64 and 89, fp32 106, 113 and 190 against 112, 131 and 256; 64 x 515 x 517 level.
 constexpr double pad_forward(bool f32) { return f32 ? 2e9 : 7e9; }
 constexpr double kPadBackward = 1e9;
 

@@ -45,9 +45,9 @@ namespace layer {
 namespace {
 
 // Words a tile looks at in one go.  4, 8 or 16: level where there are many
-// chains (69 us forward at B = 1, L = 8192, D = 4096 bf16); at D = 1024, where
-// chains are few and carries wait, 30.8, 27.1 and 26.0 us; fp32 at 3 x 1531 x
-// 1000 29.6, 29.1 and 32.9 us.
+// chains (forward at B = 1, L = 8192, D = 4096 bf16 68, 69 and 70 us); at D =
+// 1024, where chains are few and carries wait, 30.1, 27.3 and 26.0 us; fp32 at 3
+// x 1531 x 1000 28.4, 28.2 and 31.9 us.
 constexpr int kWindow = 8;
 constexpr int kMostCounters = 32;
 constexpr int kCounterGap = 32;  // counters lie on lines of their own
@@ -179,12 +179,14 @@ template <bool F32, int THREADS, int ROWS, int LANES_> struct Tile {
 };
 // Rows of a wave's loads are 256 bytes in both.  The forward holds 4 x 8 x 8
 // bf16 inputs a lane in flight, two workgroups a unit.  At B = 1, L = 8192 / B =
-// 4, L = 32768, D = 4096 bf16 a call takes 69 / 856 us; with 4 rows a lane 77 /
-// 1023, with 16 (which spill) 169 / 2339, with 128-byte rows 72 / 837 but 35
-// against 29 us in fp32 at 3 x 1531 x 1000, with 512 threads 71 / 922.
-// The backward holds five inputs: 4 rows a lane, three workgroups a unit, 128 /
-// 1566 us; 8 rows spill (650 us), 128-byte rows 136 / 1542 (fp32 at 3 x 1531 x
-// 1000 75 against 55 us), 512 threads 138 / 2013.
+// 4, L = 32768, D = 4096 bf16 a call takes 69 / 928 us (separate q, k, v, g; 878 as
+// slices of one buffer); with 4 rows a lane 77 / 1005, with 16 (which spill) 170
+// / 2347, with 128-byte rows 73 / 871 but 35 against 28 us in fp32 at 3 x 1531 x
+// 1000, with 512 threads 74 / 929.
+// The backward holds five inputs: 4 rows a lane, three workgroups a unit (its 138
+// registers do not let a fourth in), 131 / 1928 us (1708 with buffers placed
+// otherwise); 8 rows spill (587 us), 128-byte rows 139 / 1936 (fp32 at 3 x 1531 x
+// 1000 74 against 55 us), 512 threads 143 / 2195.
 template <bool F32> using FwdTile = Tile<F32, 256, 8, 16>;
 template <bool F32> using BwdTile = Tile<F32, 256, 4, 16>;
 
@@ -247,8 +249,10 @@ template <bool RESETS> __device__ inline float walk(float a, float x, float s) {
 }
 
 // Forward: 8 bytes read and 2 written a token and channel in bf16, and bound by
-// them: B = 1, L = 8192, D = 4096 in 65 us (5.2 TB/s: four rounds of workgroups,
-// whose ends leave units idle), B = 4, L = 32768 in 868 us (6.2 TB/s).
+// them: B = 1, L = 8192, D = 4096 in 68 us (5.0 TB/s: four rounds of workgroups,
+// whose ends leave units idle), B = 4, L = 32768 in 870 to 890 us (6.1 TB/s).  fp32:
+// 125 us (5.4 TB/s) at the first, 27 us (3.4 TB/s) at 3 x 1531 x 1000, whose 576
+// workgroups are a round and a bit.
 template <bool F32, bool LOG, bool PART>
 __global__ __launch_bounds__(FwdTile<F32>::NT, 2) void scan_fwd_kernel(ScanParams p) {
     using G = FwdTile<F32>;
@@ -426,9 +430,10 @@ __global__ __launch_bounds__(FwdTile<F32>::NT, 2) void scan_fwd_kernel(ScanParam
 // The states inside a tile are walked again from the saved state at its start:
 // keeping all of them would be 4 more bytes a token and channel to write and read.
 // 10 bytes read and 8 written a token and channel in bf16 and bound by them: B =
-// 1, L = 8192, D = 4096 in 125 us (4.8 TB/s), B = 4, L = 32768 in 1.56 ms (6.2
-// TB/s).  With few chains the carries bound it: fp32 at 3 x 1531 x 1000 is 48
-// chains of 24 tiles, one and a half rounds of workgroups, 50 us (3.3 TB/s).
+// 1, L = 8192, D = 4096 in 129 us (4.7 TB/s), B = 4, L = 32768 in 1.70 ms (5.7
+// TB/s).  fp32: 235 us (5.1 TB/s) at the first.  3 x 1531 x 1000 in fp32 is 1152
+// workgroups where 768 fit at three a unit, so half the card waits through the
+// second round: 53 us (3.1 TB/s).
 template <bool F32, bool LOG, bool PART>
 __global__ __launch_bounds__(BwdTile<F32>::NT, PART ? 2 : 3) void scan_bwd_kernel(ScanParams p) {
     using G = BwdTile<F32>;
@@ -640,9 +645,9 @@ template <typename G, typename K> int launch(K kernel, ScanParams p, void *works
         p.counters = (uint32_t *)workspace;
         p.words = (uint64_t *)((char *)workspace + kHeader);
         // Several counters spare the first workgroups the wait for one (B = 1, L =
-        // 8192: 69 against 71 us; 3 x 1531 x 1000 fp32: 34 against 39 us); one
+        // 8192: 69 against 71 us; 3 x 1531 x 1000 fp32: 28 against 33 us); one
         // keeps the tiles in flight closer together in memory, which counts once
-        // there are many rounds of them (B = 4, L = 32768: 887 against 1003 us).
+        // there are many rounds of them (B = 4, L = 32768: 928 against 1018 us).
         p.n_counters = 1;
         while (blocks <= 8192 && p.n_counters < kMostCounters && p.n_chains % (2 * p.n_counters) == 0) p.n_counters *= 2;
         const int64_t words = p.n_tiles * p.n_chains * G::C;

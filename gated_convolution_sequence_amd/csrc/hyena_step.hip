@@ -102,8 +102,10 @@ template <bool F32, int N> __device__ inline void load_taps(const void *h, size_
 // consecutive taps each, all their rows of the ring in flight at once; the
 // slices' sums meet by shuffles and, over the waves, in LDS.  Bound by the
 // ring's rows from memory (l_h - 1 of them a sequence; B = 64, l_h = 128, D =
-// 4096 bf16: 69 MB in 14 us, 4.9 TB/s), or by latency for few sequences (B = 1:
-// 4.6 us).  ONE: a lane's channels share a filter.
+// 4096 bf16: 69 MB in 14.5 us, 4.8 TB/s; fp32 139 MB in 25 us, 5.6 TB/s), or by
+// latency for few sequences (B = 1: 4.7 us).  ONE: a lane's channels share a
+// filter.  Where they do not, every sequence reads each channel's taps anew: B =
+// 64 with a filter per channel 27 us (2.6 TB/s of the ring's rows).
 template <bool F32, int W, int TAPS, bool ONE> __global__ __launch_bounds__(256) void conv_step_kernel(StepParams p) {
     using Ln = Lane<F32>;
     constexpr int VEC = Ln::VEC, EB = F32 ? 4 : 2, ITEMS = 4 / W;
@@ -206,8 +208,9 @@ template <bool F32, int W, int TAPS, bool ONE> __global__ __launch_bounds__(256)
     }
 }
 
-// The last rows of a prompt's k v: read and written once, bound by memory and,
-// for a few sequences, the launch.  blockIdx.y counts the rows from the last one
+// The last rows of a prompt's k v: read and written once, bound by memory (64
+// sequences, 128 rows of 4096 channels: bf16 201 MB in 33 us, fp32 403 MB in 66
+// us, 6.1 TB/s) and, for a few sequences, the launch (one: 3 us).  blockIdx.y counts the rows from the last one
 // back, blockIdx.z the sequences.
 template <bool F32> __global__ __launch_bounds__(kScanThreads) void cache_fill_kernel(StepParams p) {
     using Ln = Lane<F32>;
@@ -318,7 +321,7 @@ int hyena_conv_step(const void *q, const void *k, const void *v, const void *h, 
     p.B = B, p.D = D, p.ld = ld, p.S = S, p.R = R, p.group_size = group_size, p.l_h = l_h;
     // The cut of the taps.  Filters of up to 32 taps: one wave, 4 taps a lane.
     // Few sequences: as many lanes as there can be (B = 1, l_h = 128, D = 4096
-    // bf16, one filter for 16 channels: 4.6 us).  Once that is more waves than the
+    // bf16, one filter for 16 channels: 4.7 us).  Once that is more waves than the
     // card holds, 16 taps a lane (B = 64: 15.5 us against 19.0 with 4 and 17.7
     // with 8); 8 where a lane's channels have filters of their own, whose taps
     // take registers too (27.5 us against 33.1 with 16).

@@ -229,10 +229,10 @@ def scan_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
     row stride for the four: separate contiguous tensors or column slices of
     one [B, L, 4 D] projection.  gate: "sigmoid" (a = sigmoid(g)) or "log"
     (a = exp(g), also above 1; exp(g) and the states have to fit fp32); g = -inf
-    starts afresh from that row.  s0: [B, D] fp32 state
-    before row 0 (None: zero).  s_last: [B, D] fp32.  states: with
-    ``save_states`` the fp32 states before rows 0, 64, 128, ... that scan_bwd
-    takes, else None.  ``workspace`` (uint8) is allocated here if not given.
+    starts afresh from that row.  s0: [B, D] fp32 state before row 0 (None:
+    zero).  s_last: [B, D] fp32.  states: with ``save_states`` the fp32 states
+    before rows 0, 64, 128, ... that scan_bwd takes, else None.  ``workspace``
+    (uint8) is allocated here if not given.
     """
     code, ld = _scan_inputs((q, k, v, g), ("q", "k", "v", "g"))
     gcode = _pick(GATES, gate, "gate")
@@ -469,7 +469,10 @@ def linear_bwd(x: torch.Tensor, w: torch.Tensor, dy: torch.Tensor, preact: Optio
 
     ``preact`` is the z that linear_fwd saved (not wanted for act "none").  The
     residual's gradient is dy itself.  Parts not requested are None; ``dx``
-    may be given to be written to.
+    may be given to be written to.  In bf16 with an activation dz = dy act'(z)
+    is rounded to bf16 before its two products, as the matrix cores take it
+    (relative errors of dx and dw 0.0024, of which 0.0017 are their own
+    rounding); db sums dz as it is.
     """
     code = _code(x)
     acode = _pick(ACTS, act, "act")

@@ -42,7 +42,8 @@ extern "C" {
  *     y[b,t,d] = q[b,t,d] s[b,t,d]
  *
  * Where a is 0 (g = -inf: the first row of a packed document) the earlier
- * state is dropped whatever it holds, infinities and NaN included.
+ * state is dropped whatever it holds, infinities and NaN included; a is also 0
+ * for finite g below about -87, where it is below fp32's least normal number.
  *
  * q, k, v, g are [B, L, D] with D contiguous and one row stride `ld` >= D for
  * all four: row (b, t) of each starts (b L + t) ld elements after its pointer
