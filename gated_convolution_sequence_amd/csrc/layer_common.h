@@ -45,8 +45,9 @@ __device__ inline bool any_lane(bool x) { return __builtin_amdgcn_ballot_w64(x) 
 
 // The decay a of a gate, and da/dg.  With e = exp(-g), sigmoid(g) = 1 / (1 + e)
 // and its slope is e a^2, which keeps 1 - a exact to rounding where a is near
-// 1.  a is 0 for g = -inf and for a finite g whose e overflows (g < -88); the
-// slope of those is not a number and not used.
+// 1.  a is 0 for g = -inf and for a finite g below -87.3, where it is below the
+// least normal fp32; the slope of those is not used (nor a number where e
+// overflows).
 template <bool LOG> __device__ inline float decay(float g) {
     if constexpr (LOG) return __expf(g);
     else return __builtin_amdgcn_rcpf(1.0f + __expf(-g));
