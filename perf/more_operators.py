@@ -7,7 +7,9 @@ norm    y = (x - mean) rstd w + b over a row's D channels (kind "layer"), or
 xent    the softmax cross entropy of a readout, z = x w^T + bias over a vocabulary,
             lse_i = log sum_v exp(z_iv),   loss_i = lse_i - z_i,target_i
         (0 where the target is no entry of the vocabulary), and the gradients of x, w and bias.
-adamw   the clipping scale of all gradients together and one AdamW step over a list of tensors.
+adamw   the clipping scale of all gradients together and one AdamW step over a list of tensors,
+        the moments in fp32, or m and sqrt(v) in 8 bits (e4m3) with a scale for every 256, rounded
+        up or down at random in proportion.
 """
 import math
 
@@ -47,14 +49,15 @@ def listed():
         # ... and its gradients, a quarter of the positions being prompt or padding without a target
         dict(name="xent_bwd_8k", op="xent_bwd", M=8192, K=4096, V=65536, dtype="bf16", bias=False, masked=0.25),
         # a byte-level vocabulary: as many rows, few columns
-        dict(name="xent_fwd_bytes", op="xent_fwd", M=8192, K=4096, V=512, dtype="bf16", bias=True, masked=0.0),
         dict(name="xent_bwd_bytes", op="xent_bwd", M=8192, K=4096, V=512, dtype="bf16", bias=True, masked=0.0),
         # fp32, every size odd
         dict(name="xent_bwd_f32_odd", op="xent_bwd", M=1021, K=777, V=5003, dtype="f32", bias=True, masked=0.3),
         # the example model's weights at width 256: launches count
-        dict(name="adamw_small", op="adamw", D=256, V=32, layers=1, dtype="bf16", master=True, clip=True),
-        # two layers of the main width and a large embedding, fp32 masters of bf16 weights
-        dict(name="adamw_large", op="adamw", D=4096, V=65536, layers=1, dtype="bf16", master=True, clip=True),
+        dict(name="adamw_small", op="adamw", D=256, V=32, layers=1, dtype="bf16", master=True, clip=True, bits=32),
+        # a layer of the main width and a large embedding, fp32 masters of bf16 weights
+        dict(name="adamw_large", op="adamw", D=4096, V=65536, layers=1, dtype="bf16", master=True, clip=True, bits=32),
+        # the moments in 8 bits
+        dict(name="adamw_8bit", op="adamw", D=4096, V=512, layers=2, dtype="bf16", master=True, clip=True, bits=8),
     ]
 
 
@@ -82,7 +85,7 @@ def draw(rng):
     D = _log_int(rng, 32, 2048)
     D = D | 1 if odd else max(16, D // 16 * 16)
     return dict(op=op, D=D, V=_log_int(rng, 16, 32768), layers=rng.randrange(1, 5), dtype=dtype,
-                master=dtype == "bf16" and rng.random() < 0.7, clip=rng.random() < 0.7)
+                master=dtype == "bf16" and rng.random() < 0.7, clip=rng.random() < 0.7, bits=rng.choice([32, 32, 8]))
 
 
 def _active(case):
@@ -96,6 +99,21 @@ def _shapes(case):
     for _ in range(case["layers"]):
         shapes += [(D,)] * 4 + [(D, D)] * 4 + [(max(1, D // 16), 128)] + [(4 * D, D), (4 * D,), (D, D)]
     return shapes
+
+
+BLOCK = 256  # elements that share a scale where the moments have 8 bits
+
+
+def _room(shape, unit=BLOCK):
+    return -(-math.prod(shape) // unit) * unit
+
+
+def _views(flat, shapes, unit=BLOCK):
+    out, at = [], 0
+    for sh in shapes:
+        out.append(flat[at:at + math.prod(sh)].view(sh))
+        at += _room(sh, unit)
+    return out
 
 
 # ---- inputs ------------------------------------------------------------------
@@ -142,16 +160,27 @@ def prepare(case, seed):
             # what the training forward saved
             st["lse"] = torch.where(target >= 0, torch.logsumexp(_logits(st), dim=1), 0.0)
     else:
+        # the lists are views of one buffer each, tensors at multiples of 256 elements
         shapes = _shapes(case)
-        std = [s[-1] ** -0.5 if len(s) == 2 else 1.0 for s in shapes]
-        value = [_randn(gen, s, scale=c) for s, c in zip(shapes, std)]
-        st["params"] = [v.to(dt) for v in value]
-        st["masters"] = value if case["master"] else None
-        st["grads"] = [_randn(gen, s, dt, scale=1e-3) for s in shapes]
+        flat = _randn(gen, (sum(_room(sh) for sh in shapes),))
+        for t, sh in zip(_views(flat, shapes), shapes):
+            t.mul_(sh[-1] ** -0.5 if len(sh) == 2 else 1.0)
+        st["params_flat"] = flat.to(dt)
+        st["masters_flat"] = flat if case["master"] else None
+        st["grads"] = _views(_randn(gen, flat.shape, dt, scale=1e-3), shapes)
         # moments some way into a training
-        st["m"] = [_randn(gen, s, scale=5e-4) for s in shapes]
-        st["v"] = [_randn(gen, s, scale=1e-3).square_() for s in shapes]
-        st["step"], st["lr"] = 1000, 3e-4
+        st["m_flat"] = _randn(gen, flat.shape, scale=5e-4)
+        st["v_flat"] = _randn(gen, flat.shape, scale=1e-3).square_()
+        if case["bits"] == 8:
+            st["v_flat"].sqrt_()
+            for n in "mv":
+                scale = st[n + "_flat"].view(-1, BLOCK).abs().amax(1) / 448
+                codes = (st[n + "_flat"].view(-1, BLOCK) / scale[:, None]).to(torch.float8_e4m3fn)
+                st[n + "_flat"], st[n + "_scale_flat"] = codes.view(-1), scale
+                st[n + "_scale"] = _views(scale, [(-(-math.prod(sh) // BLOCK),) for sh in shapes], 1)
+        for n, key in (("params", "params_flat"), ("masters", "masters_flat"), ("m", "m_flat"), ("v", "v_flat")):
+            st[n] = None if st[key] is None else _views(st[key], shapes)
+        st["step"], st["lr"], st["seed"] = 1000, 3e-4, 20240
     return st
 
 
@@ -208,8 +237,42 @@ def _plain_xent_bwd(st):
 
 
 def _adamw_outputs(st, norm):
-    lists = [st["params"], st["m"], st["v"]] + ([st["masters"]] if st["masters"] else [])
-    return [t for ts in lists for t in ts] + ([] if norm is None else [norm])
+    names = ["params", "m", "v"] + (["masters"] if st["masters"] else [])
+    names += ["m_scale", "v_scale"] if st["bits"] == 8 else []
+    return [st[n + "_flat"] for n in names] + ([] if norm is None else [norm])
+
+
+def _mix(h):
+    """32 bits well mixed (the last steps of murmur3)."""
+    h = ((h ^ (h >> 16)) * 0x85EBCA6B) & 0xFFFFFFFF
+    h = ((h ^ (h >> 13)) * 0xC2B2AE35) & 0xFFFFFFFF
+    return h ^ (h >> 16)
+
+
+def _random_bits(n, seed, tensor):
+    """Two times 16 bits for each of n elements of a tensor: those of m and of v."""
+    i = torch.arange(n, device=DEV)
+    key = _mix((seed + tensor * 0x9E3779B9 + (i >> 32)) & 0xFFFFFFFF)
+    h = _mix((i & 0xFFFFFFFF) ^ key)
+    return h & 0xFFFF, h >> 16
+
+
+def _to_codes(x, bits):
+    """e4m3 codes and scales of x's blocks, each rounded up with the probability of its place between two codes."""
+    n = x.numel()
+    x = torch.nn.functional.pad(x.view(-1), (0, -n % BLOCK)).view(-1, BLOCK)
+    scale = x.abs().amax(1) / 448
+    t = torch.where(scale[:, None] > 0, x.abs() / scale[:, None], 0.0).clamp(max=448)
+    exponent = torch.frexp(t).exponent - 1
+    step = torch.ldexp(torch.ones_like(t), exponent.clamp(min=-6) - 3)
+    up = torch.nn.functional.pad(bits, (0, -n % BLOCK)).view(-1, BLOCK).float() / 65536
+    q = torch.floor(t / step + up) * step
+    return torch.copysign(q, x).view(-1)[:n].to(torch.float8_e4m3fn), scale
+
+
+def _from_codes(codes, scale):
+    n = codes.numel()
+    return codes.view(-1).float() * scale.repeat_interleave(BLOCK)[:n]
 
 
 def _plain_adamw(st):
@@ -222,14 +285,26 @@ def _plain_adamw(st):
     # one tensor at a time, since each has a size of its own
     for i, g in enumerate(grads):
         g = g * scale
-        st["m"][i].mul_(b1).add_(g * (1 - b1))
-        st["v"][i].mul_(b2).add_(g * g * (1 - b2))
+        m, v = st["m"][i], st["v"][i]
+        if st["bits"] == 8:
+            m = _from_codes(m, st["m_scale"][i]).view(g.shape)
+            v = _from_codes(v, st["v_scale"][i]).square().view(g.shape)
+        m = m * b1 + g * (1 - b1)
+        v = v * b2 + g * g * (1 - b2)
         value = st["masters"][i] if st["masters"] else st["params"][i].float()
-        move = st["m"][i] / (1 - b1 ** t) / (torch.sqrt(st["v"][i] / (1 - b2 ** t)) + ADAM_EPS)
+        move = m / (1 - b1 ** t) / (torch.sqrt(v / (1 - b2 ** t)) + ADAM_EPS)
         value = value * (1 - lr * DECAY) - lr * move
         if st["masters"]:
             st["masters"][i].copy_(value)
         st["params"][i].copy_(value)
+        if st["bits"] == 8:
+            for name, x, bits in zip("mv", (m, v.sqrt()), _random_bits(g.numel(), st["seed"], i)):
+                codes, scales = _to_codes(x, bits)
+                st[name][i].copy_(codes.view(g.shape))
+                st[name + "_scale"][i].copy_(scales)
+        else:
+            st["m"][i].copy_(m)
+            st["v"][i].copy_(v)
     return _adamw_outputs(st, norm)
 
 
@@ -259,7 +334,8 @@ def _own(st):
     if st["clip"]:
         norm, scale = hc.grad_norm(st["grads"], max_norm=1.0)
     hc.adamw_step(st["params"], st["grads"], st["m"], st["v"], step=st["step"], lr=st["lr"], betas=BETAS,
-                  eps=ADAM_EPS, weight_decay=DECAY, masters=st["masters"], grad_scale=scale)
+                  eps=ADAM_EPS, weight_decay=DECAY, masters=st["masters"], grad_scale=scale,
+                  exp_avg_scales=st.get("m_scale"), exp_avg_sq_scales=st.get("v_scale"), seed=st["seed"])
     return _adamw_outputs(st, norm)
 
 
@@ -308,23 +384,51 @@ def _exact_xent(st):
     return out + ([p.sum(0)] if st["b"] is not None else [])
 
 
+def _exact_codes(x, chance):
+    """The e4m3 values between which each x / scale lies are 2^k apart; up or down by chance."""
+    scale = torch.nn.functional.pad(x, (0, -len(x) % BLOCK)).view(-1, BLOCK).abs().amax(1) / 448
+    t = x / scale.repeat_interleave(BLOCK)[:len(x)]
+    t = torch.nan_to_num(t, nan=0.0)
+    gap = torch.exp2(torch.floor(torch.log2(t.abs().clamp(min=2.0 ** -6))) - 3)
+    low = torch.floor(t.abs() / gap)
+    return torch.sign(t) * (low + (t.abs() / gap - low + chance >= 1)) * gap, scale
+
+
 def _exact_adamw(st):
     (b1, b2), lr, t = BETAS, st["lr"], st["step"]
     norm, scale = None, 1.0
     if st["clip"]:
         norm = math.sqrt(sum(float(g.double().pow(2).sum()) for g in st["grads"]))
         scale = min(1.0, 1.0 / norm)
-    out = [[], [], [], []]
+    names = ["params", "m", "v"] + (["masters"] if st["masters"] else [])
+    names += ["m_scale", "v_scale"] if st["bits"] == 8 else []
+    flat = {n: st[n + "_flat"].double() for n in names}
+    shapes = [g.shape for g in st["grads"]]
+    out = {n: _views(flat[n], shapes) for n in names if "scale" not in n}
     for i, g in enumerate(st["grads"]):
         g = g.double() * scale
-        m = b1 * st["m"][i].double() + (1 - b1) * g
-        v = b2 * st["v"][i].double() + (1 - b2) * g ** 2
+        m, v = out["m"][i], out["v"][i]
+        if st["bits"] == 8:
+            m, v = ((c.view(-1) * s[i].double().repeat_interleave(BLOCK)[:c.numel()]).view(g.shape)
+                    for c, s in ((m, st["m_scale"]), (v, st["v_scale"])))
+            v = v ** 2
+        m = b1 * m + (1 - b1) * g
+        v = b2 * v + (1 - b2) * g ** 2
         p = (st["masters"] or st["params"])[i].double()
         p = p - lr * DECAY * p - lr * (m / (1 - b1 ** t)) / ((v / (1 - b2 ** t)) ** 0.5 + ADAM_EPS)
-        for ts, value in zip(out, (p, m, v, p)):
-            ts.append(value)
-    flat = out[0] + out[1] + out[2] + (out[3] if st["masters"] else [])
-    return flat + ([] if norm is None else [torch.tensor(norm, dtype=torch.float64, device=DEV)])
+        out["params"][i].copy_(p)
+        if st["masters"]:
+            out["masters"][i].copy_(p)
+        if st["bits"] == 8:
+            for n, x, bits in zip("mv", (m, v ** 0.5), _random_bits(g.numel(), st["seed"], i)):
+                codes, scales = _exact_codes(x.reshape(-1), bits.double() / 65536)
+                out[n][i].copy_(codes.view(g.shape))
+                at = st[n + "_scale"][i].storage_offset()
+                flat[n + "_scale"][at:at + len(scales)] = scales
+        else:
+            out["m"][i].copy_(m)
+            out["v"][i].copy_(v)
+    return [flat[n] for n in names] + ([] if norm is None else [torch.tensor(norm, dtype=torch.float64, device=DEV)])
 
 
 def exact(case, seed):
@@ -353,5 +457,6 @@ def work(case):
         return {"bytes": eb * (rows * K + M * K + 2 * V * K) + 2 * bias + 16 * M,
                 "flops": 6 * rows * K * V + 4 * rows * V}
     n = sum(math.prod(s) for s in _shapes(case))
-    return {"bytes": n * (3 * eb - (eb if case["master"] else 0) + 16 + (8 if case["master"] else 0)),
-            "flops": n * (14 + (2 if case["clip"] else 0))}
+    # gradient in, parameter out (and in, without a master); master, and the moments, both ways
+    each = 2 * eb + (8 if case["master"] else eb) + (16 if case["bits"] == 32 else 4 + 16 / BLOCK)
+    return {"bytes": int(n * each), "flops": n * (14 + (2 if case["clip"] else 0) + (10 if case["bits"] == 8 else 0))}
