@@ -443,3 +443,7 @@ from .layer import (  # noqa: E402,F401  (the operators around the convolution)
     ACTS, GATES, LAYER_EXPORTS, LAYER_LIB_PATH, STATE_ROWS, GatedScan, LayerError, LinearAct, conv_cache_fill,
     conv_step, layer_lib, layer_strerror, linear_bwd, linear_fwd, linear_workspace_bytes, scan_bwd, scan_fwd,
     scan_step, scan_workspace_bytes)
+from .model import (  # noqa: E402,F401  (the operators between a model's layers and its weights)
+    MODEL_EXPORTS, MODEL_LIB_PATH, NORMS, STATE_BLOCK, LinearXent, ModelError, Norm, adamw_step, grad_norm,
+    grad_norm_workspace_bytes, model_lib, model_strerror, norm_bwd, norm_fwd, norm_workspace_bytes, xent_bwd,
+    xent_fwd, xent_workspace_bytes)

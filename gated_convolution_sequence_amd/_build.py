@@ -12,6 +12,9 @@ LIB = os.path.join(PKG, "libhyena_conv.so")
 # the sequence-layer operators (include/hyena_layer.h)
 LAYER_SOURCES = [os.path.join(PKG, "csrc", name) for name in ("hyena_scan.hip", "hyena_step.hip", "hyena_linear.hip")]
 LAYER_LIB = os.path.join(PKG, "libhyena_layer.so")
+# the operators between a model's layers and its weights (include/hyena_model.h)
+MODEL_SOURCES = [os.path.join(PKG, "csrc", name) for name in ("hyena_norm.hip", "hyena_xent.hip", "hyena_adamw.hip")]
+MODEL_LIB = os.path.join(PKG, "libhyena_model.so")
 # the benchmark's streaming reference kernel (not part of the operator's ABI)
 STREAM_REF_SOURCE = os.path.join(PKG, "csrc", "stream_ref.hip")
 STREAM_REF_LIB = os.path.join(PKG, "libhyena_stream_ref.so")
@@ -49,6 +52,11 @@ def build_library(verbose: bool = False) -> str:
 def build_layer_library(verbose: bool = False) -> str:
     """Compile the sequence-layer operators' csrc/*.hip sources into libhyena_layer.so next to this file."""
     return _compile(LAYER_SOURCES, LAYER_LIB, verbose)
+
+
+def build_model_library(verbose: bool = False) -> str:
+    """Compile the model operators' csrc/*.hip sources into libhyena_model.so next to this file."""
+    return _compile(MODEL_SOURCES, MODEL_LIB, verbose)
 
 
 def build_stream_ref(verbose: bool = False) -> str:

@@ -1,0 +1,443 @@
+// An AdamW step and the norm of all gradients over a list of tensors, for
+// MI355X (gfx950) (hyena_model.h has the formulas).
+//
+// Bound by memory: a bf16 weight with an fp32 master moves 28 bytes (16 with
+// moments of 8 bits, and 2 more for the norm).  The tensors' addresses travel as
+// kernel arguments, up to kTensors a launch, so that nothing is copied to the device
+// beforehand and a captured call keeps its own; a workgroup finds its tensor by one
+// comparison a lane.
+
+#include <math.h>
+
+#include "hyena_model.h"
+#include "layer_gemm.h"
+
+namespace layer {
+namespace {
+
+constexpr int kTensors = 48;  // a launch: 3.5 KB of arguments
+constexpr int kSpan = 8192;   // elements a workgroup
+constexpr int kBlock = 256;   // elements that share a scale
+
+struct Entry {
+    void *param;
+    const void *grad;
+    void *m, *v;
+    float *m_scale, *v_scale, *master;
+    int64_t numel;
+};
+struct Table {
+    Entry t[kTensors];
+    uint32_t first[kTensors];  // each tensor's first workgroup
+    uint32_t place[kTensors];  // its place in the list
+    int n;
+};
+
+// The tensor of a workgroup, and the workgroup's place in it.
+__device__ inline int find(const Table &p, uint32_t block) {
+    const int lane = threadIdx.x & 63;
+    const uint64_t at = __builtin_amdgcn_ballot_w64(lane < p.n && p.first[lane] <= block);
+    return __builtin_amdgcn_readfirstlane(__popcll(at) - 1);
+}
+
+struct AdamParams {
+    double lr, beta1, beta2, weight_decay;
+    int64_t step, seed;
+    const float *lr_dev;
+    const int64_t *step_dev, *seed_dev;
+    const float *scale;
+    float eps;
+};
+
+// What a step multiplies by; from 64 bits, since 1 - beta^t cancels.
+struct Factors {
+    float b1, c1, b2, c2, keep, size, root, eps, scale;
+    uint32_t seed;
+    bool skip;
+};
+__device__ inline Factors factors_of(const AdamParams &p) {
+    Factors f;
+    const double lr = p.lr_dev ? (double)*p.lr_dev : p.lr;
+    int64_t t = p.step_dev ? *p.step_dev : p.step;
+    if (t < 1) t = 1;
+    f.b1 = (float)p.beta1, f.c1 = (float)(1.0 - p.beta1);
+    f.b2 = (float)p.beta2, f.c2 = (float)(1.0 - p.beta2);
+    f.keep = (float)(1.0 - lr * p.weight_decay);
+    f.size = (float)(lr / (1.0 - pow(p.beta1, (double)t)));
+    f.root = (float)(1.0 / (1.0 - pow(p.beta2, (double)t)));
+    f.eps = p.eps;
+    f.scale = p.scale ? *p.scale : 1.0f;
+    f.seed = (uint32_t)(p.seed_dev ? *p.seed_dev : p.seed);
+    f.skip = !(fabsf(f.scale) <= 3.402823466e38f);
+    return f;
+}
+
+// The new m and v and the value that they move, V elements at a time.
+template <int V>
+__device__ __forceinline__ void move(const Factors &f, const float (&g)[V], float (&m)[V], float (&v)[V], float (&w)[V]) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        const float d = g[k] * f.scale;
+        m[k] = f.b1 * m[k] + f.c1 * d;
+        v[k] = f.b2 * v[k] + f.c2 * (d * d);
+        w[k] = w[k] * f.keep - f.size * m[k] / (sqrtf(v[k] * f.root) + f.eps);
+    }
+}
+template <bool F32, int V> __device__ __forceinline__ void read(const void *p, int64_t e, int n, float (&x)[V]) {
+    const auto r = Pack<F32, V>::load(p, e, n);
+#pragma unroll
+    for (int k = 0; k < V; ++k) x[k] = r.get(k);
+}
+template <bool F32, int V> __device__ __forceinline__ void read_value(const Entry &t, int64_t e, int n, float (&w)[V]) {
+    if (t.master) read<true, V>(t.master, e, n, w);
+    else read<F32, V>(t.param, e, n, w);
+}
+template <bool F32, int V> __device__ __forceinline__ void write_value(const Entry &t, int64_t e, int n, const float (&w)[V]) {
+    if (t.master) Pack<true, V>::store(t.master, e, n, w);
+    Pack<F32, V>::store(t.param, e, n, w);
+}
+
+template <bool F32> __global__ __launch_bounds__(256) void adamw_kernel(Table p, AdamParams a) {
+    constexpr int V = F32 ? 4 : 8;
+    __shared__ Factors shared;
+    if (threadIdx.x == 0) shared = factors_of(a);
+    const int i = find(p, blockIdx.x);
+    const Entry t = p.t[i];
+    const int64_t begin = (int64_t)(blockIdx.x - p.first[i]) * kSpan, end = min(t.numel, begin + kSpan);
+    __syncthreads();
+    const Factors f = shared;
+    if (f.skip) return;
+    for (int64_t e = begin + threadIdx.x * V; e < end; e += 256 * V) {
+        const int n = (int)min(end - e, (int64_t)V);
+        float g[V], m[V], v[V], w[V];
+        read<F32, V>(t.grad, e, n, g);
+        read<true, V>(t.m, e, n, m);
+        read<true, V>(t.v, e, n, v);
+        read_value<F32, V>(t, e, n, w);
+        move(f, g, m, v, w);
+        Pack<true, V>::store(t.m, e, n, m);
+        Pack<true, V>::store(t.v, e, n, v);
+        write_value<F32, V>(t, e, n, w);
+    }
+}
+
+// ---- moments in 8 bits ----------------------------------------------------------------
+
+// 32 bits well mixed: the last steps of murmur3.
+__device__ inline uint32_t mix(uint32_t h) {
+    h = (h ^ (h >> 16)) * 0x85EBCA6Bu;
+    h = (h ^ (h >> 13)) * 0xC2B2AE35u;
+    return h ^ (h >> 16);
+}
+
+// Eight codes as they lie in memory, n of them where that is fewer.
+struct Codes {
+    typedef u32x2_t any __attribute__((aligned(1)));
+    u32x2_t c;
+    __device__ static Codes load(const void *p, int64_t e, int n) {
+        const uint8_t *at = (const uint8_t *)p + e;
+        if (n >= 8) return Codes{*(const any *)at};
+        uint32_t w[2] = {0, 0};
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k < n) w[k / 4] |= (uint32_t)at[k] << 8 * (k % 4);
+        return Codes{u32x2_t{w[0], w[1]}};
+    }
+    __device__ void store(void *p, int64_t e, int n) const {
+        uint8_t *at = (uint8_t *)p + e;
+        if (n >= 8) {
+            *(any *)at = c;
+            return;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k < n) at[k] = (uint8_t)(c[k / 4] >> 8 * (k % 4));
+    }
+    __device__ void get(float (&x)[8]) const {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            x[4 * h] = __builtin_amdgcn_cvt_f32_fp8(c[h], 0);
+            x[4 * h + 1] = __builtin_amdgcn_cvt_f32_fp8(c[h], 1);
+            x[4 * h + 2] = __builtin_amdgcn_cvt_f32_fp8(c[h], 2);
+            x[4 * h + 3] = __builtin_amdgcn_cvt_f32_fp8(c[h], 3);
+        }
+    }
+    // of values that e4m3 holds
+    __device__ static Codes of(const float (&x)[8]) {
+        Codes r;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            int w = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * h], x[4 * h + 1], 0, false);
+            r.c[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(x[4 * h + 2], x[4 * h + 3], w, true);
+        }
+        return r;
+    }
+};
+
+// The block's scale (32 lanes, eight values each) and the codes of x / scale: with
+// the spacing 2^(e - 3) of the codes around it (2^-9 at least), floor(x / spacing + up)
+// of them.  16 bits of `up` from each of h.
+template <int SHIFT>
+__device__ __forceinline__ Codes round_codes(const float (&x)[8], const uint32_t (&h)[8], float &scale) {
+    float top = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(x[k]));
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
+    scale = top < 0x1p-117f ? 0.0f : top / 448.0f;
+    const float inverse = scale > 0.0f ? 1.0f / scale : 0.0f;
+    float q[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        float t = fabsf(x[k]) * inverse;
+        if (t > 448.0f) t = 448.0f;  // (NaN stays)
+        int e = (int)(__float_as_uint(t) >> 23) - 127;
+        if (e < -6) e = -6;
+        const float up = (float)(h[k] >> SHIFT & 0xffffu) * 0x1p-16f;
+        const float spacing = __uint_as_float((uint32_t)(e - 3 + 127) << 23), per = __uint_as_float((uint32_t)(3 - e + 127) << 23);
+        q[k] = copysignf(floorf(t * per + up) * spacing, x[k]);
+    }
+    return Codes::of(q);
+}
+
+// As adamw_kernel; a wave's halves take a block of 256 each, so that its largest is five
+// steps between lanes.
+template <bool F32> __global__ __launch_bounds__(256) void adamw8_kernel(Table p, AdamParams a) {
+    constexpr int V = 8;
+    static_assert(kBlock == 32 * V && kSpan % kBlock == 0, "half a wave a block");
+    __shared__ Factors shared;
+    if (threadIdx.x == 0) shared = factors_of(a);
+    const int i = find(p, blockIdx.x);
+    const Entry t = p.t[i];
+    const int64_t begin = (int64_t)(blockIdx.x - p.first[i]) * kSpan, end = min(t.numel, begin + kSpan);
+    __syncthreads();
+    const Factors f = shared;
+    if (f.skip) return;
+    const uint32_t seed = f.seed + 0x9E3779B9u * p.place[i];
+    for (int64_t at = begin; at < end; at += 256 * V) {
+        const int64_t e = at + threadIdx.x * V;
+        const int n = (int)max(min(end - e, (int64_t)V), (int64_t)0);  // 0: only for its half's largest
+        const int64_t block = e / kBlock;
+        float g[V] = {}, m[V] = {}, v[V] = {}, w[V] = {};
+        if (n > 0) {
+            const Codes cm = Codes::load(t.m, e, n), cv = Codes::load(t.v, e, n);
+            const float sm = t.m_scale[block], sv = t.v_scale[block];
+            read<F32, V>(t.grad, e, n, g);
+            read_value<F32, V>(t, e, n, w);
+            cm.get(m);
+            cv.get(v);
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                m[k] *= sm;
+                v[k] *= sv;
+                v[k] *= v[k];
+            }
+        }
+        move(f, g, m, v, w);
+        uint32_t h[V];
+        const uint32_t key = mix(seed + (uint32_t)(e >> 32));
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            h[k] = mix((uint32_t)(e + k) ^ key);  // e is a multiple of 8: the high half is the same
+            v[k] = sqrtf(v[k]);
+            if (k >= n) m[k] = v[k] = 0.0f;
+        }
+        float sm, sv;
+        const Codes cm = round_codes<0>(m, h, sm), cv = round_codes<16>(v, h, sv);
+        if (n <= 0) continue;
+        cm.store(t.m, e, n);
+        cv.store(t.v, e, n);
+        if ((threadIdx.x & 31) == 0) t.m_scale[block] = sm, t.v_scale[block] = sv;
+        write_value<F32, V>(t, e, n, w);
+    }
+}
+
+// ---- norm of all gradients ------------------------------------------------------------
+
+__device__ inline double block_sum(double s) {
+    __shared__ double part[16];
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) s += __shfl_xor(s, o);
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
+    __syncthreads();
+    s = 0.0;
+    for (int w = 0; w < (int)blockDim.x / 64; ++w) s += part[w];
+    return s;
+}
+
+constexpr int kNormSpan = 32768;
+template <bool F32> __global__ __launch_bounds__(256) void squares_kernel(Table p, double *partial) {
+    constexpr int V = F32 ? 4 : 8;
+    const int i = find(p, blockIdx.x);
+    const Entry t = p.t[i];
+    const int64_t begin = (int64_t)(blockIdx.x - p.first[i]) * kNormSpan, end = min(t.numel, begin + kNormSpan);
+    double s = 0.0;
+#pragma unroll 4
+    for (int64_t e = begin + threadIdx.x * V; e < end; e += 256 * V) {
+        const auto g = Pack<F32, V>::load(t.grad, e, (int)min(end - e, (int64_t)V));
+#pragma unroll
+        for (int k = 0; k < V; ++k) s = fma((double)g.get(k), (double)g.get(k), s);
+    }
+    s = block_sum(s);
+    if (threadIdx.x == 0) partial[blockIdx.x] = s;
+}
+
+__global__ __launch_bounds__(1024) void norm_kernel(const double *partial, int64_t n, double max_norm, float *norm,
+                                                    float *scale) {
+    double s = 0.0;
+    for (int64_t i = threadIdx.x; i < n; i += 1024) s += partial[i];
+    s = sqrt(block_sum(s));
+    if (threadIdx.x == 0) {
+        *norm = (float)s;
+        // a norm that fp32 does not hold, or none: no step
+        if (scale) *scale = !(s <= 3.402823466e38) ? __builtin_nanf("") : s > max_norm ? (float)(max_norm / s) : 1.0f;
+    }
+}
+
+// ---- host --------------------------------------------------------------------------------
+
+// The next launch's tensors: from `next` on, at most kTensors with elements.  A
+// tensor below 2^40 elements has less than 2^27 workgroups, 48 less than 2^33, so
+// that a launch ends at 2^30.
+constexpr int64_t kMostBlocks = (int64_t)1 << 30, kMostElements = (int64_t)1 << 40;
+int64_t fill(Table &p, const hyena_tensor *ts, int64_t n, int64_t &next, int64_t span) {
+    p.n = 0;
+    int64_t blocks = 0;
+    for (; next < n && p.n < kTensors; ++next) {
+        const hyena_tensor &t = ts[next];
+        if (t.numel == 0) continue;
+        const int64_t more = ceil_div(t.numel, span);
+        if (blocks + more > kMostBlocks) break;
+        p.t[p.n] = Entry{t.param, t.grad, t.exp_avg, t.exp_avg_sq, t.exp_avg_scale, t.exp_avg_sq_scale, t.master, t.numel};
+        p.first[p.n] = (uint32_t)blocks;
+        p.place[p.n++] = (uint32_t)next;
+        blocks += more;
+    }
+    return blocks;
+}
+
+// The descriptors: with their gradients only (bits 0), or all of a step.
+int check_tensors(const hyena_tensor *ts, int64_t n, int dtype, int bits, int64_t *numel) {
+    if (dtype != HYENA_DTYPE_BF16 && dtype != HYENA_DTYPE_F32) return HYENA_ERR_DTYPE;
+    if (n < 0 || n >= (int64_t)1 << 31) return HYENA_ERR_SHAPE;
+    if (n > 0 && !ts) return HYENA_ERR_NULL;
+    const int64_t eb = dtype == HYENA_DTYPE_F32 ? 4 : 2;
+    int64_t all = 0;
+    for (int64_t i = 0; i < n; ++i) {
+        const hyena_tensor &t = ts[i];
+        if (t.numel < 0 || t.numel >= kMostElements) return HYENA_ERR_SHAPE;
+        all += t.numel;
+        if (all >= (int64_t)1 << 56) return HYENA_ERR_SHAPE;
+        if (t.numel == 0) continue;
+        if (!t.grad) return HYENA_ERR_NULL;
+        if (!aligned(t.grad, eb)) return HYENA_ERR_ALIGN;
+        if (bits == 0) continue;
+        if (!t.param || !t.exp_avg || !t.exp_avg_sq || (bits == 8 && (!t.exp_avg_scale || !t.exp_avg_sq_scale)))
+            return HYENA_ERR_NULL;
+        const int64_t sb = bits / 8;
+        if (!aligned(t.param, eb) || !aligned(t.exp_avg, sb) || !aligned(t.exp_avg_sq, sb) || !aligned(t.master, 4) ||
+            (bits == 8 && (!aligned(t.exp_avg_scale, 4) || !aligned(t.exp_avg_sq_scale, 4))))
+            return HYENA_ERR_ALIGN;
+        const int64_t w = t.numel * eb, f = t.numel * 4, c = t.numel * sb, s = ceil_div(t.numel, kBlock) * 4;
+        const Rows r[7] = {{t.param, 1, w, w}, {t.exp_avg, 1, c, c}, {t.exp_avg_sq, 1, c, c}, {t.master, 1, f, f},
+                           {t.grad, 1, w, w}, {bits == 8 ? t.exp_avg_scale : nullptr, 1, s, s},
+                           {bits == 8 ? t.exp_avg_sq_scale : nullptr, 1, s, s}};
+        for (int a = 0; a < 7; ++a)
+            for (int b = 0; b < a; ++b)
+                if (overlap(r[a], r[b])) return HYENA_ERR_ALIAS;
+    }
+    if (numel) *numel = all;
+    return HYENA_OK;
+}
+
+int64_t norm_partials(int64_t n, int64_t numel) { return n + numel / kNormSpan; }
+
+}  // namespace
+}  // namespace layer
+
+using namespace layer;
+
+extern "C" {
+
+int hyena_adamw_step(const hyena_tensor *tensors, int64_t n, double lr, double beta1, double beta2, double eps,
+                     double weight_decay, int64_t step, int64_t seed, const float *lr_dev, const int64_t *step_dev,
+                     const int64_t *seed_dev, const float *grad_scale, int state_bits, int dtype, void *stream) {
+    if (state_bits != 32 && state_bits != 8) return HYENA_ERR_UNSUPPORTED;
+    int st = check_tensors(tensors, n, dtype, state_bits, nullptr);
+    if (st != HYENA_OK) return st;
+    if ((!lr_dev && !isfinite(lr)) || !(beta1 >= 0 && beta1 < 1) || !(beta2 >= 0 && beta2 < 1) || !(eps >= 0) ||
+        !isfinite(eps) || !isfinite(weight_decay) || (!step_dev && step < 1))
+        return HYENA_ERR_UNSUPPORTED;
+    if (!aligned(lr_dev, 4) || !aligned(step_dev, 8) || !aligned(seed_dev, 8) || !aligned(grad_scale, 4))
+        return HYENA_ERR_ALIGN;
+    const bool f32 = dtype == HYENA_DTYPE_F32;
+    AdamParams a = {};
+    a.lr = lr, a.beta1 = beta1, a.beta2 = beta2, a.weight_decay = weight_decay, a.step = step, a.seed = seed;
+    a.lr_dev = lr_dev, a.step_dev = step_dev, a.seed_dev = seed_dev, a.scale = grad_scale, a.eps = (float)eps;
+    const auto kernel = state_bits == 8 ? (f32 ? adamw8_kernel<true> : adamw8_kernel<false>)
+                                        : (f32 ? adamw_kernel<true> : adamw_kernel<false>);
+    Table p;
+    int64_t next = 0;
+    while (const int64_t blocks = fill(p, tensors, n, next, kSpan)) {
+        hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(256), 0, (hipStream_t)stream, p, a);
+        if ((st = launch_status()) != HYENA_OK) return st;
+    }
+    return HYENA_OK;
+}
+
+int hyena_grad_norm_workspace(int64_t n, int64_t numel, int64_t *bytes_out) {
+    if (n < 0 || numel < 0 || n >= (int64_t)1 << 56 || numel >= (int64_t)1 << 56) return HYENA_ERR_SHAPE;
+    if (!bytes_out) return HYENA_ERR_NULL;
+    *bytes_out = ceil_div(norm_partials(n, numel) * 8, 16) * 16;
+    return HYENA_OK;
+}
+
+int hyena_grad_norm(const hyena_tensor *tensors, int64_t n, double max_norm, float *norm, float *scale, void *workspace,
+                    int64_t workspace_bytes, int dtype, void *stream) {
+    int64_t numel = 0, need = 0;
+    int st = check_tensors(tensors, n, dtype, 0, &numel);
+    if (st != HYENA_OK) return st;
+    if (!norm) return HYENA_ERR_NULL;
+    if (scale && !(max_norm >= 0 && isfinite(max_norm))) return HYENA_ERR_UNSUPPORTED;
+    if (!aligned(norm, 4) || !aligned(scale, 4) || !aligned(workspace, 16)) return HYENA_ERR_ALIGN;
+    hyena_grad_norm_workspace(n, numel, &need);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return HYENA_ERR_WORKSPACE;
+    const bool f32 = dtype == HYENA_DTYPE_F32;
+    const Rows out[3] = {{norm, 1, 4, 4}, {scale, 1, 4, 4}, {need > 0 ? workspace : nullptr, 1, need, need}};
+    for (int a = 0; a < 3; ++a) {
+        for (int b = 0; b < a; ++b)
+            if (overlap(out[a], out[b])) return HYENA_ERR_ALIAS;
+        for (int64_t i = 0; i < n; ++i) {
+            const int64_t w = tensors[i].numel * (f32 ? 4 : 2);
+            if (overlap(out[a], Rows{tensors[i].grad, 1, w, w})) return HYENA_ERR_ALIAS;
+        }
+    }
+    double *partial = (double *)workspace;
+    int64_t done = 0, next = 0;
+    Table p;
+    while (const int64_t blocks = fill(p, tensors, n, next, kNormSpan)) {
+        hipLaunchKernelGGL((f32 ? squares_kernel<true> : squares_kernel<false>), dim3((unsigned)blocks), dim3(256), 0,
+                           (hipStream_t)stream, p, partial + done);
+        if ((st = launch_status()) != HYENA_OK) return st;
+        done += blocks;
+    }
+    hipLaunchKernelGGL(norm_kernel, dim3(1), dim3(1024), 0, (hipStream_t)stream, partial, done, max_norm, norm, scale);
+    return launch_status();
+}
+
+const char *hyena_model_strerror(int status) {
+    switch (status) {
+    case HYENA_OK: return "ok";
+    case HYENA_ERR_NULL: return "a required pointer is NULL";
+    case HYENA_ERR_SHAPE: return "a size is negative, too small for another or overflows, or a row stride is shorter than its row";
+    case HYENA_ERR_ALIGN: return "a pointer is not aligned to its elements (workspaces: 16 bytes)";
+    case HYENA_ERR_ALIAS: return "an output overlaps an input or another output";
+    case HYENA_ERR_UNSUPPORTED: return "unknown kind or state size, a mean for the rms kind, a scalar out of its range, or a size too large to launch";
+    case HYENA_ERR_LAUNCH: return "kernel launch failed";
+    case HYENA_ERR_DTYPE: return "unknown dtype code";
+    case HYENA_ERR_WORKSPACE: return "workspace missing or smaller than the operator's workspace call reports";
+    default: return "unknown status";
+    }
+}
+
+}  // extern "C"

@@ -1,0 +1,854 @@
+// Softmax cross entropy of a readout over a vocabulary, without keeping the
+// logits, and its gradients, for MI355X (gfx950) (hyena_model.h has the formulas
+// and layouts).
+//
+// Bound by the matrix cores: one product (2 M K V) forward and three backward,
+// since the logits are formed again.  The products are layer_gemm.h's tiles.
+//   * Rows without a target are left out: rank_kernel numbers the others in
+//     order, pack_kernel copies their x to rows of whole 16 bytes, and every
+//     product after that reads the number of rows from memory.  So such rows cost
+//     no products, and what their x holds (NaN from padding) meets no zero in dw's
+//     sums.  The copy costs 2 % of a forward at K = 4096, V = 65536 and lets the
+//     products fetch odd sizes and strides straight into LDS (w is copied too where
+//     its rows are no whole 16 bytes).
+//   * Forward: a tile keeps the maximum and the sum of exp(z - maximum) of its
+//     columns for each row, from the registers that hold the sums; merge_kernel
+//     joins the tiles.
+//   * Backward, a piece of the vocabulary at a time: the logits again with dz as
+//     their epilogue (in bf16 dz is rounded, as the matrix cores take it; db sums it
+//     unrounded), then dw = dz^T x of the piece and dx += dz w in fp32, rounded
+//     after the last piece.
+//   * No more than 16 rows forward: the weights stream once through rows_product.
+
+#include "hyena_model.h"
+#include "layer_gemm.h"
+
+namespace layer {
+namespace {
+
+// ---- maxima and sums of a softmax ---------------------------------------------------
+
+// (m, s) stands for the values' maximum m and the sum of exp(z - m); where m is
+// infinite, of exp(z), which is 0 (m = -inf: no value can occur) or inf.
+struct Part {
+    float m, s;
+};
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+__device__ inline float shift_of(float m) { return fabsf(m) == __builtin_inff() ? 0.0f : m; }
+__device__ inline void join(Part &a, const Part &b) {
+    const float m = fmaxf(a.m, b.m);
+    a.s = a.s * (a.m == m ? 1.0f : __expf(a.m - m)) + b.s * (b.m == m ? 1.0f : __expf(b.m - m));
+    a.m = m;
+}
+
+// What a forward tile does with its sums.
+struct StatsEpi {
+    static constexpr bool kSums = true;
+    const void *bias;
+    const int *target;  // of each packed row
+    Part *part;         // [tiles of columns][row capacity]
+    float *at;          // the target's logit of each row
+    int64_t ldp;
+    int M, N;
+
+    // columns(), before(), finish() and close() are not reached
+    template <bool F32, int V> __device__ Pack<F32, V> columns(int) const { return Pack<F32, V>::zero(); }
+    template <bool F32, int V> __device__ int before(int64_t, int) const { return 0; }
+    template <bool F32, int V> __device__ void finish(int64_t, int, float (&)[V], const Pack<F32, V> &, int) const {}
+    template <bool F32, int V> __device__ void close(const Pack<F32, V> &, int, int, int) const {}
+
+    // A lane holds columns 16 u + 4 j + e of rows 16 t + i of its wave's part of the
+    // tile: its own 16 columns first, then the four lanes of a row, then the waves.
+    template <class S, class G, int MT, int NTL>
+    __device__ __forceinline__ void sums(const G &p, f32x4_t (&acc)[MT][NTL], int m0, int n0, int wm, int wn,
+                                         LDS_PTR unsigned char *lds) const {
+        constexpr bool F32 = S::CE == 4;
+        constexpr int WN = S::BN / (NTL * 16);
+        const int i = threadIdx.x & 15, j = (threadIdx.x >> 4) & 3;
+        const int tn = n0 / S::BN;
+        LDS_PTR f32x2_t *meet = (LDS_PTR f32x2_t *)lds;
+        const int first = n0 + wn + j * 4;
+        const bool edge = n0 + S::BN > N;  // columns past the vocabulary
+        float b[NTL][4];
+#pragma unroll
+        for (int u = 0; u < NTL; ++u) {
+            const int left = N - (first + u * 16);
+            const auto r = bias && left > 0 ? Pack<F32, 4>::load(bias, first + u * 16, left) : Pack<F32, 4>::zero();
+#pragma unroll
+            for (int e = 0; e < 4; ++e) b[u][e] = r.get(e);
+        }
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+            const int m = m0 + wm + t * 16 + i;
+            const int goal = m < M ? target[m] : -1;
+            Part r = {-__builtin_inff(), 0.0f};
+            float hit = 0.0f;
+            bool here = false;
+#pragma unroll
+            for (int u = 0; u < NTL; ++u)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int n = first + u * 16 + e;
+                    acc[t][u][e] += b[u][e];
+                    if (edge && n >= N) acc[t][u][e] = -__builtin_inff();
+                    r.m = fmaxf(r.m, acc[t][u][e]);
+                    if (n == goal) hit = acc[t][u][e], here = true;
+                }
+            r.m = fmaxf(r.m, __shfl_xor(r.m, 16));
+            r.m = fmaxf(r.m, __shfl_xor(r.m, 32));
+            const float shift = shift_of(r.m);
+#pragma unroll
+            for (int u = 0; u < NTL; ++u)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) r.s += __expf(acc[t][u][e] - shift);
+            r.s += __shfl_xor(r.s, 16);
+            r.s += __shfl_xor(r.s, 32);
+            if (here) at[m] = hit;
+            if (j == 0) {
+                if constexpr (WN == 1) {
+                    if (m < M) part[tn * ldp + m] = r;
+                } else {
+                    meet[(wn / (NTL * 16)) * S::BM + wm + t * 16 + i] = f32x2_t{r.m, r.s};
+                }
+            }
+        }
+        if constexpr (WN > 1) {
+            __syncthreads();
+            for (int row = threadIdx.x; row < S::BM; row += S::NT) {
+                f32x2_t o = meet[row];
+                Part r = {o[0], o[1]};
+#pragma unroll
+                for (int w = 1; w < WN; ++w) {
+                    o = meet[w * S::BM + row];
+                    join(r, Part{o[0], o[1]});
+                }
+                if (m0 + row < M) part[tn * ldp + m0 + row] = r;
+            }
+        }
+    }
+};
+
+// The rows of `count` take the place of the upper bound that the host planned with.
+template <class S, class E> __device__ inline bool rows_from(Gemm<E> &p, const int *count) {
+    p.M = *count;
+    p.e.M = p.M;
+    p.tiles_m = (p.M + S::BM - 1) / S::BM;
+    return (int)blockIdx.x < p.tiles_m * p.tiles_n * p.splits;
+}
+
+template <bool F32, bool DIRECT, typename S>
+__global__ __launch_bounds__(S::NT, S::WAVES) void stats_kernel(Gemm<StatsEpi> p, const int *count) {
+    TILE_BUFFERS(S)
+    if (!rows_from<S>(p, count)) return;
+    run_tile<false, false, DIRECT, S>(p, blockIdx.x, a0, a1, a2, a3, b0, b1, b2, b3);
+}
+
+// Few rows: 16 columns a workgroup; columns of four lanes a row.
+struct RowStats {
+    const void *bias;
+    const int64_t *target;
+    Part *part;
+    float *at;
+    int64_t ldp;
+    int M, N;
+    template <bool F32, int V> __device__ Pack<F32, V> columns(int n) const {
+        return bias && n < N ? Pack<F32, V>::load(bias, n, N - n) : Pack<F32, V>::zero();
+    }
+    template <bool F32, int V> __device__ int64_t before(int64_t m, int) const { return m < M ? target[m] : -1; }
+    template <bool F32, int V>
+    __device__ void finish(int64_t m, int n, float (&z)[V], const Pack<F32, V> &bias, int64_t goal) const {
+        Part r = {-__builtin_inff(), 0.0f};
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            z[e] = n + e < N ? z[e] + bias.get(e) : -__builtin_inff();
+            r.m = fmaxf(r.m, z[e]);
+            if (n + e == goal) at[m] = z[e];
+        }
+        r.m = fmaxf(r.m, __shfl_xor(r.m, 1));
+        r.m = fmaxf(r.m, __shfl_xor(r.m, 2));
+        const float shift = shift_of(r.m);
+#pragma unroll
+        for (int e = 0; e < V; ++e) r.s += __expf(z[e] - shift);
+        r.s += __shfl_xor(r.s, 1);
+        r.s += __shfl_xor(r.s, 2);
+        if ((threadIdx.x & 3) == 0 && m < M) part[(n / 16) * ldp + m] = r;
+    }
+    template <bool F32, int V> __device__ void close(const Pack<F32, V> &, int, int, int) const {}
+};
+template <bool F32> __global__ __launch_bounds__(64 * kRowWaves) void rows_stats_kernel(RowsParams<RowStats> p) {
+    __shared__ __attribute__((aligned(16))) float sums[kRowWaves][1][16][16];
+    rows_product<F32, 1>(p, sums);
+}
+
+// Loss and lse of each row from its tiles: 32 rows a workgroup, eight lanes each.
+struct MergeParams {
+    const Part *part;
+    const float *at;
+    const int *index, *count;  // the packed rows' places and their number, or null:
+    const int64_t *target;     // every row in place, those without a target among them
+    float *loss, *lse;
+    int64_t ldp, V;
+    int tiles, M;
+};
+__global__ __launch_bounds__(256) void merge_kernel(MergeParams p) {
+    __shared__ Part meet[8][32];
+    const int row = threadIdx.x & 31, slice = threadIdx.x >> 5;
+    const int m = blockIdx.x * 32 + row, rows = p.count ? *p.count : p.M;
+    Part r = {-__builtin_inff(), 0.0f};
+    if (m < rows) {
+#pragma unroll 4
+        for (int t = slice; t < p.tiles; t += 8) join(r, p.part[t * p.ldp + m]);
+    }
+    meet[slice][row] = r;
+    __syncthreads();
+    if (slice != 0 || m >= rows) return;
+#pragma unroll
+    for (int s = 1; s < 8; ++s) join(r, meet[s][row]);
+    const int64_t to = p.index ? p.index[m] : m;
+    const bool on = p.index || (uint64_t)p.target[m] < (uint64_t)p.V;
+    const float lse = shift_of(r.m) + __logf(r.s);
+    p.loss[to] = on ? lse - p.at[m] : 0.0f;
+    p.lse[to] = on ? lse : 0.0f;
+}
+
+// ---- rows with a target ----------------------------------------------------------------
+
+// Numbers the rows that have a target, in order, and brings what belongs to them
+// together; the others' loss and lse are 0.  One workgroup, 8192 targets a turn: a
+// millisecond for each 4 million rows, whose products take minutes.
+struct RankParams {
+    const int64_t *target;
+    const float *lse_in, *dloss;  // backward
+    float *lse_out, *dloss_out;   // packed
+    float *loss, *lse;            // forward: zeroed where there is no target
+    int *rank, *index, *goal, *count;
+    int64_t V;
+    int M;
+};
+__global__ __launch_bounds__(1024) void rank_kernel(RankParams p) {
+    __shared__ int waves[8][16];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int base = 0;
+    for (int64_t first = 0; first < p.M; first += 8192) {
+        int goal[8], before[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int64_t m = first + k * 1024 + threadIdx.x;
+            const int64_t t = m < p.M ? p.target[m] : -1;
+            goal[k] = (uint64_t)t < (uint64_t)p.V ? (int)t : -1;
+            const uint64_t on = __builtin_amdgcn_ballot_w64(goal[k] >= 0);
+            before[k] = __popcll(on & (((uint64_t)1 << lane) - 1));
+            if (lane == 0) waves[k][wave] = __popcll(on);
+        }
+        __syncthreads();
+        int sum = base;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            int mine = sum;
+#pragma unroll
+            for (int w = 0; w < 16; ++w) {
+                const int n = waves[k][w];
+                if (w < wave) mine += n;
+                sum += n;
+            }
+            const int64_t m = first + k * 1024 + threadIdx.x;
+            if (m >= p.M) continue;
+            const int at = mine + before[k];
+            p.rank[m] = goal[k] >= 0 ? at : -1;
+            if (goal[k] >= 0) {
+                p.index[at] = (int)m;
+                p.goal[at] = goal[k];
+                if (p.lse_in) p.lse_out[at] = p.lse_in[m], p.dloss_out[at] = p.dloss[m];
+            } else if (p.loss) {
+                p.loss[m] = 0.0f, p.lse[m] = 0.0f;
+            }
+        }
+        base = sum;
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) *p.count = base;
+}
+
+// Rows of x with a target to rows of whole 16 bytes, zeros behind them; dx of the
+// others to zero; and w to such rows where its own are not.  A wave a row.
+struct PackParams {
+    const void *from[2];  // x, w (null: as it is)
+    void *to[2];
+    int64_t rows[2], ld[2];
+    const int *rank;
+    void *dx;
+    int64_t lddx;
+    int K, chunks;
+};
+template <bool F32> __global__ __launch_bounds__(256) void pack_kernel(PackParams p) {
+    using T = typename El<F32>::type;
+    constexpr int CE = El<F32>::CE;
+    const int lane = threadIdx.x & 63;
+    const int64_t step = (int64_t)gridDim.x * 4, start = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+        if (!p.from[g]) continue;
+        for (int64_t row = start; row < p.rows[g]; row += step) {
+            const int64_t at = g == 0 ? p.rank[row] : row;
+            if (at < 0) {
+                if (p.dx) {
+                    const float none[CE] = {};
+                    for (int c = lane; c < p.chunks; c += 64)
+                        Pack<F32, CE>::store(p.dx, row * p.lddx + c * CE, p.K - c * CE, none);
+                }
+                continue;
+            }
+            const T *from = (const T *)p.from[g] + row * p.ld[g];
+            u32x4_t *to = (u32x4_t *)p.to[g] + at * p.chunks;
+#pragma unroll 4
+            for (int c = lane; c < p.chunks; c += 64) {
+                const int left = p.K - c * CE;
+                u32x4_t v;
+                if (left >= CE) {
+                    v = *(const typename El<F32>::chunk_any *)(from + c * CE);
+                } else {
+                    T x[CE];
+#pragma unroll
+                    for (int e = 0; e < CE; ++e) x[e] = e < left ? from[c * CE + e] : (T)0.0f;
+                    v = __builtin_bit_cast(u32x4_t, x);
+                }
+                to[c] = v;
+            }
+        }
+    }
+}
+
+// ---- gradients ------------------------------------------------------------------------
+
+// The logits' epilogue in the backward: dz of a piece, and its column sums.
+struct DzEpi {
+    static constexpr bool kSums = false;
+    const void *bias;           // of the piece
+    const float *lse, *dloss;   // packed
+    const int *target;          // packed, of the whole vocabulary
+    void *dz;                   // [rows][ld], ld whole 16 bytes, zeros behind the columns
+    float *sums;                // [row blocks][N] or null
+    int64_t ld;
+    int v0;                     // the piece's first entry
+    int M, N;
+
+    template <bool F32, int V> struct Columns {
+        Pack<F32, V> bias;
+        float sum[V];
+    };
+    struct Row {
+        float lse, dloss;
+        int target;
+    };
+    template <bool F32, int V> __device__ __forceinline__ Columns<F32, V> columns(int n) const {
+        Columns<F32, V> c = {bias && n < N ? Pack<F32, V>::load(bias, n, N - n) : Pack<F32, V>::zero(), {}};
+        return c;
+    }
+    template <bool F32, int V> __device__ __forceinline__ Row before(int64_t m, int) const {
+        return m < M ? Row{lse[m], dloss[m], target[m] - v0} : Row{};
+    }
+    template <bool F32, int V>
+    __device__ __forceinline__ void finish(int64_t m, int n, float (&z)[V], Columns<F32, V> &c, const Row &r) const {
+        if (m >= M || n >= ld) return;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const float p = __expf(z[e] + c.bias.get(e) - r.lse);
+            z[e] = n + e < N ? r.dloss * (n + e == r.target ? p - 1.0f : p) : 0.0f;
+            c.sum[e] += z[e];
+        }
+        Pack<F32, V>::store(dz, m * ld + n, (int)(ld - n), z);
+    }
+    template <bool F32, int V> __device__ __forceinline__ void close(const Columns<F32, V> &c, int m, int block, int n) const {
+        if (!sums || m >= M) return;  // eight lanes a row, the wave's eight rows at a time
+        float s[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            s[e] = c.sum[e];
+#pragma unroll
+            for (int o = 8; o < 64; o <<= 1) s[e] += __shfl_xor(s[e], o);
+        }
+        if ((threadIdx.x & 63) < 8 && n < N) Pack<true, V>::store(sums, (int64_t)block * N + n, N - n, s);
+    }
+};
+
+// The gradients' epilogue.  ACC: rows are put in place by `index`, and pieces of
+// the vocabulary are added up in fp32.
+template <bool ACC> struct GradEpi {
+    static constexpr bool kSums = false;
+    void *y;
+    const float *from;   // what the pieces before gave, or null
+    float *to;           // where the sum goes, or null: y
+    const int *index;
+    int64_t ldy;
+    int M, N;
+
+    template <bool F32, int V> struct Row {
+        Pack<true, V> sum;
+        int64_t at;
+    };
+    struct None {};
+    template <bool F32, int V> __device__ __forceinline__ None columns(int) const { return None{}; }
+    template <bool F32, int V> __device__ __forceinline__ auto before(int64_t m, int n) const {
+        if constexpr (ACC) {
+            Row<F32, V> r = {Pack<true, V>::zero(), 0};
+            if (m < M && n < N) {
+                if (from) r.sum = Pack<true, V>::load(from, m * N + n, N - n);
+                r.at = index[m];
+            }
+            return r;
+        } else {
+            return None{};
+        }
+    }
+    template <bool F32, int V, class R>
+    __device__ __forceinline__ void finish(int64_t m, int n, float (&z)[V], const None &, const R &r) const {
+        if (m >= M || n >= N) return;
+        if constexpr (ACC) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) z[e] += r.sum.get(e);
+            if (to) Pack<true, V>::store(to, m * N + n, N - n, z);
+            else Pack<F32, V>::store(y, r.at * ldy + n, N - n, z);
+        } else {
+            Pack<F32, V>::store(y, m * ldy + n, N - n, z);
+        }
+    }
+    template <bool F32, int V> __device__ __forceinline__ void close(const None &, int, int, int) const {}
+};
+using DwEpi = GradEpi<false>;
+using DxEpi = GradEpi<true>;
+
+template <bool F32, bool DIRECT, typename S>
+__global__ __launch_bounds__(S::NT, S::WAVES) void dz_kernel(Gemm<DzEpi> p, const int *count) {
+    TILE_BUFFERS(S)
+    if (!rows_from<S>(p, count)) return;
+    run_tile<false, false, DIRECT, S>(p, blockIdx.x, a0, a1, a2, a3, b0, b1, b2, b3);
+}
+
+// dw's sum runs over the rows: their number, cut anew between the splits.
+template <bool F32> __device__ inline void sum_from(Gemm<DwEpi> &p, const int *count) {
+    constexpr int BK = 8 * El<F32>::CE;
+    p.C = *count;
+    const int steps = (p.C + BK - 1) / BK;
+    p.c_per_split = max((steps + p.splits - 1) / p.splits, 1) * BK;
+}
+
+// The first `blocks` workgroups form dw, the others dx.
+template <bool F32, bool DIRECT, typename S>
+__global__ __launch_bounds__(S::NT, S::WAVES) void grads_kernel(Gemm<DwEpi> dw, Gemm<DxEpi> dx, int blocks, const int *count) {
+    TILE_BUFFERS(S)
+    if ((int)blockIdx.x < blocks) {
+        sum_from<F32>(dw, count);
+        run_tile<true, true, DIRECT, S>(dw, blockIdx.x, a0, a1, a2, a3, b0, b1, b2, b3);
+    } else {
+        dx.M = dx.e.M = *count;
+        dx.tiles_m = (dx.M + S::BM - 1) / S::BM;
+        const int block = blockIdx.x - blocks;
+        if (block >= dx.tiles_m * dx.tiles_n * dx.splits) return;
+        run_tile<false, true, DIRECT, S>(dx, block, a0, a1, a2, a3, b0, b1, b2, b3);
+    }
+}
+// One of them, in tiles of 256 x 256.
+template <typename S> __global__ __launch_bounds__(S::NT, S::WAVES) void large_dw_kernel(Gemm<DwEpi> p, const int *count) {
+    TILE_BUFFERS(S)
+    sum_from<false>(p, count);
+    run_tile<true, true, true, S>(p, blockIdx.x, a0, a1, a2, a3, b0, b1, b2, b3);
+}
+template <typename S> __global__ __launch_bounds__(S::NT, S::WAVES) void large_dx_kernel(Gemm<DxEpi> p, const int *count) {
+    TILE_BUFFERS(S)
+    if (!rows_from<S>(p, count)) return;
+    run_tile<false, true, true, S>(p, blockIdx.x, a0, a1, a2, a3, b0, b1, b2, b3);
+}
+
+// What remains of a piece: the sums of splits, and db from the row blocks' sums.
+struct JoinParams {
+    Gemm<DwEpi> dw;
+    Gemm<DxEpi> dx;
+    int64_t blocks[2];
+    const float *sums;
+    const int *count;
+    int rows;  // rows of a row block of the sums
+    int N;
+    void *db;
+};
+template <bool F32> __global__ __launch_bounds__(256) void join_kernel(JoinParams p) {
+    __shared__ float part[4][64];
+    int64_t block = blockIdx.x;
+    const int count = *p.count;
+    if (block < p.blocks[0]) return sum_splits<F32>(p.dw, block * 256 + threadIdx.x);
+    block -= p.blocks[0];
+    if (block < p.blocks[1]) {
+        p.dx.M = p.dx.e.M = count;
+        return sum_splits<F32>(p.dx, block * 256 + threadIdx.x);
+    }
+    block -= p.blocks[1];
+    const int c = threadIdx.x & 63, r = threadIdx.x >> 6, n_sums = (count + p.rows - 1) / p.rows;
+    const int64_t n = block * 64 + c;
+    float s = 0.0f;
+    if (n < p.N) {
+#pragma unroll 8
+        for (int b = r; b < n_sums; b += 4) s += p.sums[(int64_t)b * p.N + n];
+    }
+    part[r][c] = s;
+    __syncthreads();
+    if (r == 0 && n < p.N) store1<F32>(p.db, n, part[0][c] + part[1][c] + part[2][c] + part[3][c]);
+}
+
+// ---- host --------------------------------------------------------------------------------
+
+enum Tile { kLarge, kDeep, kSmall, kFineDeep, kFine };
+Tile tile_of(const Plan &p) { return p.large ? kLarge : p.fine ? (p.deep ? kFineDeep : kFine) : p.deep ? kDeep : kSmall; }
+// Rows of one wave, which leave one row of column sums: of a tile's WM x MT x 16.
+int wave_rows(const Plan &p) { return p.large ? 128 : p.fine ? 16 : 64; }
+
+// A product whose epilogue wants whole sums: its c is not cut.
+Plan whole_plan(int64_t M, int64_t N, int64_t K, bool f32, bool direct) {
+    const Size sz = {M, N, K};
+    Plan p = plan_of(&sz, 1, f32, direct);
+    p.splits[0] = 1;
+    p.c_per_split[0] = (int)(ceil_div(K, f32 ? 32 : 64) * (f32 ? 32 : 64));
+    p.blocks[0] = (int64_t)p.tiles_m[0] * p.tiles_n[0];
+    p.partial[0] = 0;
+    return p;
+}
+
+int64_t round16(int64_t n) { return ceil_div(n, 16) * 16; }
+
+constexpr int64_t kFewRows = 16;  // rows_product's
+
+// The forward's workspace.
+struct FwdSpace {
+    int64_t count, rank, index, goal, at, part, x, w, total;
+};
+FwdSpace fwd_space(int64_t M, int64_t K, int64_t V, bool f32) {
+    const int64_t eb = f32 ? 4 : 2;
+    FwdSpace s = {};
+    int64_t n = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t at = n;
+        n += round16(bytes);
+        return at;
+    };
+    if (M <= kFewRows) {
+        s.at = take(M * 4), s.part = take(ceil_div(V, 16) * M * 8);
+    } else {
+        // w may lie at any element, which the caller of hyena_xent_workspace does not say
+        const int64_t tiles[2] = {whole_plan(M, V, K, f32, false).tiles_n[0], whole_plan(M, V, K, f32, true).tiles_n[0]};
+        s.count = take(4), s.rank = take(M * 4), s.index = take(M * 4), s.goal = take(M * 4), s.at = take(M * 4);
+        s.part = take((tiles[0] > tiles[1] ? tiles[0] : tiles[1]) * M * 8);
+        s.x = take(M * whole(K, eb) * eb);
+        s.w = take(whole(K, eb) != K ? V * whole(K, eb) * eb : 0);
+    }
+    s.total = n;
+    return s;
+}
+
+// Entries of the vocabulary a piece of the backward takes: dz of a piece is some
+// 256 MB, or 2048 entries where the rows are many.
+int64_t piece_of(int64_t M, int64_t V, int64_t eb) {
+    int64_t most = ((int64_t)1 << 28) / ((M > 0 ? M : 1) * eb) / 256 * 256;
+    if (most < 2048) most = 2048;
+    if (most > (int64_t)1 << 18) most = (int64_t)1 << 18;
+    const int64_t pieces = ceil_div(V, most);
+    return pieces == 1 ? V : ceil_div(ceil_div(V, pieces), 256) * 256;
+}
+
+struct BwdSpace {
+    int64_t count, rank, index, goal, lse, dloss, x, w, dz, sums, acc, partial, total;
+    int64_t piece;
+};
+BwdSpace bwd_space(int64_t M, int64_t K, int64_t V, bool f32) {
+    const int64_t eb = f32 ? 4 : 2;
+    BwdSpace s = {};
+    int64_t n = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t at = n;
+        n += round16(bytes);
+        return at;
+    };
+    s.piece = piece_of(M, V, eb);
+    s.count = take(4), s.rank = take(M * 4), s.index = take(M * 4), s.goal = take(M * 4);
+    s.lse = take(M * 4), s.dloss = take(M * 4);
+    s.x = take(M * whole(K, eb) * eb);
+    s.w = take(whole(K, eb) != K ? V * whole(K, eb) * eb : 0);
+    s.dz = take(M * whole(s.piece, eb) * eb);
+    int64_t sums = 0, partial = 0;
+    for (int64_t v0 = 0; v0 < V; v0 += s.piece) {  // the first and the last piece
+        const int64_t N = V - v0 < s.piece ? V - v0 : s.piece;
+        for (bool direct : {false, true}) {  // w may lie at any element
+            const int64_t b = ceil_div(M, wave_rows(whole_plan(M, N, K, f32, direct))) * N * 4;
+            if (b > sums) sums = b;
+        }
+        const Size both[2] = {{N, K, M}, {M, K, N}};
+        for (int64_t bytes : {partial_bytes(both, 2, f32), partial_bytes(both, 1, f32), partial_bytes(both + 1, 1, f32)})
+            if (bytes > partial) partial = bytes;
+        if (v0 == 0 && V > s.piece) v0 = (ceil_div(V, s.piece) - 2) * s.piece;
+    }
+    s.sums = take(sums), s.acc = take(V > s.piece ? M * K * 4 : 0), s.partial = take(partial);
+    s.total = n;
+    return s;
+}
+
+template <bool F32> int launch_pack(const PackParams &p, hipStream_t stream) {
+    int64_t rows = p.from[0] ? p.rows[0] : 0;
+    if (p.from[1] && p.rows[1] > rows) rows = p.rows[1];
+    const int64_t blocks = ceil_div(rows, 4);
+    if (blocks == 0 || p.chunks == 0) return HYENA_OK;
+    hipLaunchKernelGGL(pack_kernel<F32>, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, stream, p);
+    return launch_status();
+}
+
+// LAUNCH(DIRECT, S) for the plan's tiles.
+#define FOR_TILE(plan, direct, LAUNCH)                                       \
+    switch (tile_of(plan)) {                                                 \
+    case kLarge: if constexpr (!F32) { LAUNCH(true, Large) } break;          \
+    case kDeep: LAUNCH(true, Deep<F32>) break;                               \
+    case kFineDeep: if constexpr (!F32) { LAUNCH(true, FineDeep) } break;    \
+    case kSmall:                                                             \
+        if (direct) { LAUNCH(true, Small<F32>) } else { LAUNCH(false, Small<F32>) } \
+        break;                                                               \
+    case kFine:                                                              \
+        if (direct) { LAUNCH(true, Fine<F32>) } else { LAUNCH(false, Fine<F32>) } \
+        break;                                                               \
+    }
+
+template <bool F32>
+int xent_fwd(const void *x, const void *w, const void *bias, const int64_t *target, int64_t M, int64_t K, int64_t V,
+             int64_t ldx, float *loss, float *lse, char *ws, hipStream_t stream) {
+    const int64_t eb = F32 ? 4 : 2;
+    const FwdSpace sp = fwd_space(M, K, V, F32);
+    MergeParams mp = {};
+    mp.part = (Part *)(ws + sp.part), mp.at = (float *)(ws + sp.at), mp.ldp = M, mp.V = V, mp.M = (int)M;
+    mp.loss = loss, mp.lse = lse;
+    int st;
+    if (M <= kFewRows) {
+        RowsParams<RowStats> p = {};
+        p.x = x, p.w = w, p.ldx = ldx, p.M = (int)M, p.N = (int)V, p.K = (int)K;
+        p.e.bias = bias, p.e.target = target, p.e.part = (Part *)(ws + sp.part), p.e.at = (float *)(ws + sp.at);
+        p.e.ldp = M, p.e.M = p.M, p.e.N = p.N;
+        mp.tiles = (int)ceil_div(V, 16), mp.target = target;
+        hipLaunchKernelGGL(rows_stats_kernel<F32>, dim3((unsigned)mp.tiles), dim3(64 * kRowWaves), 0, stream, p);
+        if ((st = launch_status()) != HYENA_OK) return st;
+    } else {
+        RankParams r = {};
+        r.target = target, r.loss = loss, r.lse = lse, r.V = V, r.M = (int)M;
+        r.rank = (int *)(ws + sp.rank), r.index = (int *)(ws + sp.index), r.goal = (int *)(ws + sp.goal);
+        r.count = (int *)(ws + sp.count);
+        hipLaunchKernelGGL(rank_kernel, dim3(1), dim3(1024), 0, stream, r);
+        if ((st = launch_status()) != HYENA_OK) return st;
+        const int64_t ld = whole(K, eb);
+        PackParams k = {};
+        k.from[0] = x, k.to[0] = ws + sp.x, k.rows[0] = M, k.ld[0] = ldx, k.rank = r.rank;
+        if (ld != K) k.from[1] = w, k.to[1] = ws + sp.w, k.rows[1] = V, k.ld[1] = K;
+        k.K = (int)K, k.chunks = (int)(ld * eb / 16);
+        if ((st = launch_pack<F32>(k, stream)) != HYENA_OK) return st;
+        const bool direct = k.from[1] || direct_ok(w, K, K, eb);
+        const Plan pl = whole_plan(M, V, K, F32, direct);
+        if (pl.blocks[0] > 0x7fffffff) return HYENA_ERR_UNSUPPORTED;
+        StatsEpi e = {};
+        e.bias = bias, e.target = r.goal, e.part = (Part *)(ws + sp.part), e.at = (float *)(ws + sp.at), e.ldp = M;
+        char *none = nullptr;
+        const Gemm<StatsEpi> p = gemm_params(pl, 0, Size{M, V, K}, k.to[0], ld, k.from[1] ? k.to[1] : w,
+                                             k.from[1] ? ld : K, e, none);
+#define STATS(DIRECT, S) \
+    hipLaunchKernelGGL((stats_kernel<F32, DIRECT, S>), dim3((unsigned)pl.blocks[0]), dim3(S::NT), 0, stream, p, r.count);
+        FOR_TILE(pl, direct, STATS)
+#undef STATS
+        if ((st = launch_status()) != HYENA_OK) return st;
+        mp.tiles = pl.tiles_n[0], mp.index = r.index, mp.count = r.count;
+    }
+    hipLaunchKernelGGL(merge_kernel, dim3((unsigned)ceil_div(M, 32)), dim3(256), 0, stream, mp);
+    return launch_status();
+}
+
+template <bool F32>
+int xent_bwd(const void *x, const void *w, const void *bias, const int64_t *target, const float *lse, const float *dloss,
+             int64_t M, int64_t K, int64_t V, int64_t ldx, int64_t lddx, void *dx, void *dw, void *db, char *ws,
+             hipStream_t stream) {
+    const int64_t eb = F32 ? 4 : 2;
+    const BwdSpace sp = bwd_space(M, K, V, F32);
+    int st;
+    RankParams r = {};
+    r.target = target, r.lse_in = lse, r.dloss = dloss, r.V = V, r.M = (int)M;
+    r.lse_out = (float *)(ws + sp.lse), r.dloss_out = (float *)(ws + sp.dloss);
+    r.rank = (int *)(ws + sp.rank), r.index = (int *)(ws + sp.index), r.goal = (int *)(ws + sp.goal);
+    r.count = (int *)(ws + sp.count);
+    hipLaunchKernelGGL(rank_kernel, dim3(1), dim3(1024), 0, stream, r);
+    if ((st = launch_status()) != HYENA_OK) return st;
+    const int64_t ld = whole(K, eb);
+    PackParams k = {};
+    k.from[0] = x, k.to[0] = ws + sp.x, k.rows[0] = M, k.ld[0] = ldx, k.rank = r.rank, k.dx = dx, k.lddx = lddx;
+    if (ld != K) k.from[1] = w, k.to[1] = ws + sp.w, k.rows[1] = V, k.ld[1] = K;
+    k.K = (int)K, k.chunks = (int)(ld * eb / 16);
+    if ((st = launch_pack<F32>(k, stream)) != HYENA_OK) return st;
+    const char *wp = (const char *)(k.from[1] ? k.to[1] : w);
+    const int64_t ldw = k.from[1] ? ld : K;
+    const bool direct = k.from[1] || direct_ok(w, K, K, eb);  // of each piece, rows being whole 16 bytes
+    for (int64_t v0 = 0; v0 < V; v0 += sp.piece) {
+        const int64_t N = V - v0 < sp.piece ? V - v0 : sp.piece, ldz = whole(N, eb);
+        const char *wv = wp + v0 * ldw * eb;
+        const Plan pl = whole_plan(M, N, K, F32, direct);
+        if (pl.blocks[0] > 0x7fffffff) return HYENA_ERR_UNSUPPORTED;
+        DzEpi e = {};
+        e.bias = bias ? (const char *)bias + v0 * eb : nullptr, e.lse = r.lse_out, e.dloss = r.dloss_out, e.target = r.goal;
+        e.dz = ws + sp.dz, e.ld = ldz, e.sums = db ? (float *)(ws + sp.sums) : nullptr, e.v0 = (int)v0;
+        char *none = nullptr;
+        const Gemm<DzEpi> p = gemm_params(pl, 0, Size{M, N, K}, k.to[0], ld, wv, ldw, e, none);
+#define DZ(DIRECT, S) \
+    hipLaunchKernelGGL((dz_kernel<F32, DIRECT, S>), dim3((unsigned)pl.blocks[0]), dim3(S::NT), 0, stream, p, r.count);
+        if (M > 0) FOR_TILE(pl, direct, DZ)
+#undef DZ
+        if ((st = launch_status()) != HYENA_OK) return st;
+
+        JoinParams j = {};
+        j.count = r.count;
+        if (dw || dx) {
+            Size sz[2];
+            int n = 0;
+            if (dw) sz[n++] = Size{N, K, M};
+            if (dx) sz[n++] = Size{M, K, N};
+            const Plan gp = plan_of(sz, n, F32, direct);
+            const int64_t blocks = gp.blocks[0] + gp.blocks[1];
+            if (blocks > 0x7fffffff) return HYENA_ERR_UNSUPPORTED;
+            char *at = ws + sp.partial;
+            int g = 0;
+            if (dw) {
+                DwEpi o = {};
+                o.y = (char *)dw + v0 * K * eb, o.ldy = K;
+                j.dw = gemm_params(gp, g, sz[g], e.dz, ldz, k.to[0], ld, o, at);
+                if (j.dw.partial) j.blocks[0] = ceil_div(N * ceil_div(K, 4), 256);
+                ++g;
+            }
+            if (dx) {
+                DxEpi o = {};
+                float *acc = (float *)(ws + sp.acc);
+                o.y = dx, o.ldy = lddx, o.index = r.index;
+                o.from = v0 > 0 ? acc : nullptr, o.to = v0 + N < V ? acc : nullptr;
+                j.dx = gemm_params(gp, g, sz[g], e.dz, ldz, wv, ldw, o, at);
+                if (j.dx.partial) j.blocks[1] = ceil_div(M * ceil_div(K, 4), 256);
+            }
+            const int first = dw ? (int)gp.blocks[0] : 0;
+            if (gp.large) {
+                if constexpr (!F32) {
+                    if (dw) hipLaunchKernelGGL((large_dw_kernel<Large>), dim3((unsigned)first), dim3(Large::NT), 0, stream, j.dw, r.count);
+                    if (dx)
+                        hipLaunchKernelGGL((large_dx_kernel<Large>), dim3((unsigned)(blocks - first)), dim3(Large::NT), 0,
+                                           stream, j.dx, r.count);
+                }
+            } else {
+#define GRADS(DIRECT, S)                                                                                                \
+    hipLaunchKernelGGL((grads_kernel<F32, DIRECT, S>), dim3((unsigned)blocks), dim3(S::NT), 0, stream, j.dw, j.dx, first, \
+                       r.count);
+                switch (tile_of(gp)) {
+                case kDeep: GRADS(true, Deep<F32>) break;
+                case kFineDeep: if constexpr (!F32) { GRADS(true, FineDeep) } break;
+                case kSmall:
+                    if (direct) { GRADS(true, Small<F32>) } else { GRADS(false, Small<F32>) }
+                    break;
+                default:
+                    if (direct) { GRADS(true, Fine<F32>) } else { GRADS(false, Fine<F32>) }
+                    break;
+                }
+#undef GRADS
+            }
+            if ((st = launch_status()) != HYENA_OK) return st;
+        }
+        int64_t blocks = j.blocks[0] + j.blocks[1];
+        if (db) {
+            j.sums = (float *)(ws + sp.sums), j.rows = wave_rows(pl), j.N = (int)N, j.db = (char *)db + v0 * eb;
+            blocks += ceil_div(N, 64);
+        }
+        if (blocks == 0) continue;
+        if (blocks > 0x7fffffff) return HYENA_ERR_UNSUPPORTED;
+        hipLaunchKernelGGL(join_kernel<F32>, dim3((unsigned)blocks), dim3(256), 0, stream, j);
+        if ((st = launch_status()) != HYENA_OK) return st;
+    }
+    return HYENA_OK;
+}
+
+int check_xent(int64_t M, int64_t K, int64_t V, int dtype) {
+    if (dtype != HYENA_DTYPE_BF16 && dtype != HYENA_DTYPE_F32) return HYENA_ERR_DTYPE;
+    int64_t n;
+    if (!mul_fits(M, V, 64, &n) || !mul_fits(M, K, 64, &n) || !mul_fits(V, K, 64, &n)) return HYENA_ERR_SHAPE;
+    const int64_t most = ((int64_t)1 << 31) - 1024;  // tile coordinates are 32 bits
+    if (M > most || V > most) return HYENA_ERR_SHAPE;
+    if (K >= (int64_t)1 << 20) return HYENA_ERR_UNSUPPORTED;  // byte offsets inside a tile are 32 bits
+    return HYENA_OK;
+}
+
+}  // namespace
+}  // namespace layer
+
+using namespace layer;
+
+extern "C" {
+
+int hyena_xent_workspace(int64_t M, int64_t K, int64_t V, int dtype, int backward, int64_t *bytes_out) {
+    const int st = check_xent(M, K, V, dtype);
+    if (st != HYENA_OK) return st;
+    if (!bytes_out) return HYENA_ERR_NULL;
+    const bool f32 = dtype == HYENA_DTYPE_F32;
+    *bytes_out = V == 0 || (M == 0 && !backward) ? 0 : backward ? bwd_space(M, K, V, f32).total : fwd_space(M, K, V, f32).total;
+    return HYENA_OK;
+}
+
+int hyena_xent_fwd(const void *x, const void *w, const void *bias, const int64_t *target, int64_t M, int64_t K, int64_t V,
+                   int64_t ldx, float *loss, float *lse, void *workspace, int64_t workspace_bytes, int dtype, void *stream) {
+    const int st = check_xent(M, K, V, dtype);
+    if (st != HYENA_OK) return st;
+    const bool f32 = dtype == HYENA_DTYPE_F32;
+    const int64_t eb = f32 ? 4 : 2;
+    int64_t n, need = 0;
+    if (ldx < K || V < 1 || !mul_fits(M, ldx, eb, &n)) return HYENA_ERR_SHAPE;
+    if (M == 0) return HYENA_OK;
+    if (!target || !loss || !lse || (K > 0 && (!x || !w))) return HYENA_ERR_NULL;
+    if (!aligned(x, eb) || !aligned(w, eb) || !aligned(bias, eb) || !aligned(target, 8) || !aligned(loss, 4) ||
+        !aligned(lse, 4) || !aligned(workspace, 16))
+        return HYENA_ERR_ALIGN;
+    hyena_xent_workspace(M, K, V, dtype, 0, &need);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return HYENA_ERR_WORKSPACE;
+    const Rows in[4] = {{x, M, K * eb, ldx * eb}, {w, V, K * eb, K * eb}, {bias, 1, V * eb, V * eb}, {target, 1, M * 8, M * 8}};
+    const Rows out[3] = {{loss, 1, M * 4, M * 4}, {lse, 1, M * 4, M * 4}, {workspace, 1, need, need}};
+    for (int i = 0; i < 3; ++i) {
+        for (const Rows &r : in)
+            if (overlap(out[i], r)) return HYENA_ERR_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i], out[j])) return HYENA_ERR_ALIAS;
+    }
+    return (f32 ? xent_fwd<true> : xent_fwd<false>)(x, w, bias, target, M, K, V, ldx, loss, lse, (char *)workspace,
+                                                    (hipStream_t)stream);
+}
+
+int hyena_xent_bwd(const void *x, const void *w, const void *bias, const int64_t *target, const float *lse,
+                   const float *dloss, int64_t M, int64_t K, int64_t V, int64_t ldx, int64_t lddx, void *dx, void *dw,
+                   void *db, void *workspace, int64_t workspace_bytes, int dtype, void *stream) {
+    const int st = check_xent(M, K, V, dtype);
+    if (st != HYENA_OK) return st;
+    const bool f32 = dtype == HYENA_DTYPE_F32;
+    const int64_t eb = f32 ? 4 : 2;
+    int64_t n, need = 0;
+    if (ldx < K || V < 1 || !mul_fits(M, ldx, eb, &n) || (dx && (lddx < K || !mul_fits(M, lddx, eb, &n)))) return HYENA_ERR_SHAPE;
+    if (!dx && !dw && !db) return M > 0 && K > 0 ? HYENA_ERR_NULL : HYENA_OK;
+    if (M > 0 && (!target || !lse || !dloss || (K > 0 && (!x || !w)))) return HYENA_ERR_NULL;
+    if (!aligned(x, eb) || !aligned(w, eb) || !aligned(bias, eb) || !aligned(target, 8) || !aligned(lse, 4) ||
+        !aligned(dloss, 4) || !aligned(dx, eb) || !aligned(dw, eb) || !aligned(db, eb) || !aligned(workspace, 16))
+        return HYENA_ERR_ALIGN;
+    hyena_xent_workspace(M, K, V, dtype, 1, &need);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return HYENA_ERR_WORKSPACE;
+    const Rows in[6] = {{x, M, K * eb, ldx * eb},  {w, V, K * eb, K * eb},  {bias, 1, V * eb, V * eb},
+                        {target, 1, M * 8, M * 8}, {lse, 1, M * 4, M * 4}, {dloss, 1, M * 4, M * 4}};
+    const Rows out[4] = {{dx, M, K * eb, lddx * eb}, {dw, V, K * eb, K * eb}, {db, 1, V * eb, V * eb},
+                         {need > 0 ? workspace : nullptr, 1, need, need}};
+    for (int i = 0; i < 4; ++i) {
+        for (const Rows &r : in)
+            if (overlap(out[i], r)) return HYENA_ERR_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i], out[j])) return HYENA_ERR_ALIAS;
+    }
+    if (M == 0 || K == 0) dx = nullptr;
+    if (K == 0) dw = nullptr;
+    if (!dx && !dw && !db) return HYENA_OK;
+    return (f32 ? xent_bwd<true> : xent_bwd<false>)(x, w, bias, target, lse, dloss, M, K, V, ldx, lddx, dx, dw, db,
+                                                    (char *)workspace, (hipStream_t)stream);
+}
+
+}  // extern "C"
