@@ -72,9 +72,12 @@ __device__ inline Factors factors_of(const AdamParams &p) {
     return f;
 }
 
-// The new m and v and the value that they move, V elements at a time.
+// The new m and v and the value that they move, V elements at a time.  Products and
+// sums are rounded one by one: codes of 8 bits then depend on the written formula
+// alone, not on what a compiler fuses.
 template <int V>
 __device__ __forceinline__ void move(const Factors &f, const float (&g)[V], float (&m)[V], float (&v)[V], float (&w)[V]) {
+#pragma clang fp contract(off)
 #pragma unroll
     for (int k = 0; k < V; ++k) {
         const float d = g[k] * f.scale;
@@ -184,12 +187,11 @@ __device__ __forceinline__ Codes round_codes(const float (&x)[8], const uint32_t
     for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(x[k]));
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
-    scale = top < 0x1p-117f ? 0.0f : top / 448.0f;
-    const float inverse = scale > 0.0f ? 1.0f / scale : 0.0f;
+    scale = top < 0x1p-117f ? 0.0f : top * (1.0f / 448.0f);
     float q[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-        float t = fabsf(x[k]) * inverse;
+        float t = scale != 0.0f ? fabsf(x[k]) / scale : 0.0f;
         if (t > 448.0f) t = 448.0f;  // (NaN stays)
         int e = (int)(__float_as_uint(t) >> 23) - 127;
         if (e < -6) e = -6;
