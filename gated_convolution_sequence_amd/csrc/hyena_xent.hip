@@ -14,10 +14,14 @@
 //   * Forward: a tile keeps the maximum and the sum of exp(z - maximum) of its
 //     columns for each row, from the registers that hold the sums; merge_kernel
 //     joins the tiles.
-//   * Backward, a piece of the vocabulary at a time: the logits again with dz as
-//     their epilogue (in bf16 dz is rounded, as the matrix cores take it; db sums it
-//     unrounded), then dw = dz^T x of the piece and dx += dz w in fp32, rounded
-//     after the last piece.
+//   * Backward, a piece of the vocabulary at a time: the logits again, with e = p -
+//     [target] as their epilogue (in bf16 rounded, as the matrix cores take it; db sums
+//     dloss e unrounded), then dw = c e^T (dloss / c x) of the piece and dx += e w in
+//     fp32, times dloss and rounded after the last piece; c is the largest |dloss|.
+//     dloss stays out of e, so that the -1 of a target, the largest part of a gradient
+//     where p is small, is exact; inside, its rounding would be that of whole rows, and
+//     with a mean's equal dloss one factor (to 0.4 % off) for all gradients.  Equal
+//     dloss leave x as it is, others round it once more.
 //   * No more than 16 rows forward: the weights stream once through rows_product.
 
 #include "hyena_model.h"
@@ -222,11 +226,14 @@ struct RankParams {
     float *lse_out, *dloss_out;   // packed
     float *loss, *lse;            // forward: zeroed where there is no target
     int *rank, *index, *goal, *count;
+    float *most;                  // backward: the largest |dloss| of them
     int64_t V;
     int M;
 };
 __global__ __launch_bounds__(1024) void rank_kernel(RankParams p) {
     __shared__ int waves[8][16];
+    __shared__ float tops[16];
+    float top = 0.0f;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     int base = 0;
     for (int64_t first = 0; first < p.M; first += 8192) {
@@ -258,7 +265,11 @@ __global__ __launch_bounds__(1024) void rank_kernel(RankParams p) {
             if (goal[k] >= 0) {
                 p.index[at] = (int)m;
                 p.goal[at] = goal[k];
-                if (p.lse_in) p.lse_out[at] = p.lse_in[m], p.dloss_out[at] = p.dloss[m];
+                if (p.lse_in) {
+                    const float d = p.dloss[m];
+                    p.lse_out[at] = p.lse_in[m], p.dloss_out[at] = d;
+                    top = fmaxf(top, fabsf(d));
+                }
             } else if (p.loss) {
                 p.loss[m] = 0.0f, p.lse[m] = 0.0f;
             }
@@ -267,6 +278,15 @@ __global__ __launch_bounds__(1024) void rank_kernel(RankParams p) {
         __syncthreads();
     }
     if (threadIdx.x == 0) *p.count = base;
+    if (!p.most) return;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
+    if (lane == 0) tops[wave] = top;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < 16; ++w) top = fmaxf(top, tops[w]);
+        *p.most = top;
+    }
 }
 
 // Rows of x with a target to rows of whole 16 bytes, zeros behind them; dx of the
@@ -274,6 +294,8 @@ __global__ __launch_bounds__(1024) void rank_kernel(RankParams p) {
 struct PackParams {
     const void *from[2];  // x, w (null: as it is)
     void *to[2];
+    void *scaled;         // backward: dloss / most x of the rows as well
+    const float *dloss, *most;
     int64_t rows[2], ld[2];
     const int *rank;
     void *dx;
@@ -300,6 +322,8 @@ template <bool F32> __global__ __launch_bounds__(256) void pack_kernel(PackParam
             }
             const T *from = (const T *)p.from[g] + row * p.ld[g];
             u32x4_t *to = (u32x4_t *)p.to[g] + at * p.chunks;
+            u32x4_t *scaled = g == 0 && p.scaled ? (u32x4_t *)p.scaled + at * p.chunks : nullptr;
+            const float by = scaled && *p.most != 0.0f ? p.dloss[row] / *p.most : 0.0f;
 #pragma unroll 4
             for (int c = lane; c < p.chunks; c += 64) {
                 const int left = p.K - c * CE;
@@ -313,6 +337,13 @@ template <bool F32> __global__ __launch_bounds__(256) void pack_kernel(PackParam
                     v = __builtin_bit_cast(u32x4_t, x);
                 }
                 to[c] = v;
+                if (scaled) {
+                    float y[CE];
+                    const auto r = Pack<F32, CE>::from(v);
+#pragma unroll
+                    for (int e = 0; e < CE; ++e) y[e] = by * r.get(e);
+                    scaled[c] = __builtin_bit_cast(u32x4_t, Pack<F32, CE>::of(y).w[0]);
+                }
             }
         }
     }
@@ -320,13 +351,14 @@ template <bool F32> __global__ __launch_bounds__(256) void pack_kernel(PackParam
 
 // ---- gradients ------------------------------------------------------------------------
 
-// The logits' epilogue in the backward: dz of a piece, and its column sums.
+// The logits' epilogue in the backward: e = p - [target] of a piece, and the column
+// sums of dloss e.
 struct DzEpi {
     static constexpr bool kSums = false;
     const void *bias;           // of the piece
     const float *lse, *dloss;   // packed
     const int *target;          // packed, of the whole vocabulary
-    void *dz;                   // [rows][ld], ld whole 16 bytes, zeros behind the columns
+    void *dz;                   // e: [rows][ld], ld whole 16 bytes, zeros behind the columns
     float *sums;                // [row blocks][N] or null
     int64_t ld;
     int v0;                     // the piece's first entry
@@ -353,8 +385,8 @@ struct DzEpi {
 #pragma unroll
         for (int e = 0; e < V; ++e) {
             const float p = __expf(z[e] + c.bias.get(e) - r.lse);
-            z[e] = n + e < N ? r.dloss * (n + e == r.target ? p - 1.0f : p) : 0.0f;
-            c.sum[e] += z[e];
+            z[e] = n + e < N ? (n + e == r.target ? p - 1.0f : p) : 0.0f;
+            c.sum[e] += r.dloss * z[e];
         }
         Pack<F32, V>::store(dz, m * ld + n, (int)(ld - n), z);
     }
@@ -371,29 +403,31 @@ struct DzEpi {
     }
 };
 
-// The gradients' epilogue.  ACC: rows are put in place by `index`, and pieces of
-// the vocabulary are added up in fp32.
+// The gradients' epilogue.  ACC: pieces of the vocabulary are added up in fp32, and
+// rows are scaled and put in place by `index` at last.
 template <bool ACC> struct GradEpi {
     static constexpr bool kSums = false;
     void *y;
     const float *from;   // what the pieces before gave, or null
     float *to;           // where the sum goes, or null: y
     const int *index;
+    const float *scale;  // ACC: packed, one a row; else one for all
     int64_t ldy;
     int M, N;
 
     template <bool F32, int V> struct Row {
         Pack<true, V> sum;
         int64_t at;
+        float scale;
     };
     struct None {};
-    template <bool F32, int V> __device__ __forceinline__ None columns(int) const { return None{}; }
+    template <bool F32, int V> __device__ __forceinline__ float columns(int) const { return ACC ? 0.0f : *scale; }
     template <bool F32, int V> __device__ __forceinline__ auto before(int64_t m, int n) const {
         if constexpr (ACC) {
-            Row<F32, V> r = {Pack<true, V>::zero(), 0};
+            Row<F32, V> r = {Pack<true, V>::zero(), 0, 0.0f};
             if (m < M && n < N) {
                 if (from) r.sum = Pack<true, V>::load(from, m * N + n, N - n);
-                r.at = index[m];
+                if (!to) r.at = index[m], r.scale = scale[m];
             }
             return r;
         } else {
@@ -401,18 +435,22 @@ template <bool ACC> struct GradEpi {
         }
     }
     template <bool F32, int V, class R>
-    __device__ __forceinline__ void finish(int64_t m, int n, float (&z)[V], const None &, const R &r) const {
+    __device__ __forceinline__ void finish(int64_t m, int n, float (&z)[V], float by, const R &r) const {
         if (m >= M || n >= N) return;
         if constexpr (ACC) {
 #pragma unroll
             for (int e = 0; e < V; ++e) z[e] += r.sum.get(e);
-            if (to) Pack<true, V>::store(to, m * N + n, N - n, z);
-            else Pack<F32, V>::store(y, r.at * ldy + n, N - n, z);
+            if (to) return Pack<true, V>::store(to, m * N + n, N - n, z);
+#pragma unroll
+            for (int e = 0; e < V; ++e) z[e] *= r.scale;
+            Pack<F32, V>::store(y, r.at * ldy + n, N - n, z);
         } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e) z[e] *= by;
             Pack<F32, V>::store(y, m * ldy + n, N - n, z);
         }
     }
-    template <bool F32, int V> __device__ __forceinline__ void close(const None &, int, int, int) const {}
+    template <bool F32, int V> __device__ __forceinline__ void close(float, int, int, int) const {}
 };
 using DwEpi = GradEpi<false>;
 using DxEpi = GradEpi<true>;
@@ -553,7 +591,7 @@ int64_t piece_of(int64_t M, int64_t V, int64_t eb) {
 }
 
 struct BwdSpace {
-    int64_t count, rank, index, goal, lse, dloss, x, w, dz, sums, acc, partial, total;
+    int64_t count, rank, index, goal, lse, dloss, x, scaled, w, dz, sums, acc, partial, total;
     int64_t piece;
 };
 BwdSpace bwd_space(int64_t M, int64_t K, int64_t V, bool f32) {
@@ -566,9 +604,9 @@ BwdSpace bwd_space(int64_t M, int64_t K, int64_t V, bool f32) {
         return at;
     };
     s.piece = piece_of(M, V, eb);
-    s.count = take(4), s.rank = take(M * 4), s.index = take(M * 4), s.goal = take(M * 4);
+    s.count = take(8), s.rank = take(M * 4), s.index = take(M * 4), s.goal = take(M * 4);
     s.lse = take(M * 4), s.dloss = take(M * 4);
-    s.x = take(M * whole(K, eb) * eb);
+    s.x = take(M * whole(K, eb) * eb), s.scaled = take(M * whole(K, eb) * eb);
     s.w = take(whole(K, eb) != K ? V * whole(K, eb) * eb : 0);
     s.dz = take(M * whole(s.piece, eb) * eb);
     int64_t sums = 0, partial = 0;
@@ -671,12 +709,13 @@ int xent_bwd(const void *x, const void *w, const void *bias, const int64_t *targ
     r.target = target, r.lse_in = lse, r.dloss = dloss, r.V = V, r.M = (int)M;
     r.lse_out = (float *)(ws + sp.lse), r.dloss_out = (float *)(ws + sp.dloss);
     r.rank = (int *)(ws + sp.rank), r.index = (int *)(ws + sp.index), r.goal = (int *)(ws + sp.goal);
-    r.count = (int *)(ws + sp.count);
+    r.count = (int *)(ws + sp.count), r.most = (float *)(ws + sp.count) + 1;
     hipLaunchKernelGGL(rank_kernel, dim3(1), dim3(1024), 0, stream, r);
     if ((st = launch_status()) != HYENA_OK) return st;
     const int64_t ld = whole(K, eb);
     PackParams k = {};
     k.from[0] = x, k.to[0] = ws + sp.x, k.rows[0] = M, k.ld[0] = ldx, k.rank = r.rank, k.dx = dx, k.lddx = lddx;
+    if (dw) k.scaled = ws + sp.scaled, k.dloss = dloss, k.most = r.most;
     if (ld != K) k.from[1] = w, k.to[1] = ws + sp.w, k.rows[1] = V, k.ld[1] = K;
     k.K = (int)K, k.chunks = (int)(ld * eb / 16);
     if ((st = launch_pack<F32>(k, stream)) != HYENA_OK) return st;
@@ -713,15 +752,15 @@ int xent_bwd(const void *x, const void *w, const void *bias, const int64_t *targ
             int g = 0;
             if (dw) {
                 DwEpi o = {};
-                o.y = (char *)dw + v0 * K * eb, o.ldy = K;
-                j.dw = gemm_params(gp, g, sz[g], e.dz, ldz, k.to[0], ld, o, at);
+                o.y = (char *)dw + v0 * K * eb, o.ldy = K, o.scale = r.most;
+                j.dw = gemm_params(gp, g, sz[g], e.dz, ldz, k.scaled, ld, o, at);
                 if (j.dw.partial) j.blocks[0] = ceil_div(N * ceil_div(K, 4), 256);
                 ++g;
             }
             if (dx) {
                 DxEpi o = {};
                 float *acc = (float *)(ws + sp.acc);
-                o.y = dx, o.ldy = lddx, o.index = r.index;
+                o.y = dx, o.ldy = lddx, o.index = r.index, o.scale = r.dloss_out;
                 o.from = v0 > 0 ? acc : nullptr, o.to = v0 + N < V ? acc : nullptr;
                 j.dx = gemm_params(gp, g, sz[g], e.dz, ldz, wv, ldw, o, at);
                 if (j.dx.partial) j.blocks[1] = ceil_div(M * ceil_div(K, 4), 256);

@@ -64,6 +64,10 @@ template <bool F32, int V> struct Pack {
         if constexpr (F32) return __uint_as_float(word(i));
         else return i & 1 ? bf_hi(word(i >> 1)) : bf_lo(word(i >> 1));
     }
+    __device__ static Pack from(u32x4_t v) {  // of 16 bytes
+        static_assert(WORDS == 4, "16 bytes");
+        return Pack{{__builtin_bit_cast(words, v)}};
+    }
     __device__ static Pack of(const float (&x)[V]) {
         Pack r;
 #pragma unroll

@@ -86,9 +86,9 @@ int hyena_xent_fwd(const void *x, const void *w, const void *bias,
  *     dz_iv = dloss_i (exp(z_iv - lse_i) - [v = target_i]),
  *     dx = dz w,  dw = dz^T x,  db = sum_i dz_i
  * dx [M, K] has row stride lddx; dw [V, K], db [V] contiguous; all in `dtype`.
- * Any output may be NULL, not all.  bf16: dz is rounded once to bf16 as the
- * operand of its two products; db sums the unrounded dz; sums are fp32, outputs
- * rounded once. */
+ * Any output may be NULL, not all.  bf16: softmax - [target] and, for dw, dloss x
+ * (over the largest |dloss|) are rounded once each to bf16, as operands of the products; db sums unrounded
+ * values; sums are fp32, outputs rounded once. */
 int hyena_xent_bwd(const void *x, const void *w, const void *bias,
                    const int64_t *target, const float *lse, const float *dloss,
                    int64_t M, int64_t K, int64_t V, int64_t ldx, int64_t lddx,

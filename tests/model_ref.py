@@ -111,8 +111,12 @@ def xent_fwd(x, w, target, bias):
 
 
 def xent_bwd(x, w, target, lse, dloss, bias, bf16):
-    """dx, dw, db as (ref, bound) from the saved lse.  bf16: dz is rounded as an operand, but not for db."""
+    """dx, dw, db as (ref, bound) from the saved lse.
+
+    bf16: p - [target] is rounded as an operand of dx = dloss ((p - [target]) w), and with dloss x as an operand of
+    dw; not for db."""
     V, K = w.shape
+    half = 2.0 ** -8 if bf16 else 0.0
     rows = torch.nonzero((target >= 0) & (target < V))[:, 0]
     dx = torch.zeros(x.shape, dtype=F64, device=x.device)
     edx = torch.zeros_like(dx)
@@ -125,15 +129,17 @@ def xent_bwd(x, w, target, lse, dloss, bias, bf16):
     dl = dloss.double()[rows][:, None]
     dz = p.clone()
     dz[torch.arange(len(rows), device=x.device), target[rows]] -= 1
-    e = dl.abs() * (ep + 2 * U * dz.abs())
-    dz = dz * dl
-    op = e + (dz.abs() * 2.0 ** -8 if bf16 else 0.0)
+    e = ep + 2 * U * dz.abs()
+    op = e + dz.abs() * half
     xa, wa, n = x[rows].double(), w.double(), len(rows)
-    dx[rows] = dz @ wa
-    edx[rows] = (V + 8) * U * (dz.abs() @ wa.abs()) + op @ wa.abs()
-    dw = dz.t().contiguous() @ xa
-    edw = (n + 8) * U * (dz.abs().t().contiguous() @ xa.abs()) + op.t().contiguous() @ xa.abs()
-    return (dx, edx), (dw, edw), (dz.sum(0), (n + 8) * U * dz.abs().sum(0) + e.sum(0))
+    dx[rows] = dl * (dz @ wa)
+    edx[rows] = dl.abs() * ((V + 10) * U * (dz.abs() @ wa.abs()) + op @ wa.abs())
+    xs = dl * xa
+    t = lambda a: a.t().contiguous()  # noqa: E731
+    dw = t(dz) @ xs
+    edw = t((n + 8) * U * dz.abs() + op + (half + 4 * U) * (dz.abs() + op)) @ xs.abs()
+    db = dl * dz
+    return (dx, edx), (dw, edw), (db.sum(0), (n + 8) * U * db.abs().sum(0) + (dl.abs() * e).sum(0))
 
 
 # ---- AdamW ------------------------------------------------------------------------------

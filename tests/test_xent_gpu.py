@@ -214,6 +214,26 @@ def test_offsets_past_32_bits():
     check(lse[pick], *want[1], "lse")
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_upstream_gradients(dtype):
+    """Of either sign, of very unlike sizes, 0, and alike: where p is small those leave one rounding, the output's."""
+    t = inputs(200, 64, 5000, dtype, 21, masked=0.1)
+    t["dloss"] = torch.randn(200, device=DEV) * torch.exp2(torch.randint(-30, 30, (200,), device=DEV).float())
+    check_all(**t, what="unlike")
+    t["dloss"].zero_()
+    _, _, dx, dw, db = check_all(**t, what="zero")
+    assert not dx.any() and not dw.any() and not db.any()
+    t["dloss"].fill_(1.0 / 173)
+    t["w"] *= 0.01  # p about 1 / 5000
+    t["bias"].zero_()
+    loss, lse, dx, dw, _ = check_all(**t, what="alike")
+    want = ref.xent_bwd(t["x"], t["w"], t["target"], lse, t["dloss"], t["bias"], False)
+    if dtype == BF16:  # rows of targets: rounded once, and p (a part in 5000, in both) once more
+        hit = torch.bincount(t["target"][(t["target"] >= 0) & (t["target"] < 5000)], minlength=5000) == 1
+        err = (dw.double() - want[1][0])[hit].norm() / want[1][0][hit].norm()
+        assert err < 2.0 ** -9 * 1.1, err
+
+
 @pytest.mark.parametrize("M", [8, 200])
 def test_the_same_bits_again(M):
     t = inputs(M, 520, 1000, BF16, 16)
