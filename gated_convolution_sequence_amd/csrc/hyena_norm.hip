@@ -4,7 +4,12 @@
 // Both directions are bound by memory: the forward reads and writes a row once,
 // the backward reads x and dy and writes dx.  A row is held in the registers of
 // T lanes (a wave, a workgroup of 4 waves or one of 16, by the row's length), 16 bytes
-// a lane and chunk, so that mean, deviations and output come from one read.
+// a lane and chunk, so that mean, deviations and output come from one read; the
+// workgroups walk the rows with the next one's loads in flight, past the caches.
+// 8192 x 4096 bf16: forward 24.3 us (134 MB, 5.5 TB/s; at 32768 rows 5.9), backward
+// 45 us (201 MB, 4.5 TB/s; of it 4 to 5 us the launch that adds the workgroups' sums
+// for dw and db; at 32768 rows 5.4).  Without the streaming accesses and the loads
+// ahead the forward took 28.5 us.
 
 #include "hyena_model.h"
 #include "layer_gemm.h"
@@ -58,37 +63,45 @@ template <int T, int N> __device__ inline void row_sums(float (&s)[N], float *ld
     }
 }
 
-// Chunk c of a lane of T: values (c T + lane) V .. of the row.
-template <bool F32, int T, int CH> struct RowOf {
+// Chunk c of a lane of T: values (c T + lane) V .. of the row.  WHOLE: the row is
+// T CH V values long, and no chunk needs a look at its end.
+template <bool F32, int T, int CH, bool WHOLE> struct RowOf {
     static constexpr int V = kVec<F32>;
     Pack<F32, V> r[CH];
-    __device__ void load(const void *p, int64_t at, int lane, int64_t D) {
+    // Values of chunk c that belong to the row.
+    __device__ static int count(int c, int lane, int D) {
+        return WHOLE ? V : max(min(D - (c * T + lane) * V, V), 0);
+    }
+    template <bool STREAM> __device__ void load(const void *p, int64_t at, int lane, int D) {
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            const int64_t d = (int64_t)(c * T + lane) * V;
-            r[c] = d < D ? Pack<F32, V>::load(p, at + d, (int)min(D - d, (int64_t)V)) : Pack<F32, V>::zero();
+            const int n = count(c, lane, D);
+            r[c] = n > 0 ? Pack<F32, V>::template load<STREAM>(p, at + (c * T + lane) * V, n) : Pack<F32, V>::zero();
         }
     }
 };
 
 // The forward.  T lanes a row, NT / T rows a workgroup at a time; workgroups walk
 // the rows and keep w and b in registers.
-template <bool F32, int T, int CH, int NT> __global__ __launch_bounds__(NT) void norm_fwd_kernel(NormParams p) {
+template <bool F32, int T, int CH, int NT, bool WHOLE> __global__ __launch_bounds__(NT) void norm_fwd_kernel(NormParams p) {
+    using R = RowOf<F32, T, CH, WHOLE>;
     constexpr int V = kVec<F32>, ROWS = NT / T;
     __shared__ float lds[T > 64 ? 2 * ROWS * (T / 64) : 1];
-    const int lane = threadIdx.x % T, sub = threadIdx.x / T;
+    const int lane = threadIdx.x % T, sub = threadIdx.x / T, D = (int)p.D;
     float *area = lds + sub * 2 * (T / 64);
-    RowOf<F32, T, CH> w, b;
-    if (p.w) w.load(p.w, 0, lane, p.D);
-    if (p.b) b.load(p.b, 0, lane, p.D);
-    const float inv = 1.0f / (float)p.D;
+    R w, b;
+    if (p.w) w.template load<false>(p.w, 0, lane, D);
+    if (p.b) b.template load<false>(p.b, 0, lane, D);
+    const float inv = 1.0f / (float)D;
     int turn = 0;
-    // T > 64: every wave of the workgroup takes part in each barrier
-    for (int64_t first = (int64_t)blockIdx.x * ROWS; first < p.M; first += (int64_t)gridDim.x * ROWS) {
-        const int64_t m = first + sub;
-        const bool on = m < p.M;
-        RowOf<F32, T, CH> x;
-        x.load(p.x, on ? m * p.ldx : 0, lane, on ? p.D : 0);
+    const int64_t step = (int64_t)gridDim.x * ROWS;
+    int64_t m = (int64_t)blockIdx.x * ROWS + sub;
+    R next;
+    if (m < p.M) next.template load<true>(p.x, m * p.ldx, lane, D);
+    // T > 64: one row a workgroup, so that every wave takes part in each barrier
+    for (; m < p.M; m += step) {
+        const R x = next;
+        if (m + step < p.M) next.template load<true>(p.x, (m + step) * p.ldx, lane, D);
         float s[1] = {0.0f}, mean = 0.0f;
         if (!p.rms) {
 #pragma unroll
@@ -101,24 +114,23 @@ template <bool F32, int T, int CH, int NT> __global__ __launch_bounds__(NT) void
         s[0] = 0.0f;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            const int64_t left = p.D - (int64_t)(c * T + lane) * V;
+            const int n = R::count(c, lane, D);
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                const float d = e < left ? x.r[c].get(e) - mean : 0.0f;
+                const float d = WHOLE || e < n ? x.r[c].get(e) - mean : 0.0f;
                 s[0] += d * d;
             }
         }
         row_sums<T>(s, area, turn++);
         const float rstd = 1.0f / sqrtf(s[0] * inv + p.eps);
-        if (!on) continue;
         if (lane == 0) {
             if (p.mean) p.mean[m] = mean;
             if (p.rstd) p.rstd[m] = rstd;
         }
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            const int64_t d = (int64_t)(c * T + lane) * V;
-            if (d >= p.D) continue;
+            const int n = R::count(c, lane, D);
+            if (n <= 0) continue;
             float y[V];
 #pragma unroll
             for (int e = 0; e < V; ++e) {
@@ -126,7 +138,7 @@ template <bool F32, int T, int CH, int NT> __global__ __launch_bounds__(NT) void
                 if (p.w) y[e] *= w.r[c].get(e);
                 if (p.b) y[e] += b.r[c].get(e);
             }
-            Pack<F32, V>::store(p.y, m * p.ldy + d, (int)min(p.D - d, (int64_t)V), y);
+            Pack<F32, V>::template store<true>(p.y, m * p.ldy + (c * T + lane) * V, n, y);
         }
     }
 }
@@ -185,55 +197,63 @@ template <bool F32> __global__ __launch_bounds__(kWide) void norm_fwd_wide_kerne
 
 // The backward.  As the forward, with the sums over rows that dw and db want kept
 // in registers, a lane's columns being the same in every row, and written once a
-// workgroup; sums_kernel adds the workgroups'.
-template <bool F32, int T, int CH, int NT> __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormParams p) {
+// workgroup; column_sums_kernel adds the workgroups'.  A row's loads go out before the
+// row before it is finished.
+template <bool F32, int T, int CH, int NT, bool WHOLE> __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormParams p) {
+    using R = RowOf<F32, T, CH, WHOLE>;
     constexpr int V = kVec<F32>, ROWS = NT / T;
     __shared__ float lds[T > 64 ? 4 * ROWS * (T / 64) : 1];
     __shared__ float joint[ROWS > 1 ? T * V : 1];
-    const int lane = threadIdx.x % T, sub = threadIdx.x / T;
+    const int lane = threadIdx.x % T, sub = threadIdx.x / T, D = (int)p.D;
     float *area = lds + sub * 4 * (T / 64);
-    RowOf<F32, T, CH> w;
-    if (p.w) w.load(p.w, 0, lane, p.D);
+    R w;
+    if (p.w) w.template load<false>(p.w, 0, lane, D);
     float dw[CH][V] = {}, db[CH][V] = {};
-    const float inv = 1.0f / (float)p.D;
+    const float inv = 1.0f / (float)D;
     int turn = 0;
-    for (int64_t first = (int64_t)blockIdx.x * ROWS; first < p.M; first += (int64_t)gridDim.x * ROWS) {
-        const int64_t m = first + sub;
-        const bool on = m < p.M;
-        RowOf<F32, T, CH> x, dy;
-        x.load(p.x, on ? m * p.ldx : 0, lane, on ? p.D : 0);
-        dy.load(p.dy, on ? m * p.lddy : 0, lane, on ? p.D : 0);
-        const float mean = on && !p.rms ? p.mean_in[m] : 0.0f, rstd = on ? p.rstd_in[m] : 0.0f;
+    const int64_t step = (int64_t)gridDim.x * ROWS;
+    int64_t m = (int64_t)blockIdx.x * ROWS + sub;
+    R x, dy;
+    float mean = 0.0f, rstd = 0.0f;
+    auto fetch = [&](int64_t m) {
+        if (m >= p.M) return;
+        x.template load<true>(p.x, m * p.ldx, lane, D);
+        dy.template load<true>(p.dy, m * p.lddy, lane, D);
+        mean = p.rms ? 0.0f : p.mean_in[m];
+        rstd = p.rstd_in[m];
+    };
+    fetch(m);
+    // T > 64: one row a workgroup, so that every wave takes part in each barrier
+    for (; m < p.M; m += step) {
         float s[2] = {0.0f, 0.0f};
+        float u[CH][V], g[CH][V];
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            const int64_t left = on ? p.D - (int64_t)(c * T + lane) * V : 0;
+            const int n = R::count(c, lane, D);
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                const float u = e < left ? (x.r[c].get(e) - mean) * rstd : 0.0f, d = dy.r[c].get(e);
-                const float g = p.w ? d * w.r[c].get(e) : d;
-                s[0] += g;
-                s[1] += g * u;
-                dw[c][e] += d * u;
+                u[c][e] = WHOLE || e < n ? (x.r[c].get(e) - mean) * rstd : 0.0f;
+                const float d = dy.r[c].get(e);
+                g[c][e] = p.w ? d * w.r[c].get(e) : d;
+                s[0] += g[c][e];
+                s[1] += g[c][e] * u[c][e];
+                dw[c][e] += d * u[c][e];
                 db[c][e] += d;
             }
         }
+        const float r = rstd;
+        fetch(m + step);
         if (!p.y) continue;
         row_sums<T>(s, area, turn++);
-        if (!on) continue;
         const float c0 = p.rms ? 0.0f : s[0] * inv, c1 = s[1] * inv;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            const int64_t d = (int64_t)(c * T + lane) * V;
-            if (d >= p.D) continue;
+            const int n = R::count(c, lane, D);
+            if (n <= 0) continue;
             float dx[V];
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float u = (x.r[c].get(e) - mean) * rstd, t = dy.r[c].get(e);
-                const float g = p.w ? t * w.r[c].get(e) : t;
-                dx[e] = rstd * (g - c0 - u * c1);
-            }
-            Pack<F32, V>::store(p.y, m * p.ldy + d, (int)min(p.D - d, (int64_t)V), dx);
+            for (int e = 0; e < V; ++e) dx[e] = r * (g[c][e] - c0 - u[c][e] * c1);
+            Pack<F32, V>::template store<true>(p.y, m * p.ldy + (c * T + lane) * V, n, dx);
         }
     }
     if (!p.sums) return;
@@ -258,8 +278,8 @@ template <bool F32, int T, int CH, int NT> __global__ __launch_bounds__(NT) void
                     for (int e = 0; e < V; ++e) mine[e] = joint[lane * V + e];
                 }
             }
-            const int64_t d = (int64_t)(c * T + lane) * V;
-            if (sub == 0 && d < p.D) Pack<true, V>::store(to, d, (int)min(p.D - d, (int64_t)V), mine);
+            const int n = R::count(c, lane, D);
+            if (sub == 0 && n > 0) Pack<true, V>::store(to, (c * T + lane) * V, n, mine);
         }
     }
 }
@@ -349,48 +369,58 @@ template <bool F32> __global__ __launch_bounds__(1024) void column_sums_kernel(C
 
 // ---- host --------------------------------------------------------------------------------
 
-// Lanes and chunks of a row of D values: a wave for short rows, a workgroup of 256 or
-// 1024 for longer ones; 0 chunks: longer than registers hold.
+// Lanes and chunks of a row of D values, and the workgroups that walk the rows; 0
+// chunks: longer than registers hold.  us, bf16 unless said:
+//   forward  8192 x 4096: 256 lanes x 2 chunks 24.3 with 768 workgroups, 24.6 with
+//            1024, 27.2 with 2048, and 38 with a wave a row (275 registers); 8192 x
+//            2048: a wave x 4 14.6, 256 lanes x 1 18.6; 8192 x 1024 fp32 13.7 against
+//            17.8; 8192 x 8192: 256 x 4 46, 1024 x 1 50; 8192 x 16384: 256 x 8 and
+//            1024 x 2 92 and 91
+//   backward 8192 x 4096: 256 x 2 45.0 with 256 workgroups, 45.6 with 512, 48.7 with
+//            768, 1000 x 4096: 14.6 with 256, 19.3 with 512 (each leaves a row of sums
+//            to be read again); 1024 x 1 48.3; 8192 x 2048: 256 x 1 26.7 with 512, 34.8
+//            with 256; 8192 x 1000: a wave x 2 18.3, 256 x 1 24.8; 8192 x 8192: 1024 x 1
+//            with 256 74.7, 256 x 4 75.8
 struct Form {
-    int lanes, chunks;
+    int lanes, chunks, blocks;
 };
-Form form_of(int64_t D, int64_t M, bool f32, bool backward) {
-    const int64_t v = f32 ? 4 : 8, n = ceil_div(D, v);
-    const int most = backward ? 2 : 8;
-    for (int lanes : {64, 256, 1024}) {
-        const int limit = lanes == 1024 ? (most < 4 ? most : 4) : lanes == 64 && M < 2048 ? 2 : most;
-        for (int ch = 1; ch <= limit; ch *= 2)
-            if (n <= (int64_t)lanes * ch) return Form{lanes, ch};
+Form form_of(int64_t D, bool f32, bool backward) {
+    static const Form fwd[] = {{64, 1, 1024}, {64, 2, 1024}, {64, 4, 1024}, {256, 2, 768}, {256, 4, 768}, {256, 8, 768}, {1024, 4, 512}};
+    static const Form bwd[] = {{64, 1, 256}, {64, 2, 256}, {256, 1, 512}, {256, 2, 256}, {1024, 1, 256}, {1024, 2, 256}};
+    const int64_t n = ceil_div(D, f32 ? 4 : 8);
+    if (backward) {
+        for (const Form &f : bwd)
+            if (n <= (int64_t)f.lanes * f.chunks) return f;
+        return Form{kWide, 0, 256};
     }
-    return Form{kWide, 0};
+    for (const Form &f : fwd)
+        if (n <= (int64_t)f.lanes * f.chunks) return f;
+    return Form{kWide, 0, 2048};
 }
-
-// Workgroups of the backward, each of which leaves a row of sums.
-int bwd_blocks(int64_t M, const Form &f) {
-    const int64_t rows = f.lanes == 64 ? 4 : 1, groups = ceil_div(M, rows);
-    return (int)(groups < 512 ? groups : 512);
+// Workgroups for M rows, four at a time where a row is a wave's.
+int blocks_of(const Form &f, int64_t M) {
+    const int64_t groups = ceil_div(M, f.lanes == 64 ? 4 : 1);
+    return (int)(groups < f.blocks ? groups : f.blocks);
 }
-int wide_blocks(int64_t M) { return (int)(M < 256 ? M : 256); }
 
 template <bool F32> int launch_fwd(const NormParams &p, hipStream_t stream) {
-    const Form f = form_of(p.D, p.M, F32, false);
-    const int64_t rows = f.lanes == 64 ? 4 : 1, groups = ceil_div(p.M, rows);
-    const dim3 grid((unsigned)(groups < 2048 ? groups : 2048));
-#define FWD(T, CH, NT)                                                                                   \
-    if (f.lanes == T && f.chunks == CH) {                                                                \
-        hipLaunchKernelGGL((norm_fwd_kernel<F32, T, CH, NT>), grid, dim3(NT), 0, stream, p);             \
-        return launch_status();                                                                          \
+    const Form f = form_of(p.D, F32, false);
+    const dim3 grid(blocks_of(f, p.M));
+    const bool whole = p.D == (int64_t)f.lanes * f.chunks * kVec<F32>;
+#define FWD(T, CH, NT)                                                                                                \
+    if (f.lanes == T && f.chunks == CH) {                                                                             \
+        hipLaunchKernelGGL((whole ? norm_fwd_kernel<F32, T, CH, NT, true> : norm_fwd_kernel<F32, T, CH, NT, false>),  \
+                           grid, dim3(NT), 0, stream, p);                                                             \
+        return launch_status();                                                                                       \
     }
-    FWD(64, 1, 256) FWD(64, 2, 256) FWD(64, 4, 256) FWD(64, 8, 256)
-    FWD(256, 1, 256) FWD(256, 2, 256) FWD(256, 4, 256) FWD(256, 8, 256)
-    FWD(1024, 1, 1024) FWD(1024, 2, 1024) FWD(1024, 4, 1024)
+    FWD(64, 1, 256) FWD(64, 2, 256) FWD(64, 4, 256) FWD(256, 2, 256) FWD(256, 4, 256) FWD(256, 8, 256) FWD(1024, 4, 1024)
 #undef FWD
     hipLaunchKernelGGL(norm_fwd_wide_kernel<F32>, grid, dim3(kWide), 0, stream, p);
     return launch_status();
 }
 
 template <bool F32> int launch_bwd(NormParams p, char *ws, hipStream_t stream) {
-    const Form f = form_of(p.D, p.M, F32, true);
+    const Form f = form_of(p.D, F32, true);
     const bool sums = p.want_dw || p.want_db;
     int blocks = 0, st = HYENA_OK;
     if (p.M > 0) {
@@ -402,16 +432,18 @@ template <bool F32> int launch_bwd(NormParams p, char *ws, hipStream_t stream) {
                 hipLaunchKernelGGL(norm_dots_kernel<F32>, dim3((unsigned)(p.M < 2048 ? p.M : 2048)), dim3(kWide), 0, stream, p);
                 if ((st = launch_status()) != HYENA_OK) return st;
             }
-            blocks = wide_blocks(p.M);
+            blocks = blocks_of(f, p.M);
             hipLaunchKernelGGL(norm_bwd_wide_kernel<F32>, dim3((unsigned)ceil_div(p.D, 256 * kVec<F32>), blocks), dim3(256), 0,
                                stream, p);
         } else {
             p.sums = sums ? (float *)ws : nullptr;
-            blocks = bwd_blocks(p.M, f);
+            blocks = blocks_of(f, p.M);
             const dim3 grid(blocks);
-#define BWD(T, CH, NT)                 \
-    if (f.lanes == T && f.chunks == CH) \
-        hipLaunchKernelGGL((norm_bwd_kernel<F32, T, CH, NT>), grid, dim3(NT), 0, stream, p);
+            const bool whole = p.D == (int64_t)f.lanes * f.chunks * kVec<F32>;
+#define BWD(T, CH, NT)                                                                                                \
+    if (f.lanes == T && f.chunks == CH)                                                                               \
+        hipLaunchKernelGGL((whole ? norm_bwd_kernel<F32, T, CH, NT, true> : norm_bwd_kernel<F32, T, CH, NT, false>),  \
+                           grid, dim3(NT), 0, stream, p);
             BWD(64, 1, 256) BWD(64, 2, 256) BWD(256, 1, 256) BWD(256, 2, 256) BWD(1024, 1, 1024) BWD(1024, 2, 1024)
 #undef BWD
         }
@@ -444,8 +476,8 @@ int hyena_norm_workspace(int64_t M, int64_t D, int dtype, int64_t *bytes_out) {
     const int st = check_norm(M, D, dtype);
     if (st != HYENA_OK) return st;
     if (!bytes_out) return HYENA_ERR_NULL;
-    const Form f = form_of(D, M, dtype == HYENA_DTYPE_F32, true);
-    const int64_t blocks = M == 0 ? 0 : f.chunks == 0 ? wide_blocks(M) : bwd_blocks(M, f);
+    const Form f = form_of(D, dtype == HYENA_DTYPE_F32, true);
+    const int64_t blocks = blocks_of(f, M);
     *bytes_out = D == 0 ? 0 : (f.chunks == 0 ? ceil_div(M * 8, 16) * 16 : 0) + ceil_div(blocks * D * 8, 16) * 16;
     return HYENA_OK;
 }

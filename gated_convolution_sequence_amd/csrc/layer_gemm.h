@@ -74,12 +74,16 @@ template <bool F32, int V> struct Pack {
         for (int i = 0; i < WORDS; ++i) r.w[i / 4][i % 4] = F32 ? __float_as_uint(x[i]) : pack_bf16(x[2 * i % V], x[(2 * i + 1) % V]);
         return r;
     }
-    __device__ static Pack load(const void *p, size_t e, int n) {
+    // STREAM: read (written) once, past the caches.
+    template <bool STREAM = false> __device__ static Pack load(const void *p, size_t e, int n) {
         using T = typename El<F32>::type;
         Pack r;
         if (n >= V) {
 #pragma unroll
-            for (int i = 0; i < PARTS; ++i) r.w[i] = *(const words_any *)((const T *)p + e + i * 4);
+            for (int i = 0; i < PARTS; ++i) {
+                const words_any *at = (const words_any *)((const T *)p + e + i * 4);
+                r.w[i] = STREAM ? __builtin_nontemporal_load(at) : *at;
+            }
             return r;
         }
         float x[V];
@@ -87,12 +91,16 @@ template <bool F32, int V> struct Pack {
         for (int i = 0; i < V; ++i) x[i] = i < n ? load1<F32>(p, e + i) : 0.0f;
         return of(x);
     }
-    __device__ static void store(void *p, size_t e, int n, const float (&x)[V]) {
+    template <bool STREAM = false> __device__ static void store(void *p, size_t e, int n, const float (&x)[V]) {
         using T = typename El<F32>::type;
         if (n >= V) {
             const Pack r = of(x);
 #pragma unroll
-            for (int i = 0; i < PARTS; ++i) *(words_any *)((T *)p + e + i * 4) = r.w[i];
+            for (int i = 0; i < PARTS; ++i) {
+                words_any *at = (words_any *)((T *)p + e + i * 4);
+                if (STREAM) __builtin_nontemporal_store((words_any)r.w[i], at);
+                else *at = r.w[i];
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < V; ++i)

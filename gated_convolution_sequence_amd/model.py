@@ -122,7 +122,8 @@ def norm_fwd(x: torch.Tensor, w: Optional[torch.Tensor] = None, b: Optional[torc
     dev, dt = x.device, x.dtype
     if x.dim() < 1:
         raise ValueError("x must be [..., D]")
-    D, M = x.shape[-1], _rows_of(x)
+    D = x.shape[-1]
+    M = x.numel() // D if D else _rows_of(x)
     ldx = ldy = D
     if not x.is_contiguous():
         ldx = _shared_stride((x,), ("x",), D)
@@ -159,7 +160,8 @@ def norm_bwd(x: torch.Tensor, w: Optional[torch.Tensor], dy: torch.Tensor, mean:
     dev, dt = x.device, x.dtype
     if x.dim() < 1:
         raise ValueError("x must be [..., D]")
-    D, M = x.shape[-1], _rows_of(x)
+    D = x.shape[-1]
+    M = x.numel() // D if D else _rows_of(x)
     ldx = lddy = lddx = D
     if not x.is_contiguous():
         ldx = _shared_stride((x,), ("x",), D)
