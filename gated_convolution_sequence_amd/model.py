@@ -11,8 +11,10 @@ grad_norm, adamw_step   the norm of all gradients and an AdamW step over a list 
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import functools
+import operator
 import os
 from typing import Optional, Sequence, Tuple, Union
 
@@ -312,19 +314,26 @@ class LinearXent(torch.autograd.Function):
 
 # ---- AdamW over many tensors ------------------------------------------------------------
 
+_shape, _dtype = operator.attrgetter("shape"), operator.attrgetter("dtype")
+
+
 class _Tensor(ctypes.Structure):
-    """hyena_tensor of hyena_model.h."""
+    """hyena_tensor of hyena_model.h: eight words of 64 bits."""
     _fields_ = [(n, ctypes.c_void_p) for n in ("param", "grad", "exp_avg", "exp_avg_sq", "exp_avg_scale",
                                                "exp_avg_sq_scale", "master")] + [("numel", ctypes.c_int64)]
 
 
-def _list(ts, name: str, like, dtype, dev) -> None:
-    """ts as long as ``like`` and alike in shapes, contiguous, ``dtype`` and on ``dev``."""
-    if len(ts) != len(like):
-        raise ValueError("%s has %d tensors, expected %d" % (name, len(ts), len(like)))
-    for t, p in zip(ts, like):
-        if t.dtype is not dtype or t.device != dev or t.shape != p.shape or not t.is_contiguous():
-            raise ValueError("every tensor of %s must be contiguous %s on %s, shaped as its like" % (name, dtype, dev))
+def _column(table: list, at: int, ts, name: str, shapes, dtype, dev) -> None:
+    """The addresses of ts into every eighth word of ``table`` from ``at`` on.
+
+    ts has a tensor for each of ``shapes``, contiguous, ``dtype`` and on ``dev``.
+    """
+    if len(ts) != len(shapes):
+        raise ValueError("%s has %d tensors, expected %d" % (name, len(ts), len(shapes)))
+    if (list(map(_shape, ts)) != shapes or not all(map(torch.Tensor.is_contiguous, ts))
+            or any(d is not dtype for d in map(_dtype, ts)) or set(map(torch.Tensor.get_device, ts)) != {dev.index}):
+        raise ValueError("every tensor of %s must be contiguous %s on %s, shaped as its like" % (name, dtype, dev))
+    table[at::8] = map(torch.Tensor.data_ptr, ts)
 
 
 def _scalar(t: Optional[torch.Tensor], name: str, dtype, dev) -> None:
@@ -350,30 +359,19 @@ def grad_norm(grads: Sequence[torch.Tensor], max_norm: Optional[float] = None,
         raise ValueError("grads is empty")
     code = _code(grads[0])
     dev = grads[0].device
-    _list(grads, "grads", grads, grads[0].dtype, dev)
-    table = (_Tensor * len(grads))()
-    numel = 0
-    for e, g in zip(table, grads):
-        e.grad, e.numel = g.data_ptr(), g.numel()
-        numel += e.numel
-    out = torch.empty(1 if max_norm is None else 2, dtype=torch.float32, device=dev)
-    ws = _workspace(grad_norm_workspace_bytes(len(grads), numel), workspace, dev)
-    _call("hyena_grad_norm", dev, ctypes.addressof(table), len(grads), 0.0 if max_norm is None else max_norm,
-          out.data_ptr(), None if max_norm is None else out.data_ptr() + 4, *_ws_args(ws), code)
-    return out[0], None if max_norm is None else out[1]
+    table = [0] * (8 * len(grads))
+    _column(table, 1, grads, "grads", [g.shape for g in grads], grads[0].dtype, dev)
+    table[7::8] = sizes = [g.numel() for g in grads]
+    words = array.array("q", table)
+    norm = torch.empty((), dtype=torch.float32, device=dev)
+    scale = None if max_norm is None else torch.empty((), dtype=torch.float32, device=dev)
+    ws = _workspace(grad_norm_workspace_bytes(len(grads), sum(sizes)), workspace, dev)
+    _call("hyena_grad_norm", dev, words.buffer_info()[0], len(grads), 0.0 if max_norm is None else max_norm,
+          norm.data_ptr(), _ptr(scale), *_ws_args(ws), code)
+    return norm, scale
 
 
 STATE_BLOCK = 256  # elements that share a scale where the moments have 8 bits
-
-
-def _scales(ts, name: str, like, dev) -> None:
-    if ts is None or len(ts) != len(like):
-        raise ValueError("%s must be one fp32 tensor for each parameter" % name)
-    for t, p in zip(ts, like):
-        if (t.dtype is not torch.float32 or t.device != dev or t.numel() != -(-p.numel() // STATE_BLOCK)
-                or not t.is_contiguous()):
-            raise ValueError("every tensor of %s must be contiguous fp32 on %s, one for every %d elements"
-                             % (name, dev, STATE_BLOCK))
 
 
 @_on_stream
@@ -389,7 +387,7 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], ex
 
     params, grads: all bf16 or all fp32; masters (None, or the fp32 values of which params are the roundings, and
     which then take the step); exp_avgs, exp_avg_sqs: the moments m and v in fp32, or m and sqrt(v) in
-    float8_e4m3fn with exp_avg_scales and exp_avg_sq_scales, an fp32 tensor for each parameter with one scale for
+    float8_e4m3fn with exp_avg_scales and exp_avg_sq_scales, an fp32 vector for each parameter with one scale for
     every 256 elements (codes and scales of zeros to begin with; rounding is random, by ``seed``, which should
     differ from step to step).  All contiguous, shaped as params.  step counts from 1.  lr, step and seed may be
     one-element tensors on the device (fp32, int64, int64), which a captured step reads anew in each replay.
@@ -401,30 +399,27 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], ex
     code = _code(params[0])
     dev, dt = params[0].device, params[0].dtype
     bits = 8 if len(exp_avgs) and exp_avgs[0].dtype is torch.float8_e4m3fn else 32
-    held = torch.float32 if bits == 32 else torch.float8_e4m3fn
-    _list(params, "params", params, dt, dev)
-    _list(grads, "grads", params, dt, dev)
-    _list(exp_avgs, "exp_avgs", params, held, dev)
-    _list(exp_avg_sqs, "exp_avg_sqs", params, held, dev)
+    held, fp32 = (torch.float8_e4m3fn if bits == 8 else torch.float32), torch.float32
+    table = [0] * (8 * len(params))
+    shapes = [p.shape for p in params]
+    _column(table, 0, params, "params", shapes, dt, dev)
+    _column(table, 1, grads, "grads", shapes, dt, dev)
+    _column(table, 2, exp_avgs, "exp_avgs", shapes, held, dev)
+    _column(table, 3, exp_avg_sqs, "exp_avg_sqs", shapes, held, dev)
     if masters is not None:
-        _list(masters, "masters", params, torch.float32, dev)
+        _column(table, 6, masters, "masters", shapes, fp32, dev)
+    table[7::8] = sizes = [p.numel() for p in params]
     if bits == 8:
-        _scales(exp_avg_scales, "exp_avg_scales", params, dev)
-        _scales(exp_avg_sq_scales, "exp_avg_sq_scales", params, dev)
+        blocks = [(-(-n // STATE_BLOCK),) for n in sizes]
+        _column(table, 4, () if exp_avg_scales is None else exp_avg_scales, "exp_avg_scales", blocks, fp32, dev)
+        _column(table, 5, () if exp_avg_sq_scales is None else exp_avg_sq_scales, "exp_avg_sq_scales", blocks, fp32, dev)
     elif exp_avg_scales is not None or exp_avg_sq_scales is not None:
         raise ValueError("scales belong to moments in float8_e4m3fn")
     given = [t if isinstance(t, torch.Tensor) else None for t in (lr, step, seed)]
     for t, name, kind in zip((*given, grad_scale), ("lr", "step", "seed", "grad_scale"),
                              (torch.float32, torch.int64, torch.int64, torch.float32)):
         _scalar(t, name, kind, dev)
-    table = (_Tensor * len(params))()
-    for i, (e, p) in enumerate(zip(table, params)):
-        e.param, e.grad, e.numel = p.data_ptr(), grads[i].data_ptr(), p.numel()
-        e.exp_avg, e.exp_avg_sq = exp_avgs[i].data_ptr(), exp_avg_sqs[i].data_ptr()
-        if masters is not None:
-            e.master = masters[i].data_ptr()
-        if bits == 8:
-            e.exp_avg_scale, e.exp_avg_sq_scale = exp_avg_scales[i].data_ptr(), exp_avg_sq_scales[i].data_ptr()
+    words = array.array("q", table)
     number = [x if t is None else zero for x, t, zero in zip((lr, step, seed), given, (0.0, 1, 0))]
-    _call("hyena_adamw_step", dev, ctypes.addressof(table), len(params), number[0], betas[0], betas[1], eps,
+    _call("hyena_adamw_step", dev, words.buffer_info()[0], len(params), number[0], betas[0], betas[1], eps,
           weight_decay, number[1], number[2], *(_ptr(t) for t in given), _ptr(grad_scale), bits, code)
