@@ -50,7 +50,7 @@ struct StatsEpi {
     static constexpr bool kSums = true;
     const void *bias;
     const int *target;  // of each packed row
-    Part *part;         // [tiles of columns][row capacity]
+    Part *part;         // [tiles of columns][ldp rows]
     float *at;          // the target's logit of each row
     int64_t ldp;
     int M, N;
@@ -151,7 +151,7 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void stats_kernel(Gemm<StatsEpi> p
 struct RowStats {
     const void *bias;
     const int64_t *target;
-    Part *part;
+    Part *part;  // [rows][ldp groups of 16 columns]
     float *at;
     int64_t ldp;
     int M, N;
@@ -175,7 +175,7 @@ struct RowStats {
         for (int e = 0; e < V; ++e) r.s += __expf(z[e] - shift);
         r.s += __shfl_xor(r.s, 1);
         r.s += __shfl_xor(r.s, 2);
-        if ((threadIdx.x & 3) == 0 && m < M) part[(n / 16) * ldp + m] = r;
+        if ((threadIdx.x & 3) == 0 && m < M) part[m * ldp + n / 16] = r;
     }
     template <bool F32, int V> __device__ void close(const Pack<F32, V> &, int, int, int) const {}
 };
@@ -184,30 +184,34 @@ template <bool F32> __global__ __launch_bounds__(64 * kRowWaves) void rows_stats
     rows_product<F32, 1>(p, sums);
 }
 
-// Loss and lse of each row from its tiles: 32 rows a workgroup, eight lanes each.
+// Loss and lse of each row from its tiles, by SLICES lanes a row.
 struct MergeParams {
     const Part *part;
     const float *at;
     const int *index, *count;  // the packed rows' places and their number, or null:
     const int64_t *target;     // every row in place, those without a target among them
     float *loss, *lse;
-    int64_t ldp, V;
+    int64_t tile, row;         // parts from one tile, and from one row, to the next
+    int64_t V;
     int tiles, M;
 };
-__global__ __launch_bounds__(256) void merge_kernel(MergeParams p) {
-    __shared__ Part meet[8][32];
-    const int row = threadIdx.x & 31, slice = threadIdx.x >> 5;
-    const int m = blockIdx.x * 32 + row, rows = p.count ? *p.count : p.M;
+template <int SLICES> __global__ __launch_bounds__(256) void merge_kernel(MergeParams p) {
+    constexpr int ROWS = 256 / SLICES;
+    __shared__ Part meet[SLICES][ROWS];
+    const int row = threadIdx.x % ROWS, slice = threadIdx.x / ROWS;
+    const int m = blockIdx.x * ROWS + row, rows = p.count ? *p.count : p.M;
     Part r = {-__builtin_inff(), 0.0f};
     if (m < rows) {
 #pragma unroll 4
-        for (int t = slice; t < p.tiles; t += 8) join(r, p.part[t * p.ldp + m]);
+        for (int t = slice; t < p.tiles; t += SLICES) join(r, p.part[t * p.tile + m * p.row]);
     }
     meet[slice][row] = r;
-    __syncthreads();
+    for (int n = SLICES / 2; n > 0; n /= 2) {
+        __syncthreads();
+        if (slice < n) join(meet[slice][row], meet[slice + n][row]);
+    }
     if (slice != 0 || m >= rows) return;
-#pragma unroll
-    for (int s = 1; s < 8; ++s) join(r, meet[s][row]);
+    r = meet[0][row];
     const int64_t to = p.index ? p.index[m] : m;
     const bool on = p.index || (uint64_t)p.target[m] < (uint64_t)p.V;
     const float lse = shift_of(r.m) + __logf(r.s);
@@ -231,50 +235,61 @@ struct RankParams {
     int M;
 };
 __global__ __launch_bounds__(1024) void rank_kernel(RankParams p) {
-    __shared__ int waves[8][16];
+    __shared__ int ahead[128];  // rows in the waves before, of the turn's 8 times 16
+    __shared__ int first_half, both;
     __shared__ float tops[16];
     float top = 0.0f;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     int base = 0;
     for (int64_t first = 0; first < p.M; first += 8192) {
         int goal[8], before[8];
+        float lse[8], d[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             const int64_t m = first + k * 1024 + threadIdx.x;
             const int64_t t = m < p.M ? p.target[m] : -1;
+            if (p.lse_in) lse[k] = m < p.M ? p.lse_in[m] : 0.0f, d[k] = m < p.M ? p.dloss[m] : 0.0f;
             goal[k] = (uint64_t)t < (uint64_t)p.V ? (int)t : -1;
-            const uint64_t on = __builtin_amdgcn_ballot_w64(goal[k] >= 0);
-            before[k] = __popcll(on & (((uint64_t)1 << lane) - 1));
-            if (lane == 0) waves[k][wave] = __popcll(on);
         }
-        __syncthreads();
-        int sum = base;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            int mine = sum;
+            const uint64_t on = __builtin_amdgcn_ballot_w64(goal[k] >= 0);
+            before[k] = __popcll(on & (((uint64_t)1 << lane) - 1));
+            if (lane == 0) ahead[k * 16 + wave] = __popcll(on);
+        }
+        __syncthreads();
+        if (wave < 2) {  // running sums of the 128 counts, 64 a wave
+            const int mine = ahead[threadIdx.x];
+            int sum = mine;
 #pragma unroll
-            for (int w = 0; w < 16; ++w) {
-                const int n = waves[k][w];
-                if (w < wave) mine += n;
-                sum += n;
+            for (int o = 1; o < 64; o <<= 1) {
+                const int other = __shfl_up(sum, o);
+                if (lane >= o) sum += other;
             }
+            ahead[threadIdx.x] = sum - mine;
+            if (threadIdx.x == 63) first_half = sum;
+            if (threadIdx.x == 127) both = sum;
+        }
+        __syncthreads();
+        const int half = first_half;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
             const int64_t m = first + k * 1024 + threadIdx.x;
             if (m >= p.M) continue;
-            const int at = mine + before[k];
+            const int at = base + (k >= 4 ? half : 0) + ahead[k * 16 + wave] + before[k];
             p.rank[m] = goal[k] >= 0 ? at : -1;
             if (goal[k] >= 0) {
                 p.index[at] = (int)m;
                 p.goal[at] = goal[k];
                 if (p.lse_in) {
-                    const float d = p.dloss[m];
-                    p.lse_out[at] = p.lse_in[m], p.dloss_out[at] = d;
-                    top = fmaxf(top, fabsf(d));
+                    p.lse_out[at] = lse[k], p.dloss_out[at] = d[k];
+                    top = fmaxf(top, fabsf(d[k]));
                 }
             } else if (p.loss) {
                 p.loss[m] = 0.0f, p.lse[m] = 0.0f;
             }
         }
-        base = sum;
+        base += half + both;
         __syncthreads();
     }
     if (threadIdx.x == 0) *p.count = base;
@@ -485,16 +500,26 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void grads_kernel(Gemm<DwEpi> dw, 
         run_tile<false, true, DIRECT, S>(dx, block, a0, a1, a2, a3, b0, b1, b2, b3);
     }
 }
-// One of them, in tiles of 256 x 256.
-template <typename S> __global__ __launch_bounds__(S::NT, S::WAVES) void large_dw_kernel(Gemm<DwEpi> p, const int *count) {
+// The same in tiles of 256 x 256, whichever walks more steps a tile first: what is left
+// of its last round is then filled by the other's shorter tiles.  (6144 rows, a piece of
+// 16384 entries, K = 4096: dx's 384 tiles alone take two rounds of 256 units, 971 us,
+// and dw's 1024 another 671.)
+template <typename S>
+__global__ __launch_bounds__(S::NT, S::WAVES) void large_grads_kernel(Gemm<DwEpi> dw, Gemm<DxEpi> dx, int lead, int dx_first,
+                                                                      const int *count) {
     TILE_BUFFERS(S)
-    sum_from<false>(p, count);
-    run_tile<true, true, true, S>(p, blockIdx.x, a0, a1, a2, a3, b0, b1, b2, b3);
-}
-template <typename S> __global__ __launch_bounds__(S::NT, S::WAVES) void large_dx_kernel(Gemm<DxEpi> p, const int *count) {
-    TILE_BUFFERS(S)
-    if (!rows_from<S>(p, count)) return;
-    run_tile<false, true, true, S>(p, blockIdx.x, a0, a1, a2, a3, b0, b1, b2, b3);
+    const bool in_lead = (int)blockIdx.x < lead;
+    const int block = in_lead ? blockIdx.x : blockIdx.x - lead;
+    if (in_lead != (dx_first != 0)) {
+        if (block >= dw.tiles_m * dw.tiles_n * dw.splits) return;
+        sum_from<false>(dw, count);
+        run_tile<true, true, true, S>(dw, block, a0, a1, a2, a3, b0, b1, b2, b3);
+    } else {
+        dx.M = dx.e.M = *count;
+        dx.tiles_m = (dx.M + S::BM - 1) / S::BM;
+        if (block >= dx.tiles_m * dx.tiles_n * dx.splits) return;
+        run_tile<false, true, true, S>(dx, block, a0, a1, a2, a3, b0, b1, b2, b3);
+    }
 }
 
 // What remains of a piece: the sums of splits, and db from the row blocks' sums.
@@ -655,15 +680,15 @@ int xent_fwd(const void *x, const void *w, const void *bias, const int64_t *targ
     const int64_t eb = F32 ? 4 : 2;
     const FwdSpace sp = fwd_space(M, K, V, F32);
     MergeParams mp = {};
-    mp.part = (Part *)(ws + sp.part), mp.at = (float *)(ws + sp.at), mp.ldp = M, mp.V = V, mp.M = (int)M;
+    mp.part = (Part *)(ws + sp.part), mp.at = (float *)(ws + sp.at), mp.V = V, mp.M = (int)M;
     mp.loss = loss, mp.lse = lse;
     int st;
     if (M <= kFewRows) {
         RowsParams<RowStats> p = {};
         p.x = x, p.w = w, p.ldx = ldx, p.M = (int)M, p.N = (int)V, p.K = (int)K;
         p.e.bias = bias, p.e.target = target, p.e.part = (Part *)(ws + sp.part), p.e.at = (float *)(ws + sp.at);
-        p.e.ldp = M, p.e.M = p.M, p.e.N = p.N;
-        mp.tiles = (int)ceil_div(V, 16), mp.target = target;
+        mp.tiles = (int)ceil_div(V, 16), mp.target = target, mp.tile = 1, mp.row = mp.tiles;
+        p.e.ldp = mp.tiles, p.e.M = p.M, p.e.N = p.N;
         hipLaunchKernelGGL(rows_stats_kernel<F32>, dim3((unsigned)mp.tiles), dim3(64 * kRowWaves), 0, stream, p);
         if ((st = launch_status()) != HYENA_OK) return st;
     } else {
@@ -692,9 +717,12 @@ int xent_fwd(const void *x, const void *w, const void *bias, const int64_t *targ
         FOR_TILE(pl, direct, STATS)
 #undef STATS
         if ((st = launch_status()) != HYENA_OK) return st;
-        mp.tiles = pl.tiles_n[0], mp.index = r.index, mp.count = r.count;
+        mp.tiles = pl.tiles_n[0], mp.index = r.index, mp.count = r.count, mp.tile = M, mp.row = 1;
     }
-    hipLaunchKernelGGL(merge_kernel, dim3((unsigned)ceil_div(M, 32)), dim3(256), 0, stream, mp);
+    // a workgroup a row for few rows, whose tiles are many: 59 us at 8 rows of 4096 tiles
+    // with eight lanes a row, 5 with 256
+    if (M <= 256) hipLaunchKernelGGL(merge_kernel<256>, dim3((unsigned)M), dim3(256), 0, stream, mp);
+    else hipLaunchKernelGGL(merge_kernel<8>, dim3((unsigned)ceil_div(M, 32)), dim3(256), 0, stream, mp);
     return launch_status();
 }
 
@@ -768,10 +796,12 @@ int xent_bwd(const void *x, const void *w, const void *bias, const int64_t *targ
             const int first = dw ? (int)gp.blocks[0] : 0;
             if (gp.large) {
                 if constexpr (!F32) {
-                    if (dw) hipLaunchKernelGGL((large_dw_kernel<Large>), dim3((unsigned)first), dim3(Large::NT), 0, stream, j.dw, r.count);
-                    if (dx)
-                        hipLaunchKernelGGL((large_dx_kernel<Large>), dim3((unsigned)(blocks - first)), dim3(Large::NT), 0,
-                                           stream, j.dx, r.count);
+                    // whole rounds of the eight XCDs for the first, so that place() holds for both
+                    const bool dx_first = N >= M;
+                    const int64_t n_dw = dw ? gp.blocks[0] : 0, n_dx = blocks - n_dw;
+                    const int64_t lead = ceil_div(dx_first ? n_dx : n_dw, 8) * 8;
+                    hipLaunchKernelGGL((large_grads_kernel<Large>), dim3((unsigned)(lead + (dx_first ? n_dw : n_dx))),
+                                       dim3(Large::NT), 0, stream, j.dw, j.dx, (int)lead, (int)dx_first, r.count);
                 }
             } else {
 #define GRADS(DIRECT, S)                                                                                                \
