@@ -4,13 +4,13 @@
 //
 // Bound by the matrix cores: one product (2 M K V) forward and three backward,
 // since the logits are formed again.  The products are layer_gemm.h's tiles.
-//   * Rows without a target are left out: rank_kernel numbers the others in
-//     order, pack_kernel copies their x to rows of whole 16 bytes, and every
-//     product after that reads the number of rows from memory.  So such rows cost
-//     no products, and what their x holds (NaN from padding) meets no zero in dw's
-//     sums.  The copy costs 2 % of a forward at K = 4096, V = 65536 and lets the
-//     products fetch odd sizes and strides straight into LDS (w is copied too where
-//     its rows are no whole 16 bytes).
+//   * Rows without a target are left out: rank_kernel numbers the others in order,
+//     and every product after that reads the number of rows from memory.  So such
+//     rows cost no products, and what their x holds (NaN from padding) meets no zero in
+//     dw's sums.  The logits fetch the rows from where they are; dw's sum runs over
+//     rows, so for it pack_kernel copies them together.  Where the rows are no whole 16
+//     bytes, or 2 GiB apart, they are copied for the logits as well, and w where its
+//     rows are no whole 16 bytes.
 //   * Forward: a tile keeps the maximum and the sum of exp(z - maximum) of its
 //     columns for each row, from the registers that hold the sums; merge_kernel
 //     joins the tiles.
@@ -140,11 +140,11 @@ template <class S, class E> __device__ inline bool rows_from(Gemm<E> &p, const i
     return (int)blockIdx.x < p.tiles_m * p.tiles_n * p.splits;
 }
 
-template <bool F32, bool DIRECT, typename S>
+template <bool F32, bool DIRECT, bool GATHER, typename S>
 __global__ __launch_bounds__(S::NT, S::WAVES) void stats_kernel(Gemm<StatsEpi> p, const int *count) {
     TILE_BUFFERS(S)
     if (!rows_from<S>(p, count)) return;
-    run_tile<false, false, DIRECT, S>(p, blockIdx.x, a0, a1, a2, a3, b0, b1, b2, b3);
+    run_tile<false, false, DIRECT, S, GATHER>(p, blockIdx.x, a0, a1, a2, a3, b0, b1, b2, b3);
 }
 
 // Few rows: 16 columns a workgroup; columns of four lanes a row.
@@ -308,7 +308,7 @@ __global__ __launch_bounds__(1024) void rank_kernel(RankParams p) {
 // others to zero; and w to such rows where its own are not.  A wave a row.
 struct PackParams {
     const void *from[2];  // x, w (null: as it is)
-    void *to[2];
+    void *to[2];          // null: only what follows is wanted
     void *scaled;         // backward: dloss / most x of the rows as well
     const float *dloss, *most;
     int64_t rows[2], ld[2];
@@ -336,7 +336,7 @@ template <bool F32> __global__ __launch_bounds__(256) void pack_kernel(PackParam
                 continue;
             }
             const T *from = (const T *)p.from[g] + row * p.ld[g];
-            u32x4_t *to = (u32x4_t *)p.to[g] + at * p.chunks;
+            u32x4_t *to = p.to[g] ? (u32x4_t *)p.to[g] + at * p.chunks : nullptr;
             u32x4_t *scaled = g == 0 && p.scaled ? (u32x4_t *)p.scaled + at * p.chunks : nullptr;
             const float by = scaled && *p.most != 0.0f ? p.dloss[row] / *p.most : 0.0f;
 #pragma unroll 4
@@ -351,7 +351,7 @@ template <bool F32> __global__ __launch_bounds__(256) void pack_kernel(PackParam
                     for (int e = 0; e < CE; ++e) x[e] = e < left ? from[c * CE + e] : (T)0.0f;
                     v = __builtin_bit_cast(u32x4_t, x);
                 }
-                to[c] = v;
+                if (to) to[c] = v;
                 if (scaled) {
                     float y[CE];
                     const auto r = Pack<F32, CE>::from(v);
@@ -470,11 +470,11 @@ template <bool ACC> struct GradEpi {
 using DwEpi = GradEpi<false>;
 using DxEpi = GradEpi<true>;
 
-template <bool F32, bool DIRECT, typename S>
+template <bool F32, bool DIRECT, bool GATHER, typename S>
 __global__ __launch_bounds__(S::NT, S::WAVES) void dz_kernel(Gemm<DzEpi> p, const int *count) {
     TILE_BUFFERS(S)
     if (!rows_from<S>(p, count)) return;
-    run_tile<false, false, DIRECT, S>(p, blockIdx.x, a0, a1, a2, a3, b0, b1, b2, b3);
+    run_tile<false, false, DIRECT, S, GATHER>(p, blockIdx.x, a0, a1, a2, a3, b0, b1, b2, b3);
 }
 
 // dw's sum runs over the rows: their number, cut anew between the splits.
@@ -574,7 +574,12 @@ Plan whole_plan(int64_t M, int64_t N, int64_t K, bool f32, bool direct) {
     return p;
 }
 
-int64_t round16(int64_t n) { return ceil_div(n, 16) * 16; }
+// What lies in the workspace begins on whole cache lines, wherever the workspace does:
+// operands whose 128-byte rows straddled two lines took 6 % longer (a forward of 8192 x
+// 4096 x 65536 3.63 against 3.36 ms).
+constexpr int64_t kLine = 256;
+int64_t lines(int64_t n) { return ceil_div(n, kLine) * kLine; }
+char *first_line(void *ws) { return (char *)(((uintptr_t)ws + kLine - 1) & ~(uintptr_t)(kLine - 1)); }
 
 constexpr int64_t kFewRows = 16;  // rows_product's
 
@@ -588,7 +593,7 @@ FwdSpace fwd_space(int64_t M, int64_t K, int64_t V, bool f32) {
     int64_t n = 0;
     auto take = [&](int64_t bytes) {
         const int64_t at = n;
-        n += round16(bytes);
+        n += lines(bytes);
         return at;
     };
     if (M <= kFewRows) {
@@ -601,7 +606,7 @@ FwdSpace fwd_space(int64_t M, int64_t K, int64_t V, bool f32) {
         s.x = take(M * whole(K, eb) * eb);
         s.w = take(whole(K, eb) != K ? V * whole(K, eb) * eb : 0);
     }
-    s.total = n;
+    s.total = n + kLine - 16;  // to the first whole line
     return s;
 }
 
@@ -625,7 +630,7 @@ BwdSpace bwd_space(int64_t M, int64_t K, int64_t V, bool f32) {
     int64_t n = 0;
     auto take = [&](int64_t bytes) {
         const int64_t at = n;
-        n += round16(bytes);
+        n += lines(bytes);
         return at;
     };
     s.piece = piece_of(M, V, eb);
@@ -647,7 +652,7 @@ BwdSpace bwd_space(int64_t M, int64_t K, int64_t V, bool f32) {
         if (v0 == 0 && V > s.piece) v0 = (ceil_div(V, s.piece) - 2) * s.piece;
     }
     s.sums = take(sums), s.acc = take(V > s.piece ? M * K * 4 : 0), s.partial = take(partial);
-    s.total = n;
+    s.total = n + kLine - 16;  // to the first whole line
     return s;
 }
 
@@ -660,19 +665,27 @@ template <bool F32> int launch_pack(const PackParams &p, hipStream_t stream) {
     return launch_status();
 }
 
-// LAUNCH(DIRECT, S) for the plan's tiles.
-#define FOR_TILE(plan, direct, LAUNCH)                                       \
-    switch (tile_of(plan)) {                                                 \
-    case kLarge: if constexpr (!F32) { LAUNCH(true, Large) } break;          \
-    case kDeep: LAUNCH(true, Deep<F32>) break;                               \
-    case kFineDeep: if constexpr (!F32) { LAUNCH(true, FineDeep) } break;    \
-    case kSmall:                                                             \
-        if (direct) { LAUNCH(true, Small<F32>) } else { LAUNCH(false, Small<F32>) } \
-        break;                                                               \
-    case kFine:                                                              \
-        if (direct) { LAUNCH(true, Fine<F32>) } else { LAUNCH(false, Fine<F32>) } \
-        break;                                                               \
+// LAUNCH(DIRECT, GATHER, S) for the plan's tiles.
+#define FOR_TILE(plan, direct, gather, LAUNCH)                                        \
+    switch (tile_of(plan)) {                                                          \
+    case kLarge: if constexpr (!F32) { BOTH(gather, LAUNCH, Large) } break;           \
+    case kDeep: BOTH(gather, LAUNCH, Deep<F32>) break;                                \
+    case kFineDeep: if constexpr (!F32) { BOTH(gather, LAUNCH, FineDeep) } break;     \
+    case kSmall:                                                                      \
+        if (direct) { BOTH(gather, LAUNCH, Small<F32>) } else { LAUNCH(false, false, Small<F32>) } \
+        break;                                                                        \
+    case kFine:                                                                       \
+        if (direct) { BOTH(gather, LAUNCH, Fine<F32>) } else { LAUNCH(false, false, Fine<F32>) } \
+        break;                                                                        \
     }
+#define BOTH(gather, LAUNCH, S)                                      \
+    if (gather) { LAUNCH(true, true, S) } else { LAUNCH(true, false, S) }
+
+// Whether the logits can fetch the rows of x from where they are: whole aligned 16
+// bytes, all within 32-bit offsets, w as well (rows are gathered straight into LDS).
+bool gather_ok(const void *x, int64_t M, int64_t ldx, int64_t K, int64_t eb, const void *w) {
+    return direct_ok(x, ldx, K, eb) && direct_ok(w, K, K, eb) && M * ldx * eb < (int64_t)1 << 31;
+}
 
 template <bool F32>
 int xent_fwd(const void *x, const void *w, const void *bias, const int64_t *target, int64_t M, int64_t K, int64_t V,
@@ -699,22 +712,27 @@ int xent_fwd(const void *x, const void *w, const void *bias, const int64_t *targ
         hipLaunchKernelGGL(rank_kernel, dim3(1), dim3(1024), 0, stream, r);
         if ((st = launch_status()) != HYENA_OK) return st;
         const int64_t ld = whole(K, eb);
+        const bool gather = gather_ok(x, M, ldx, K, eb, w);
         PackParams k = {};
-        k.from[0] = x, k.to[0] = ws + sp.x, k.rows[0] = M, k.ld[0] = ldx, k.rank = r.rank;
-        if (ld != K) k.from[1] = w, k.to[1] = ws + sp.w, k.rows[1] = V, k.ld[1] = K;
-        k.K = (int)K, k.chunks = (int)(ld * eb / 16);
-        if ((st = launch_pack<F32>(k, stream)) != HYENA_OK) return st;
-        const bool direct = k.from[1] || direct_ok(w, K, K, eb);
+        if (!gather) {
+            k.from[0] = x, k.to[0] = ws + sp.x, k.rows[0] = M, k.ld[0] = ldx, k.rank = r.rank;
+            if (ld != K) k.from[1] = w, k.to[1] = ws + sp.w, k.rows[1] = V, k.ld[1] = K;
+            k.K = (int)K, k.chunks = (int)(ld * eb / 16);
+            if ((st = launch_pack<F32>(k, stream)) != HYENA_OK) return st;
+        }
+        const bool direct = gather || k.from[1] || direct_ok(w, K, K, eb);
         const Plan pl = whole_plan(M, V, K, F32, direct);
         if (pl.blocks[0] > 0x7fffffff) return HYENA_ERR_UNSUPPORTED;
         StatsEpi e = {};
         e.bias = bias, e.target = r.goal, e.part = (Part *)(ws + sp.part), e.at = (float *)(ws + sp.at), e.ldp = M;
         char *none = nullptr;
-        const Gemm<StatsEpi> p = gemm_params(pl, 0, Size{M, V, K}, k.to[0], ld, k.from[1] ? k.to[1] : w,
-                                             k.from[1] ? ld : K, e, none);
-#define STATS(DIRECT, S) \
-    hipLaunchKernelGGL((stats_kernel<F32, DIRECT, S>), dim3((unsigned)pl.blocks[0]), dim3(S::NT), 0, stream, p, r.count);
-        FOR_TILE(pl, direct, STATS)
+        Gemm<StatsEpi> p = gemm_params(pl, 0, Size{M, V, K}, gather ? x : k.to[0], gather ? ldx : ld,
+                                       k.from[1] ? k.to[1] : w, k.from[1] ? ld : K, e, none);
+        p.rows = r.index;
+#define STATS(DIRECT, GATHER, S)                                                                                       \
+    hipLaunchKernelGGL((stats_kernel<F32, DIRECT, GATHER, S>), dim3((unsigned)pl.blocks[0]), dim3(S::NT), 0, stream, p, \
+                       r.count);
+        FOR_TILE(pl, direct, gather, STATS)
 #undef STATS
         if ((st = launch_status()) != HYENA_OK) return st;
         mp.tiles = pl.tiles_n[0], mp.index = r.index, mp.count = r.count, mp.tile = M, mp.row = 1;
@@ -741,8 +759,9 @@ int xent_bwd(const void *x, const void *w, const void *bias, const int64_t *targ
     hipLaunchKernelGGL(rank_kernel, dim3(1), dim3(1024), 0, stream, r);
     if ((st = launch_status()) != HYENA_OK) return st;
     const int64_t ld = whole(K, eb);
+    const bool gather = gather_ok(x, M, ldx, K, eb, w);
     PackParams k = {};
-    k.from[0] = x, k.to[0] = ws + sp.x, k.rows[0] = M, k.ld[0] = ldx, k.rank = r.rank, k.dx = dx, k.lddx = lddx;
+    k.from[0] = x, k.to[0] = gather ? nullptr : ws + sp.x, k.rows[0] = M, k.ld[0] = ldx, k.rank = r.rank, k.dx = dx, k.lddx = lddx;
     if (dw) k.scaled = ws + sp.scaled, k.dloss = dloss, k.most = r.most;
     if (ld != K) k.from[1] = w, k.to[1] = ws + sp.w, k.rows[1] = V, k.ld[1] = K;
     k.K = (int)K, k.chunks = (int)(ld * eb / 16);
@@ -759,10 +778,12 @@ int xent_bwd(const void *x, const void *w, const void *bias, const int64_t *targ
         e.bias = bias ? (const char *)bias + v0 * eb : nullptr, e.lse = r.lse_out, e.dloss = r.dloss_out, e.target = r.goal;
         e.dz = ws + sp.dz, e.ld = ldz, e.sums = db ? (float *)(ws + sp.sums) : nullptr, e.v0 = (int)v0;
         char *none = nullptr;
-        const Gemm<DzEpi> p = gemm_params(pl, 0, Size{M, N, K}, k.to[0], ld, wv, ldw, e, none);
-#define DZ(DIRECT, S) \
-    hipLaunchKernelGGL((dz_kernel<F32, DIRECT, S>), dim3((unsigned)pl.blocks[0]), dim3(S::NT), 0, stream, p, r.count);
-        if (M > 0) FOR_TILE(pl, direct, DZ)
+        Gemm<DzEpi> p = gemm_params(pl, 0, Size{M, N, K}, gather ? x : k.to[0], gather ? ldx : ld, wv, ldw, e, none);
+        p.rows = r.index;
+#define DZ(DIRECT, GATHER, S)                                                                                       \
+    hipLaunchKernelGGL((dz_kernel<F32, DIRECT, GATHER, S>), dim3((unsigned)pl.blocks[0]), dim3(S::NT), 0, stream, p, \
+                       r.count);
+        if (M > 0) FOR_TILE(pl, direct, gather, DZ)
 #undef DZ
         if ((st = launch_status()) != HYENA_OK) return st;
 
@@ -883,8 +904,8 @@ int hyena_xent_fwd(const void *x, const void *w, const void *bias, const int64_t
         for (int j = 0; j < i; ++j)
             if (overlap(out[i], out[j])) return HYENA_ERR_ALIAS;
     }
-    return (f32 ? xent_fwd<true> : xent_fwd<false>)(x, w, bias, target, M, K, V, ldx, loss, lse, (char *)workspace,
-                                                    (hipStream_t)stream);
+    return (f32 ? xent_fwd<true> : xent_fwd<false>)(x, w, bias, target, M, K, V, ldx, loss, lse,
+                                                    first_line(workspace), (hipStream_t)stream);
 }
 
 int hyena_xent_bwd(const void *x, const void *w, const void *bias, const int64_t *target, const float *lse,
@@ -917,7 +938,7 @@ int hyena_xent_bwd(const void *x, const void *w, const void *bias, const int64_t
     if (K == 0) dw = nullptr;
     if (!dx && !dw && !db) return HYENA_OK;
     return (f32 ? xent_bwd<true> : xent_bwd<false>)(x, w, bias, target, lse, dloss, M, K, V, ldx, lddx, dx, dw, db,
-                                                    (char *)workspace, (hipStream_t)stream);
+                                                    first_line(workspace), (hipStream_t)stream);
 }
 
 }  // extern "C"

@@ -119,6 +119,7 @@ template <bool F32, int V> struct Pack {
 // or, where E::kSums, e.sums<S>(...) on the sums as the matrix cores leave them.
 template <class E> struct Gemm {
     const void *a, *b;
+    const int *rows;          // GATHER: the memory row of each row of a (all within 2^31 bytes)
     int64_t lda, ldb;         // elements between memory rows of a and b
     int M, N, C;
     int tiles_m, tiles_n;
@@ -127,8 +128,9 @@ template <class E> struct Gemm {
     E e;
 };
 
-// One operand's LDS tile of X values of m (or n) by one step of c.
-template <bool F32, bool TALL, int X, int NT> struct Operand {
+// One operand's LDS tile of X values of m (or n) by one step of c.  GATHER (flat): its
+// rows lie in memory where a list of row numbers says.
+template <bool F32, bool TALL, int X, int NT, bool GATHER = false> struct Operand {
     static constexpr int CE = El<F32>::CE;
     static constexpr int BK = 8 * CE;
     static constexpr int BYTES = X * 128;
@@ -160,22 +162,24 @@ template <bool F32, bool TALL, int X, int NT> struct Operand {
     // descriptor's range, a tall tile's columns by an offset past every range.
     static constexpr uint32_t kOutside = 0x80000000u;
     static constexpr int STEP = NT / ROW_CHUNKS;
-    static constexpr int PHASES = STEP >= 16 ? 1 : 16 / STEP;
+    static constexpr int PHASES = GATHER ? LOADS : STEP >= 16 ? 1 : 16 / STEP;
+    static_assert(!GATHER || !TALL, "rows of a flat operand");
     static_assert(NT % ROW_CHUNKS == 0 && (STEP % 16 == 0 || 16 % STEP == 0) && LOADS % PHASES == 0, "phases of the XOR");
     struct Lane {
         uint32_t off[PHASES], step, range;
     };
-    __device__ static Lane plan(int64_t ld, int x_left) {
+    __device__ static Lane plan(int64_t ld, int x_left, const int *rows) {
         const uint32_t pitch = (uint32_t)ld * sizeof(typename El<F32>::type);  // below 2^23 (the host checks)
         Lane l;
 #pragma unroll
         for (int h = 0; h < PHASES; ++h) {
             int row, chunk;
             source(h * NT + threadIdx.x, row, chunk);
-            l.off[h] = !TALL || chunk * CE < x_left ? row * pitch + chunk * 16 : kOutside;
+            if constexpr (GATHER) l.off[h] = row < x_left ? (uint32_t)rows[row] * pitch + chunk * 16 : kOutside;
+            else l.off[h] = !TALL || chunk * CE < x_left ? row * pitch + chunk * 16 : kOutside;
         }
         l.step = STEP * pitch;
-        l.range = TALL ? 0x7fffffffu : (uint32_t)min(x_left, X) * pitch;
+        l.range = TALL || GATHER ? 0x7fffffffu : (uint32_t)min(x_left, X) * pitch;
         return l;
     }
     __device__ static void fetch(const typename El<F32>::type *tile, const Lane &l, int c_left,
@@ -185,7 +189,7 @@ template <bool F32, bool TALL, int X, int NT> struct Operand {
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         uint32_t at[LOADS];
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i) at[i] = l.off[i % PHASES] + (i - i % PHASES) * l.step;
+        for (int i = 0; i < LOADS; ++i) at[i] = l.off[i % PHASES] + (i - i % PHASES) * l.step;  // (GATHER: off[i])
         if (c_left < BK) {  // the last step: zeros past the end of c
 #pragma unroll
             for (int i = 0; i < LOADS; ++i) {
@@ -318,10 +322,10 @@ template <bool F32, int WM, int WN, int MT, int NTL, int ST> struct Shape {
     static constexpr int WAVES = LDS > 80 * 1024 ? NT / 256 : LDS > 53 * 1024 ? NT / 128 : 3;  // a SIMD, by LDS
 
     // The workgroup's tile of one product; la and lb are the operands' buffers.
-    template <bool TALL_A, bool TALL_B, bool DIRECT, class E>
+    template <bool TALL_A, bool TALL_B, bool DIRECT, bool GATHER, class E>
     __device__ __forceinline__ static void run(const Gemm<E> &p, int block, unsigned char *const (&la)[ST],
                                                unsigned char *const (&lb)[ST]) {
-        using A = Operand<F32, TALL_A, BM, NT>;
+        using A = Operand<F32, TALL_A, BM, NT, GATHER>;
         using B = Operand<F32, TALL_B, BN, NT>;
         using T = typename El<F32>::type;
         typedef LDS_PTR unsigned char *lds;
@@ -329,7 +333,9 @@ template <bool F32, int WM, int WN, int MT, int NTL, int ST> struct Shape {
         place(p, block, tm, tn, split);
         const int m0 = tm * BM, n0 = tn * BN;
         const int c_begin = split * p.c_per_split, c_end = min(p.C, c_begin + p.c_per_split);
-        const T *a = (const T *)p.a + (TALL_A ? (int64_t)c_begin * p.lda + m0 : (int64_t)m0 * p.lda + c_begin);
+        const T *a = (const T *)p.a + (TALL_A   ? (int64_t)c_begin * p.lda + m0
+                                       : GATHER ? (int64_t)c_begin
+                                                : (int64_t)m0 * p.lda + c_begin);
         const T *b = (const T *)p.b + (TALL_B ? (int64_t)c_begin * p.ldb + n0 : (int64_t)n0 * p.ldb + c_begin);
         const int64_t step_a = TALL_A ? BK * p.lda : BK, step_b = TALL_B ? BK * p.ldb : BK;
 
@@ -380,8 +386,8 @@ template <bool F32, int WM, int WN, int MT, int NTL, int ST> struct Shape {
         int left = c_end - c_begin;
         if constexpr (DIRECT) {
             constexpr int LOADS = A::LOADS + B::LOADS;
-            const typename A::Lane lane_a = A::plan(p.lda, p.M - m0);
-            const typename B::Lane lane_b = B::plan(p.ldb, p.N - n0);
+            const typename A::Lane lane_a = A::plan(p.lda, p.M - m0, GATHER ? p.rows + m0 : nullptr);
+            const typename B::Lane lane_b = B::plan(p.ldb, p.N - n0, nullptr);
             auto fetch = [&](int s, int c_left) {
                 A::fetch(a, lane_a, c_left, (lds)la[s]);
                 B::fetch(b, lane_b, c_left, (lds)lb[s]);
@@ -399,7 +405,7 @@ template <bool F32, int WM, int WN, int MT, int NTL, int ST> struct Shape {
                 }
             }
         } else {
-            static_assert(DIRECT || ST == 2, "through registers: one step ahead");
+            static_assert(DIRECT || (ST == 2 && !GATHER), "through registers: one step ahead");
             u32x4_t ra[A::LOADS], rb[B::LOADS];
             auto pull = [&](int c_left) {
                 A::pull(a, p.lda, p.M - m0, c_left, ra);
@@ -488,13 +494,13 @@ template <bool F32, int WM, int WN, int MT, int NTL, int ST> struct Shape {
     BUFFER(a2, S::STAGES > 2 ? S::A_BYTES : 16); BUFFER(b2, S::STAGES > 2 ? S::B_BYTES : 16);                 \
     BUFFER(a3, S::STAGES > 3 ? S::A_BYTES : 16); BUFFER(b3, S::STAGES > 3 ? S::B_BYTES : 16);
 
-template <bool TALL_A, bool TALL_B, bool DIRECT, typename S, class E>
+template <bool TALL_A, bool TALL_B, bool DIRECT, typename S, bool GATHER = false, class E>
 __device__ __forceinline__ void run_tile(const Gemm<E> &p, int block, unsigned char *a0, unsigned char *a1,
                                          unsigned char *a2, unsigned char *a3, unsigned char *b0, unsigned char *b1,
                                          unsigned char *b2, unsigned char *b3) {
-    if constexpr (S::STAGES == 2) S::template run<TALL_A, TALL_B, DIRECT>(p, block, {a0, a1}, {b0, b1});
-    else if constexpr (S::STAGES == 3) S::template run<TALL_A, TALL_B, DIRECT>(p, block, {a0, a1, a2}, {b0, b1, b2});
-    else S::template run<TALL_A, TALL_B, DIRECT>(p, block, {a0, a1, a2, a3}, {b0, b1, b2, b3});
+    if constexpr (S::STAGES == 2) S::template run<TALL_A, TALL_B, DIRECT, GATHER>(p, block, {a0, a1}, {b0, b1});
+    else if constexpr (S::STAGES == 3) S::template run<TALL_A, TALL_B, DIRECT, GATHER>(p, block, {a0, a1, a2}, {b0, b1, b2});
+    else S::template run<TALL_A, TALL_B, DIRECT, GATHER>(p, block, {a0, a1, a2, a3}, {b0, b1, b2, b3});
 }
 
 // The sums of the splits with their epilogue, four columns a thread.
