@@ -305,7 +305,8 @@ __global__ __launch_bounds__(1024) void rank_kernel(RankParams p) {
 }
 
 // Rows of x with a target to rows of whole 16 bytes, zeros behind them; dx of the
-// others to zero; and w to such rows where its own are not.  A wave a row.
+// others to zero; and w to such rows where its own are not.  A wave a row, or 64 chunks
+// of one where the rows are few.  8192 x 4096 bf16 with dloss x besides: 22 us (134 MB).
 struct PackParams {
     const void *from[2];  // x, w (null: as it is)
     void *to[2];          // null: only what follows is wanted
@@ -315,9 +316,9 @@ struct PackParams {
     const int *rank;
     void *dx;
     int64_t lddx;
-    int K, chunks;
+    int K, chunks, parts;
 };
-template <bool F32> __global__ __launch_bounds__(256) void pack_kernel(PackParams p) {
+template <bool F32, bool PARTS> __global__ __launch_bounds__(256) void pack_kernel(PackParams p) {
     using T = typename El<F32>::type;
     constexpr int CE = El<F32>::CE;
     const int lane = threadIdx.x & 63;
@@ -325,12 +326,15 @@ template <bool F32> __global__ __launch_bounds__(256) void pack_kernel(PackParam
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
         if (!p.from[g]) continue;
-        for (int64_t row = start; row < p.rows[g]; row += step) {
+        for (int64_t id = start; id < p.rows[g] * p.parts; id += step) {
+            const int64_t row = PARTS ? id / p.parts : id;
+            const int first = PARTS ? (int)(id - row * p.parts) * 64 + lane : lane;
+            const int end = PARTS ? min(first + 1, p.chunks) : p.chunks;
             const int64_t at = g == 0 ? p.rank[row] : row;
             if (at < 0) {
                 if (p.dx) {
                     const float none[CE] = {};
-                    for (int c = lane; c < p.chunks; c += 64)
+                    for (int c = first; c < end; c += 64)
                         Pack<F32, CE>::store(p.dx, row * p.lddx + c * CE, p.K - c * CE, none);
                 }
                 continue;
@@ -340,7 +344,7 @@ template <bool F32> __global__ __launch_bounds__(256) void pack_kernel(PackParam
             u32x4_t *scaled = g == 0 && p.scaled ? (u32x4_t *)p.scaled + at * p.chunks : nullptr;
             const float by = scaled && *p.most != 0.0f ? p.dloss[row] / *p.most : 0.0f;
 #pragma unroll 4
-            for (int c = lane; c < p.chunks; c += 64) {
+            for (int c = first; c < end; c += 64) {
                 const int left = p.K - c * CE;
                 u32x4_t v;
                 if (left >= CE) {
@@ -563,10 +567,21 @@ Tile tile_of(const Plan &p) { return p.large ? kLarge : p.fine ? (p.deep ? kFine
 // Rows of one wave, which leave one row of column sums: of a tile's WM x MT x 16.
 int wave_rows(const Plan &p) { return p.large ? 128 : p.fine ? 16 : 64; }
 
-// A product whose epilogue wants whole sums: its c is not cut.
+// A product whose epilogue wants whole sums: its c is not cut, so tiles that fill the
+// last round of units count for more than in plan_of.  fp32: 64 x 64 always (us, with
+// 128 x 128 and with 64 x 64: 1021 x 776 x 5000 115 and 81, 600 x 2048 x 8192 261 and
+// 179, 3000 x 1024 x 4000 227 and 208, 8192 x 4096 x 4096 2040 and 2026).  bf16: 256 x
+// 256 where that is no more than 2/5 of the rounds of 128 x 128 (3000 x 1024 x 4000 38
+// against 43, 4000 x 2048 x 2500 56 against 69; but with 2 rounds against 1, 600 x 2048
+// x 8192, 55 against 38).
 Plan whole_plan(int64_t M, int64_t N, int64_t K, bool f32, bool direct) {
     const Size sz = {M, N, K};
     Plan p = plan_of(&sz, 1, f32, direct);
+    const int64_t t128 = ceil_div(M, 128) * ceil_div(N, 128), t256 = ceil_div(M, 256) * ceil_div(N, 256);
+    if (f32) p.fine = true, p.deep = false;
+    else if (direct && t256 >= 128 && 5 * ceil_div(t256, 256) <= 2 * ceil_div(t128, 256)) p.large = true, p.deep = false;
+    const int edge = p.large ? 256 : p.fine ? 64 : 128;
+    p.tiles_m[0] = (int)ceil_div(M, edge), p.tiles_n[0] = (int)ceil_div(N, edge);
     p.splits[0] = 1;
     p.c_per_split[0] = (int)(ceil_div(K, f32 ? 32 : 64) * (f32 ? 32 : 64));
     p.blocks[0] = (int64_t)p.tiles_m[0] * p.tiles_n[0];
@@ -656,27 +671,33 @@ BwdSpace bwd_space(int64_t M, int64_t K, int64_t V, bool f32) {
     return s;
 }
 
-template <bool F32> int launch_pack(const PackParams &p, hipStream_t stream) {
+template <bool F32> int launch_pack(PackParams p, hipStream_t stream) {
     int64_t rows = p.from[0] ? p.rows[0] : 0;
     if (p.from[1] && p.rows[1] > rows) rows = p.rows[1];
-    const int64_t blocks = ceil_div(rows, 4);
-    if (blocks == 0 || p.chunks == 0) return HYENA_OK;
-    hipLaunchKernelGGL(pack_kernel<F32>, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, stream, p);
+    if (rows == 0 || p.chunks == 0) return HYENA_OK;
+    p.parts = rows < 1024 ? (int)ceil_div(p.chunks, 64) : 1;
+    const int64_t blocks = ceil_div(rows * p.parts, 4);
+    hipLaunchKernelGGL((p.parts > 1 ? pack_kernel<F32, true> : pack_kernel<F32, false>),
+                       dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, stream, p);
     return launch_status();
 }
 
-// LAUNCH(DIRECT, GATHER, S) for the plan's tiles.
-#define FOR_TILE(plan, direct, gather, LAUNCH)                                        \
-    switch (tile_of(plan)) {                                                          \
-    case kLarge: if constexpr (!F32) { BOTH(gather, LAUNCH, Large) } break;           \
-    case kDeep: BOTH(gather, LAUNCH, Deep<F32>) break;                                \
-    case kFineDeep: if constexpr (!F32) { BOTH(gather, LAUNCH, FineDeep) } break;     \
-    case kSmall:                                                                      \
-        if (direct) { BOTH(gather, LAUNCH, Small<F32>) } else { LAUNCH(false, false, Small<F32>) } \
-        break;                                                                        \
-    case kFine:                                                                       \
-        if (direct) { BOTH(gather, LAUNCH, Fine<F32>) } else { LAUNCH(false, false, Fine<F32>) } \
-        break;                                                                        \
+// LAUNCH(DIRECT, GATHER, S) for whole_plan's tiles.
+#define FOR_TILE(plan, direct, gather, LAUNCH)                                               \
+    if constexpr (F32) {                                                                     \
+        if (direct) { BOTH(gather, LAUNCH, Fine<true>) } else { LAUNCH(false, false, Fine<true>) } \
+    } else {                                                                                 \
+        switch (tile_of(plan)) {                                                             \
+        case kLarge: BOTH(gather, LAUNCH, Large) break;                                      \
+        case kDeep: BOTH(gather, LAUNCH, Deep<false>) break;                                 \
+        case kFineDeep: BOTH(gather, LAUNCH, FineDeep) break;                                \
+        case kSmall:                                                                         \
+            if (direct) { BOTH(gather, LAUNCH, Small<false>) } else { LAUNCH(false, false, Small<false>) } \
+            break;                                                                           \
+        case kFine:                                                                          \
+            LAUNCH(false, false, Fine<false>)                                                \
+            break;                                                                           \
+        }                                                                                    \
     }
 #define BOTH(gather, LAUNCH, S)                                      \
     if (gather) { LAUNCH(true, true, S) } else { LAUNCH(true, false, S) }
@@ -783,7 +804,9 @@ int xent_bwd(const void *x, const void *w, const void *bias, const int64_t *targ
 #define DZ(DIRECT, GATHER, S)                                                                                       \
     hipLaunchKernelGGL((dz_kernel<F32, DIRECT, GATHER, S>), dim3((unsigned)pl.blocks[0]), dim3(S::NT), 0, stream, p, \
                        r.count);
-        if (M > 0) FOR_TILE(pl, direct, gather, DZ)
+        if (M > 0) {
+            FOR_TILE(pl, direct, gather, DZ)
+        }
 #undef DZ
         if ((st = launch_status()) != HYENA_OK) return st;
 
