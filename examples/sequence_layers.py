@@ -7,7 +7,10 @@ Two layers, each a residual block over x [B, L, D]:
                      x += (GatedScan(q, k, v, g)) Wo^T
 
 between an embedding and a readout.  The task is next-token prediction of a
-sequence whose second half repeats its first.  Decoding keeps a ring cache of
+sequence whose second half repeats its first.  Training takes the loss from the last
+layer's output without logits in between (LinearXent; the first half, which cannot be
+known, has no target), and the step over all weights in a few launches (grad_norm,
+adamw_step; fp32 masters of bf16 weights).  Decoding keeps a ring cache of
 past rows for the convolution and one state row for the recurrence; a step is a
 fixed set of launches, captured once in a HIP graph and replayed for each token.
 
@@ -45,16 +48,23 @@ class Model(torch.nn.Module):
         self.scan_out = new(D, D, scale=D ** -0.5)
         self.readout = new(VOCAB, D, scale=0.1 * D ** -0.5)
 
-    def forward(self, tokens):
-        """Logits [B, L, VOCAB] of tokens [B, L], with gradients."""
+    def hidden(self, tokens):
+        """What the readout sees of tokens [B, L], [B, L, width]."""
         D, lin = self.width, hc.LinearAct.apply
         x = self.embed[tokens]
         q, k, v = (lin(x, w, None, None, "none") for w in self.conv_in)
         x = lin(hc.HyenaConv.apply(q, k, v, self.taps, GROUP), self.conv_out, None, x, "none")
         z = lin(x, self.scan_in, self.scan_bias, None, "none")
         y, _ = hc.GatedScan.apply(*(z[..., i * D:(i + 1) * D] for i in range(4)))
-        x = lin(y, self.scan_out, None, x, "none")
-        return lin(x, self.readout, None, None, "none")
+        return lin(y, self.scan_out, None, x, "none")
+
+    def forward(self, tokens):
+        """Logits [B, L, VOCAB] of tokens [B, L], with gradients."""
+        return hc.LinearAct.apply(self.hidden(tokens), self.readout, None, None, "none")
+
+    def loss(self, tokens, target):
+        """The loss of each position [B, L] (fp32), with gradients; 0 where target is no token."""
+        return hc.LinearXent.apply(self.hidden(tokens), self.readout, target)
 
 
 class Decoder:
@@ -124,25 +134,22 @@ def train(model: Model, steps: int, B: int = 64, half: int = 8, lr: float = 3e-3
     gen = torch.Generator().manual_seed(seed)
     # fp32 copies of the weights take the updates
     params = list(model.parameters())
-    master = [p.detach().float().clone().requires_grad_(True) for p in params]
-    opt = torch.optim.Adam(master, lr=lr)
+    masters = [p.detach().float().clone() for p in params]
+    moments = [[torch.zeros_like(m) for m in masters] for _ in range(2)]
     losses = []
     for step in range(steps):
-        opt.param_groups[0]["lr"] = lr * (1 - step / steps)
         tokens = batch(B, half, gen).to(model.embed.device)
-        logits = model(tokens[:, :-1])
         # what can be known: the repeated half
-        loss = torch.nn.functional.cross_entropy(logits[:, half - 1:].float().flatten(0, 1),
-                                                 tokens[:, half:].flatten())
+        target = tokens[:, 1:].clone()
+        target[:, :half - 1] = -100
+        loss = model.loss(tokens[:, :-1], target).sum() / (B * half)
         model.zero_grad(set_to_none=True)
         loss.backward()
-        for m, p in zip(master, params):
-            m.grad = p.grad.float()
-        torch.nn.utils.clip_grad_norm_(master, 1.0)
-        opt.step()
         with torch.no_grad():
-            for m, p in zip(master, params):
-                p.copy_(m)
+            grads = [p.grad.contiguous() for p in params]
+            _, scale = hc.grad_norm(grads, max_norm=1.0)
+            hc.adamw_step(params, grads, *moments, step=step + 1, lr=lr * (1 - step / steps), masters=masters,
+                          grad_scale=scale)
         losses.append(loss.item())
         if step % 50 == 0 or step == steps - 1:
             log("step %d loss %.4f" % (step, losses[-1]))
