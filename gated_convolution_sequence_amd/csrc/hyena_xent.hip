@@ -339,6 +339,7 @@ template <bool F32, bool PARTS> __global__ __launch_bounds__(256) void pack_kern
                 }
                 continue;
             }
+            if (!p.to[g] && !(g == 0 && p.scaled)) continue;  // only dx of the others
             const T *from = (const T *)p.from[g] + row * p.ld[g];
             u32x4_t *to = p.to[g] ? (u32x4_t *)p.to[g] + at * p.chunks : nullptr;
             u32x4_t *scaled = g == 0 && p.scaled ? (u32x4_t *)p.scaled + at * p.chunks : nullptr;

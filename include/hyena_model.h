@@ -88,7 +88,8 @@ int hyena_xent_fwd(const void *x, const void *w, const void *bias,
  * dx [M, K] has row stride lddx; dw [V, K], db [V] contiguous; all in `dtype`.
  * Any output may be NULL, not all.  bf16: softmax - [target] and, for dw, dloss x
  * (over the largest |dloss|) are rounded once each to bf16, as operands of the products; db sums unrounded
- * values; sums are fp32, outputs rounded once. */
+ * values; sums are fp32, outputs rounded once.  (In dw, a dloss below 2^-126 of the
+ * largest counts as 0.)  A row whose lse is not finite has gradients of NaN. */
 int hyena_xent_bwd(const void *x, const void *w, const void *bias,
                    const int64_t *target, const float *lse, const float *dloss,
                    int64_t M, int64_t K, int64_t V, int64_t ldx, int64_t lddx,
@@ -104,8 +105,8 @@ int hyena_xent_workspace(int64_t M, int64_t K, int64_t V, int dtype,
  *
  * `tensors` is an array of n descriptors in HOST memory, read before the call
  * returns.  Tensors are contiguous, of any sizes (0 among them) below 2^40
- * elements; param and grad are `dtype`.  No two descriptors may share memory that
- * is written. */
+ * elements; param and grad are `dtype`.  Nothing that a step writes may overlap
+ * anything else of it (HYENA_ERR_ALIAS), in one tensor or between two. */
 typedef struct hyena_tensor {
     void *param;           /* [numel] */
     const void *grad;      /* [numel] */

@@ -207,6 +207,25 @@ def test_a_captured_step_takes_its_numbers_from_the_device(bits):
                 assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)) if a.dtype == F8 else torch.equal(a, b), (r, k)
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_neighbours_in_one_buffer(bits):
+    """Tensors that touch, and a gradient that two parameters share: accepted; the same tensor twice is not."""
+    flat = [torch.randn(2000, device=DEV) for _ in range(3)]
+    flat[2].square_()
+    if bits == 8:
+        flat[1:] = [torch.zeros(2000, dtype=torch.uint8, device=DEV).view(F8) for _ in range(2)]
+    t = dict(zip(("params", "exp_avgs", "exp_avg_sqs"), ([f[:999], f[999:]] for f in flat)))
+    if bits == 8:
+        s = torch.zeros(2, 8, device=DEV)
+        t["exp_avg_scales"], t["exp_avg_sq_scales"] = ([x[:4], x[4:]] for x in s)
+    g = torch.randn(1001, device=DEV)
+    t["grads"] = [g[:999], g]
+    check_step(t, 2, seed=9)
+    t["params"] = [t["params"][0], flat[0][:1001]]
+    with pytest.raises(hc.ModelError):
+        hc.adamw_step(**t, step=3, **HYPER)
+
+
 def test_a_step_below_one_on_the_device_counts_as_one():
     t = lists([100], F32, 7)
     check_step(t, 1, step_arg=torch.zeros(1, dtype=torch.int64, device=DEV))

@@ -162,6 +162,10 @@ def adamw(rows=(ROW,), n=None, lr=1e-3, b1=0.9, b2=0.95, eps=1e-8, decay=0.1, st
     (dict(step_dev=P[8] + 4), -5), (dict(seed_dev=P[8] + 4), -5),
     (dict(rows=({**ROW, "master": P[2]},)), -6), (dict(rows=({**ROW, "grad": P[0]},)), -6),
     (dict(rows=({**ROW, "exp_avg_scale": P[5]},), bits=8), -6), (dict(rows=({**ROW, "exp_avg_sq": P[2] + 3996},)), -6),
+    (dict(rows=(ROW, ROW)), -6),
+    (dict(rows=(ROW, {**{k: v + 4096 for k, v in ROW.items()}, "numel": 1000, "exp_avg": P[3] + 3996})), -6),
+    (dict(rows=(ROW, {**{k: v + 4096 for k, v in ROW.items()}, "numel": 1000, "grad": P[6]})), -6),
+    (dict(scale=P[2] + 40), -6), (dict(step_dev=P[6]), -6),
     (dict(lr=math.nan), -7), (dict(b1=1.0), -7), (dict(b1=-0.1), -7), (dict(b2=1.0), -7), (dict(b2=math.nan), -7),
     (dict(eps=-1e-8), -7), (dict(eps=math.inf), -7), (dict(decay=math.inf), -7), (dict(step=0), -7), (dict(bits=16), -7),
     (dict(dtype=2), -9),
