@@ -235,8 +235,7 @@ __device__ __forceinline__ Codes round_codes(const float (&x)[8], const uint32_t
     float top = 0.0f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(x[k]));
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
+    top = over_32(top, [](float a, float b) { return fmaxf(a, b); });
     scale = top < 0x1p-117f ? 0.0f : top * (1.0f / 448.0f);
     const float inverse = scale != 0.0f ? 1.0f / scale : 0.0f;
     float q[8];

@@ -33,12 +33,6 @@ struct NormParams {
 
 template <bool F32> constexpr int kVec = F32 ? 4 : 8;  // values of 16 bytes
 
-__device__ inline float wave_sum(float s) {
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) s += __shfl_xor(s, o);
-    return s;
-}
-
 // The sums over the T lanes that share a row.  `lds` is the row's own: [2][T /
 // 64] values a call; calls alternate between two areas (`turn`), so that one barrier each
 // is enough.

@@ -33,6 +33,31 @@ typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef short s16x8_t __attribute__((ext_vector_type(8)));
 #define LDS_PTR __attribute__((address_space(3)))
 
+// ---- over the lanes of a wave --------------------------------------------------------
+
+// x of the lane that a data-parallel move of the vector unit takes it from: without a
+// trip through LDS, as a shuffle makes.
+template <int CTRL> __device__ __forceinline__ float moved(float x) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true));
+}
+// f of x over each 16 lanes, in all of them: pairs, fours, the other four of eight
+// (mirrored: its lanes are alike by then), the other eight.
+template <class F> __device__ __forceinline__ float over_16(float x, F f) {
+    x = f(x, moved<0xB1>(x));
+    x = f(x, moved<0x4E>(x));
+    x = f(x, moved<0x141>(x));
+    return f(x, moved<0x140>(x));
+}
+template <class F> __device__ __forceinline__ float over_32(float x, F f) {
+    x = over_16(x, f);
+    return f(x, __shfl_xor(x, 16));
+}
+__device__ __forceinline__ float wave_sum(float x) {
+    const auto add = [](float a, float b) { return a + b; };
+    x = over_32(x, add);
+    return x + __shfl_xor(x, 32);
+}
+
 // ---- V values of a row ------------------------------------------------------------
 
 template <bool F32> struct El;
