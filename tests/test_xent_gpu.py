@@ -188,6 +188,18 @@ def test_parts_of_the_backward(need, M, K, V):
         assert (g is not None) == bool(n)
 
 
+@pytest.mark.parametrize("M", [8191, 8192, 8193, 16384, 70001])
+@pytest.mark.parametrize("K,V", [(8, 3), (100, 4), (264, 1), (1, 130)])
+@pytest.mark.parametrize("masked", [0.0, 0.5, 0.999])
+def test_many_rows_of_few_entries(M, K, V, masked):
+    """Rows numbered by several workgroups, short rows packed several a wave, narrow bias gradients."""
+    t = inputs(M, K, V, BF16 if K != 100 else F32, M + V, masked=masked)
+    t["target"][M // 2:M // 2 + 3000] = -1  # a stretch without
+    loss, _, dx, _, _ = check_all(**t, what="%d rows" % M)
+    off = (t["target"] < 0) | (t["target"] >= V)
+    assert not loss[off].any() and not dx[off].any()
+
+
 def test_pieces_of_the_vocabulary():
     """Rows so many that a piece holds 2048 entries: three pieces, dx added up over them."""
     M, K, V = 66000, 24, 5000
