@@ -8,9 +8,8 @@
 //     and every product after that reads the number of rows from memory.  So such
 //     rows cost no products, and what their x holds (NaN from padding) meets no zero in
 //     dw's sums.  The logits fetch the rows from where they are; dw's sum runs over
-//     rows, so for it pack_kernel copies them together.  Where the rows are no whole 16
-//     bytes, or 2 GiB apart, they are copied for the logits as well, and w where its
-//     rows are no whole 16 bytes.
+//     rows, so for it pack_kernel copies them together.  Where rows are no whole 16
+//     bytes they are copied for the logits as well, and w where its are not.
 //   * Forward: a tile keeps the maximum and the sum of exp(z - maximum) of its
 //     columns for each row, from the registers that hold the sums; merge_kernel
 //     joins the tiles.
@@ -23,6 +22,8 @@
 //     with a mean's equal dloss one factor (to 0.4 % off) for all gradients.  Equal
 //     dloss leave x as it is, others round it once more.
 //   * No more than 16 rows forward: the weights stream once through rows_product.
+
+#include <initializer_list>
 
 #include "hyena_model.h"
 #include "layer_gemm.h"
@@ -141,9 +142,9 @@ template <class S, class E> __device__ inline bool rows_from(Gemm<E> &p, const i
 }
 
 template <bool F32, bool DIRECT, bool GATHER, typename S>
-__global__ __launch_bounds__(S::NT, S::WAVES) void stats_kernel(Gemm<StatsEpi> p, const int *count) {
+__global__ __launch_bounds__(S::NT, S::WAVES) void stats_kernel(Gemm<StatsEpi> p, const int *count, const int *apart) {
     TILE_BUFFERS(S)
-    if (!rows_from<S>(p, count)) return;
+    if ((apart && (*apart != 0) == GATHER) || !rows_from<S>(p, count)) return;
     run_tile<false, false, DIRECT, S, GATHER>(p, blockIdx.x, a0, a1, a2, a3, b0, b1, b2, b3);
 }
 
@@ -230,6 +231,7 @@ struct RankParams {
     float *lse_out, *dloss_out;   // packed
     float *loss, *lse;            // forward: zeroed where there is no target
     int *rank, *index, *goal, *count;
+    int *apart;                   // cleared, for apart_kernel; or null
     float *most;                  // backward: the largest |dloss| of them
     int *counts;                  // of each workgroup's rows (more than one workgroup)
     float *tops;                  // backward: the largest |dloss| there
@@ -330,10 +332,22 @@ __global__ __launch_bounds__(1024) void rank_kernel(RankParams p) {
             p.loss[m] = 0.0f, p.lse[m] = 0.0f;
         }
     }
-    if (blockIdx.x == gridDim.x - 1 && threadIdx.x == 0) *p.count = base + half + both;
+    if (blockIdx.x == gridDim.x - 1 && threadIdx.x == 0) {
+        *p.count = base + half + both;
+        if (p.apart) *p.apart = 0;
+    }
     if (!p.most || blockIdx.x != 0) return;
     top = over_1024(top, tops, larger);
     if (threadIdx.x == 0) *p.most = top;
+}
+
+// Where x is 2 GiB or more, a tile's rows may lie further apart than its 32-bit offsets
+// reach (a few with a target among very many without): then the rows are packed, and the
+// products that gather them leave at once; else those of packed rows do.
+__global__ __launch_bounds__(256) void apart_kernel(const int *index, const int *count, int reach, int *apart) {
+    const int n = *count;
+    const int64_t first = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 256;
+    if (first < n && index[min(first + 255, (int64_t)n - 1)] - index[first] > reach) *apart = 1;
 }
 
 // Rows of x with a target to rows of whole 16 bytes, zeros behind them; dx of the
@@ -346,6 +360,7 @@ struct PackParams {
     const float *dloss, *most;
     int64_t rows[2], ld[2];
     const int *rank;
+    const int *apart;     // to[0] only where it says so, or null
     void *dx;
     int64_t lddx;
     int K, chunks, parts;
@@ -376,9 +391,10 @@ template <bool F32, int MODE> __global__ __launch_bounds__(256) void pack_kernel
                 }
                 continue;
             }
-            if (!p.to[g] && !(g == 0 && p.scaled)) continue;  // only dx of the others
+            void *const whole = g == 0 && p.apart && *p.apart == 0 ? nullptr : p.to[g];
+            if (!whole && !(g == 0 && p.scaled)) continue;  // only dx of the others
             const T *from = (const T *)p.from[g] + row * p.ld[g];
-            u32x4_t *to = p.to[g] ? (u32x4_t *)p.to[g] + at * p.chunks : nullptr;
+            u32x4_t *to = whole ? (u32x4_t *)whole + at * p.chunks : nullptr;
             u32x4_t *scaled = g == 0 && p.scaled ? (u32x4_t *)p.scaled + at * p.chunks : nullptr;
             const float by = scaled && *p.most != 0.0f ? p.dloss[row] / *p.most : 0.0f;
 #pragma unroll 4
@@ -513,9 +529,9 @@ using DwEpi = GradEpi<false>;
 using DxEpi = GradEpi<true>;
 
 template <bool F32, bool DIRECT, bool GATHER, typename S>
-__global__ __launch_bounds__(S::NT, S::WAVES) void dz_kernel(Gemm<DzEpi> p, const int *count) {
+__global__ __launch_bounds__(S::NT, S::WAVES) void dz_kernel(Gemm<DzEpi> p, const int *count, const int *apart) {
     TILE_BUFFERS(S)
-    if (!rows_from<S>(p, count)) return;
+    if ((apart && (*apart != 0) == GATHER) || !rows_from<S>(p, count)) return;
     run_tile<false, false, DIRECT, S, GATHER>(p, blockIdx.x, a0, a1, a2, a3, b0, b1, b2, b3);
 }
 
@@ -662,7 +678,7 @@ FwdSpace fwd_space(int64_t M, int64_t K, int64_t V, bool f32) {
     } else {
         // w may lie at any element, which the caller of hyena_xent_workspace does not say
         const int64_t tiles[2] = {whole_plan(M, V, K, f32, false).tiles_n[0], whole_plan(M, V, K, f32, true).tiles_n[0]};
-        s.count = take(4), s.counts = take(rank_blocks(M) * 4);
+        s.count = take(8), s.counts = take(rank_blocks(M) * 4);
         s.rank = take(M * 4), s.index = take(M * 4), s.goal = take(M * 4), s.at = take(M * 4);
         s.part = take((tiles[0] > tiles[1] ? tiles[0] : tiles[1]) * M * 8);
         s.x = take(M * whole(K, eb) * eb);
@@ -698,7 +714,7 @@ BwdSpace bwd_space(int64_t M, int64_t K, int64_t V, bool f32) {
         return at;
     };
     s.piece = piece_of(M, V, eb);
-    s.count = take(8), s.counts = take(rank_blocks(M) * 4), s.tops = take(rank_blocks(M) * 4);
+    s.count = take(12), s.counts = take(rank_blocks(M) * 4), s.tops = take(rank_blocks(M) * 4);
     s.rank = take(M * 4), s.index = take(M * 4), s.goal = take(M * 4);
     s.lse = take(M * 4), s.dloss = take(M * 4);
     s.x = take(M * whole(K, eb) * eb), s.scaled = take(M * whole(K, eb) * eb);
@@ -768,9 +784,17 @@ template <bool F32> int launch_pack(PackParams p, hipStream_t stream) {
     if (gather) { LAUNCH(true, true, S) } else { LAUNCH(true, false, S) }
 
 // Whether the logits can fetch the rows of x from where they are: whole aligned 16
-// bytes, all within 32-bit offsets, w as well (rows are gathered straight into LDS).
-bool gather_ok(const void *x, int64_t M, int64_t ldx, int64_t K, int64_t eb, const void *w) {
-    return direct_ok(x, ldx, K, eb) && direct_ok(w, K, K, eb) && M * ldx * eb < (int64_t)1 << 31;
+// bytes, w as well (rows are gathered straight into LDS); and whether all lie within
+// their offsets, or apart_kernel has to look.
+bool gather_ok(const void *x, int64_t ldx, int64_t K, int64_t eb, const void *w) {
+    return direct_ok(x, ldx, K, eb) && direct_ok(w, K, K, eb);
+}
+constexpr int64_t kReach = ((int64_t)1 << 31) - ((int64_t)1 << 23);  // a row is below 2^23 bytes
+bool all_near(int64_t M, int64_t ldx, int64_t eb) { return M * ldx * eb <= kReach; }
+int launch_apart(const RankParams &r, int64_t ldx, int64_t eb, hipStream_t stream) {
+    hipLaunchKernelGGL(apart_kernel, dim3((unsigned)ceil_div(r.M, 256 * 256)), dim3(256), 0, stream, r.index, r.count,
+                       (int)(kReach / (ldx * eb)) - 1, r.apart);
+    return launch_status();
 }
 
 template <bool F32>
@@ -795,14 +819,16 @@ int xent_fwd(const void *x, const void *w, const void *bias, const int64_t *targ
         r.target = target, r.loss = loss, r.lse = lse, r.V = V, r.M = (int)M;
         r.rank = (int *)(ws + sp.rank), r.index = (int *)(ws + sp.index), r.goal = (int *)(ws + sp.goal);
         r.count = (int *)(ws + sp.count), r.counts = (int *)(ws + sp.counts);
+        const bool gather = gather_ok(x, ldx, K, eb, w);
+        if (gather && !all_near(M, ldx, eb)) r.apart = r.count + 1;
         if ((st = launch_rank(r, stream)) != HYENA_OK) return st;
         const int64_t ld = whole(K, eb);
-        const bool gather = gather_ok(x, M, ldx, K, eb, w);
         PackParams k = {};
-        if (!gather) {
-            k.from[0] = x, k.to[0] = ws + sp.x, k.rows[0] = M, k.ld[0] = ldx, k.rank = r.rank;
+        if (!gather || r.apart) {
+            k.from[0] = x, k.to[0] = ws + sp.x, k.rows[0] = M, k.ld[0] = ldx, k.rank = r.rank, k.apart = r.apart;
             if (ld != K) k.from[1] = w, k.to[1] = ws + sp.w, k.rows[1] = V, k.ld[1] = K;
             k.K = (int)K, k.chunks = (int)(ld * eb / 16);
+            if (r.apart && (st = launch_apart(r, ldx, eb, stream)) != HYENA_OK) return st;
             if ((st = launch_pack<F32>(k, stream)) != HYENA_OK) return st;
         }
         const bool direct = gather || k.from[1] || direct_ok(w, K, K, eb);
@@ -810,16 +836,20 @@ int xent_fwd(const void *x, const void *w, const void *bias, const int64_t *targ
         if (pl.blocks[0] > 0x7fffffff) return HYENA_ERR_UNSUPPORTED;
         StatsEpi e = {};
         e.bias = bias, e.target = r.goal, e.part = (Part *)(ws + sp.part), e.at = (float *)(ws + sp.at), e.ldp = M;
-        char *none = nullptr;
-        Gemm<StatsEpi> p = gemm_params(pl, 0, Size{M, V, K}, gather ? x : k.to[0], gather ? ldx : ld,
-                                       k.from[1] ? k.to[1] : w, k.from[1] ? ld : K, e, none);
-        p.rows = r.index;
+        // of rows in place, of packed rows, or of whichever apart_kernel found
+        for (const bool here : {true, false}) {
+            if (here ? !gather : gather && !r.apart) continue;
+            char *none = nullptr;
+            Gemm<StatsEpi> p = gemm_params(pl, 0, Size{M, V, K}, here ? x : k.to[0], here ? ldx : ld,
+                                           k.from[1] ? k.to[1] : w, k.from[1] ? ld : K, e, none);
+            p.rows = r.index;
 #define STATS(DIRECT, GATHER, S)                                                                                       \
     hipLaunchKernelGGL((stats_kernel<F32, DIRECT, GATHER, S>), dim3((unsigned)pl.blocks[0]), dim3(S::NT), 0, stream, p, \
-                       r.count);
-        FOR_TILE(pl, direct, gather, STATS)
+                       r.count, r.apart);
+            FOR_TILE(pl, direct, here, STATS)
 #undef STATS
-        if ((st = launch_status()) != HYENA_OK) return st;
+            if ((st = launch_status()) != HYENA_OK) return st;
+        }
         mp.tiles = pl.tiles_n[0], mp.index = r.index, mp.count = r.count, mp.tile = M, mp.row = 1;
     }
     // a workgroup a row for few rows, whose tiles are many: 59 us at 8 rows of 4096 tiles
@@ -842,14 +872,16 @@ int xent_bwd(const void *x, const void *w, const void *bias, const int64_t *targ
     r.rank = (int *)(ws + sp.rank), r.index = (int *)(ws + sp.index), r.goal = (int *)(ws + sp.goal);
     r.count = (int *)(ws + sp.count), r.most = (float *)(ws + sp.count) + 1;
     r.counts = (int *)(ws + sp.counts), r.tops = (float *)(ws + sp.tops);
+    const bool gather = gather_ok(x, ldx, K, eb, w);
+    if (gather && !all_near(M, ldx, eb)) r.apart = r.count + 2;
     if ((st = launch_rank(r, stream)) != HYENA_OK) return st;
     const int64_t ld = whole(K, eb);
-    const bool gather = gather_ok(x, M, ldx, K, eb, w);
     PackParams k = {};
-    k.from[0] = x, k.to[0] = gather ? nullptr : ws + sp.x, k.rows[0] = M, k.ld[0] = ldx, k.rank = r.rank, k.dx = dx, k.lddx = lddx;
+    k.from[0] = x, k.to[0] = gather && !r.apart ? nullptr : ws + sp.x, k.apart = r.apart, k.rows[0] = M, k.ld[0] = ldx, k.rank = r.rank, k.dx = dx, k.lddx = lddx;
     if (dw) k.scaled = ws + sp.scaled, k.dloss = dloss, k.most = r.most;
     if (ld != K) k.from[1] = w, k.to[1] = ws + sp.w, k.rows[1] = V, k.ld[1] = K;
     k.K = (int)K, k.chunks = (int)(ld * eb / 16);
+    if (r.apart && (st = launch_apart(r, ldx, eb, stream)) != HYENA_OK) return st;
     if ((st = launch_pack<F32>(k, stream)) != HYENA_OK) return st;
     const char *wp = (const char *)(k.from[1] ? k.to[1] : w);
     const int64_t ldw = k.from[1] ? ld : K;
@@ -862,17 +894,18 @@ int xent_bwd(const void *x, const void *w, const void *bias, const int64_t *targ
         DzEpi e = {};
         e.bias = bias ? (const char *)bias + v0 * eb : nullptr, e.lse = r.lse_out, e.dloss = r.dloss_out, e.target = r.goal;
         e.dz = ws + sp.dz, e.ld = ldz, e.sums = db ? (float *)(ws + sp.sums) : nullptr, e.v0 = (int)v0;
-        char *none = nullptr;
-        Gemm<DzEpi> p = gemm_params(pl, 0, Size{M, N, K}, gather ? x : k.to[0], gather ? ldx : ld, wv, ldw, e, none);
-        p.rows = r.index;
+        for (const bool here : {true, false}) {  // as in the forward
+            if (M == 0 || (here ? !gather : gather && !r.apart)) continue;
+            char *none = nullptr;
+            Gemm<DzEpi> p = gemm_params(pl, 0, Size{M, N, K}, here ? x : k.to[0], here ? ldx : ld, wv, ldw, e, none);
+            p.rows = r.index;
 #define DZ(DIRECT, GATHER, S)                                                                                       \
     hipLaunchKernelGGL((dz_kernel<F32, DIRECT, GATHER, S>), dim3((unsigned)pl.blocks[0]), dim3(S::NT), 0, stream, p, \
-                       r.count);
-        if (M > 0) {
-            FOR_TILE(pl, direct, gather, DZ)
-        }
+                       r.count, r.apart);
+            FOR_TILE(pl, direct, here, DZ)
 #undef DZ
-        if ((st = launch_status()) != HYENA_OK) return st;
+            if ((st = launch_status()) != HYENA_OK) return st;
+        }
 
         JoinParams j = {};
         j.count = r.count;

@@ -144,7 +144,7 @@ template <bool F32, int V> struct Pack {
 // or, where E::kSums, e.sums<S>(...) on the sums as the matrix cores leave them.
 template <class E> struct Gemm {
     const void *a, *b;
-    const int *rows;          // GATHER: the memory row of each row of a (all within 2^31 bytes)
+    const int *rows;          // GATHER: the memory row of each row of a, ascending; a tile's within 2^31 bytes
     int64_t lda, ldb;         // elements between memory rows of a and b
     int M, N, C;
     int tiles_m, tiles_n;
@@ -200,7 +200,7 @@ template <bool F32, bool TALL, int X, int NT, bool GATHER = false> struct Operan
         for (int h = 0; h < PHASES; ++h) {
             int row, chunk;
             source(h * NT + threadIdx.x, row, chunk);
-            if constexpr (GATHER) l.off[h] = row < x_left ? (uint32_t)rows[row] * pitch + chunk * 16 : kOutside;
+            if constexpr (GATHER) l.off[h] = row < x_left ? (uint32_t)(rows[row] - rows[0]) * pitch + chunk * 16 : kOutside;
             else l.off[h] = !TALL || chunk * CE < x_left ? row * pitch + chunk * 16 : kOutside;
         }
         l.step = STEP * pitch;
@@ -359,7 +359,7 @@ template <bool F32, int WM, int WN, int MT, int NTL, int ST> struct Shape {
         const int m0 = tm * BM, n0 = tn * BN;
         const int c_begin = split * p.c_per_split, c_end = min(p.C, c_begin + p.c_per_split);
         const T *a = (const T *)p.a + (TALL_A   ? (int64_t)c_begin * p.lda + m0
-                                       : GATHER ? (int64_t)c_begin
+                                       : GATHER ? (int64_t)p.rows[m0] * p.lda + c_begin
                                                 : (int64_t)m0 * p.lda + c_begin);
         const T *b = (const T *)p.b + (TALL_B ? (int64_t)c_begin * p.ldb + n0 : (int64_t)n0 * p.ldb + c_begin);
         const int64_t step_a = TALL_A ? BK * p.lda : BK, step_b = TALL_B ? BK * p.ldb : BK;

@@ -246,6 +246,22 @@ def test_upstream_gradients(dtype):
         assert err < 2.0 ** -9 * 1.1, err
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("masked", [0.0, 0.5, 0.99, 0.998, 1.0])
+def test_rows_far_apart(dtype, masked):
+    """8.6 GB of rows: fetched where they are, or, where a tile's lie past 32-bit offsets, packed first."""
+    M, K, V = 66000, 16, 300
+    t = inputs(M, K, V, dtype, 22, masked=masked)
+    x = torch.empty(M, 65536 * 2 // t["x"].element_size(), dtype=dtype, device=DEV)[:, :K]
+    x.copy_(t["x"])
+    near = check_all(**t)
+    t["x"] = x
+    for a, b in zip(check_all(**t, what="masked %.3f" % masked), near):
+        assert torch.equal(a, b)
+    for need in ((1, 0), (0, 1)):
+        check_all(**t, need_dx=bool(need[0]), need_dw=bool(need[1]))
+
+
 @pytest.mark.parametrize("M", [8, 200])
 def test_the_same_bits_again(M):
     t = inputs(M, 520, 1000, BF16, 16)
