@@ -352,7 +352,7 @@ __global__ __launch_bounds__(256) void apart_kernel(const int *index, const int 
 
 // Rows of x with a target to rows of whole 16 bytes, zeros behind them; dx of the
 // others to zero; and w to such rows where its own are not.  A wave a row, 64 chunks of
-// one where the rows are few, or several rows a wave where they are short.  8192 x 4096 bf16 with dloss x besides: 22 us (134 MB).
+// one where the rows are few, or several rows a wave where they are short.  8192 x 4096 bf16, dloss x only: 22 us (134 MB).
 struct PackParams {
     const void *from[2];  // x, w (null: as it is)
     void *to[2];          // null: only what follows is wanted
@@ -374,7 +374,8 @@ template <bool F32, int MODE> __global__ __launch_bounds__(256) void pack_kernel
     // SHORT: rows of no more chunks than lanes, 256 / lanes of them a workgroup
     const int lane = SHORT ? threadIdx.x & (p.lanes - 1) : threadIdx.x & 63;
     const int rows = SHORT ? 256 / p.lanes : 4;
-    const int64_t step = (int64_t)gridDim.x * rows, start = (int64_t)blockIdx.x * rows + (SHORT ? threadIdx.x / p.lanes : threadIdx.x >> 6);
+    const int64_t step = (int64_t)gridDim.x * rows;
+    const int64_t start = (int64_t)blockIdx.x * rows + (SHORT ? threadIdx.x / p.lanes : threadIdx.x >> 6);
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
         if (!p.from[g]) continue;
@@ -397,18 +398,7 @@ template <bool F32, int MODE> __global__ __launch_bounds__(256) void pack_kernel
             u32x4_t *to = whole ? (u32x4_t *)whole + at * p.chunks : nullptr;
             u32x4_t *scaled = g == 0 && p.scaled ? (u32x4_t *)p.scaled + at * p.chunks : nullptr;
             const float by = scaled && *p.most != 0.0f ? p.dloss[row] / *p.most : 0.0f;
-#pragma unroll 4
-            for (int c = first; c < end; c += 64) {
-                const int left = p.K - c * CE;
-                u32x4_t v;
-                if (left >= CE) {
-                    v = *(const typename El<F32>::chunk_any *)(from + c * CE);
-                } else {
-                    T x[CE];
-#pragma unroll
-                    for (int e = 0; e < CE; ++e) x[e] = e < left ? from[c * CE + e] : (T)0.0f;
-                    v = __builtin_bit_cast(u32x4_t, x);
-                }
+            auto put = [&](int c, u32x4_t v) {
                 if (to) to[c] = v;
                 if (scaled) {
                     float y[CE];
@@ -417,6 +407,15 @@ template <bool F32, int MODE> __global__ __launch_bounds__(256) void pack_kernel
                     for (int e = 0; e < CE; ++e) y[e] = by * r.get(e);
                     scaled[c] = __builtin_bit_cast(u32x4_t, Pack<F32, CE>::of(y).w[0]);
                 }
+            };
+            const int full = p.K / CE;  // chunks inside the row
+#pragma unroll 4
+            for (int c = first; c < min(end, full); c += 64) put(c, *(const typename El<F32>::chunk_any *)(from + c * CE));
+            if (full < end && full >= first && (full - first) % 64 == 0) {
+                T x[CE];
+#pragma unroll
+                for (int e = 0; e < CE; ++e) x[e] = full * CE + e < p.K ? from[full * CE + e] : (T)0.0f;
+                put(full, __builtin_bit_cast(u32x4_t, x));
             }
         }
     }
@@ -588,7 +587,7 @@ struct JoinParams {
     const float *sums;
     const int *count;
     int rows;     // rows of a row block of the sums
-    int columns;  // of db a workgroup
+    int columns;  // of db a workgroup: 2 to this power
     int N;
     void *db;
 };
@@ -603,17 +602,17 @@ template <bool F32> __global__ __launch_bounds__(256) void join_kernel(JoinParam
         return sum_splits<F32>(p.dx, block * 256 + threadIdx.x);
     }
     block -= p.blocks[1];
-    // `columns` of them, a power of two up to 64, by the other threads
-    const int c = threadIdx.x & (p.columns - 1), r = threadIdx.x / p.columns, lanes = 256 / p.columns;
-    const int n_sums = (count + p.rows - 1) / p.rows;
-    const int64_t n = block * p.columns + c;
+    // 2^`columns` of them, up to 64, by the other threads
+    const int columns = 1 << p.columns, c = threadIdx.x & (columns - 1), r = threadIdx.x >> p.columns;
+    const int lanes = 256 >> p.columns, n_sums = (count + p.rows - 1) / p.rows;
+    const int64_t n = (block << p.columns) + c;
     float s = 0.0f;
     if (n < p.N) {
 #pragma unroll 8
         for (int b = r; b < n_sums; b += lanes) s += p.sums[(int64_t)b * p.N + n];
     }
     part[threadIdx.x] = s;
-    for (int o = 128; o >= p.columns; o /= 2) {
+    for (int o = 128; o >= columns; o /= 2) {
         __syncthreads();
         if ((int)threadIdx.x < o) part[threadIdx.x] += part[threadIdx.x + o];
     }
@@ -967,8 +966,9 @@ int xent_bwd(const void *x, const void *w, const void *bias, const int64_t *targ
             j.sums = (float *)(ws + sp.sums), j.rows = wave_rows(pl), j.N = (int)N, j.db = (char *)db + v0 * eb;
             // few entries leave their lanes to the rows: 4 of them over 4 million rows 747 us with
             // 64 columns a workgroup
-            for (j.columns = 1; j.columns < N && j.columns < 64;) j.columns *= 2;
-            blocks += ceil_div(N, j.columns);
+            // (16 columns where there are more: 128 sums of each are then eight a thread)
+            for (j.columns = 0; (1 << j.columns) < N && j.columns < 4;) ++j.columns;
+            blocks += ceil_div(N, 1 << j.columns);
         }
         if (blocks == 0) continue;
         if (blocks > 0x7fffffff) return HYENA_ERR_UNSUPPORTED;
