@@ -15,12 +15,12 @@
 //     joins the tiles.
 //   * Backward, a piece of the vocabulary at a time: the logits again, with e = p -
 //     [target] as their epilogue (in bf16 rounded, as the matrix cores take it; db sums
-//     dloss e unrounded), then dw = c e^T (dloss / c x) of the piece and dx += e w in
-//     fp32, times dloss and rounded after the last piece; c is the largest |dloss|.
-//     dloss stays out of e, so that the -1 of a target, the largest part of a gradient
-//     where p is small, is exact; inside, its rounding would be that of whole rows, and
-//     with a mean's equal dloss one factor (to 0.4 % off) for all gradients.  Equal
-//     dloss leave x as it is, others round it once more.
+//     dloss e unrounded), then dx += e w in fp32, times dloss and rounded after the last
+//     piece, and dw = c e^T (dloss / c x), or c (dloss / c e)^T x where the entries are few;
+//     c is the largest |dloss|.  dloss stays out of dx's e, so that the -1 of a target,
+//     the largest part of a gradient where p is small, is exact; inside, its rounding
+//     would be that of whole rows, and with a mean's equal dloss one factor (to 0.4 %
+//     off) for all gradients.  Equal dloss leave dw's operands as they are.
 //   * No more than 16 rows forward: the weights stream once through rows_product.
 
 #include <initializer_list>
@@ -233,8 +233,9 @@ struct RankParams {
     int *rank, *index, *goal, *count;
     int *apart;                   // cleared, for apart_kernel; or null
     float *most;                  // backward: the largest |dloss| of them
+    int *alike;                   // backward: whether all of them are that
     int *counts;                  // of each workgroup's rows (more than one workgroup)
-    float *tops;                  // backward: the largest |dloss| there
+    float *tops;                  // backward: the largest |dloss| there, and the least dloss
     int64_t V;
     int M;
 };
@@ -254,31 +255,38 @@ template <class T, class F> __device__ inline T over_1024(T x, T *lds, F f) {
 }
 __device__ inline int add(int a, int b) { return a + b; }
 __device__ inline float larger(float a, float b) { return fmaxf(a, b); }
+__device__ inline float lesser(float a, float b) { return fminf(a, b); }
+// The largest |d| and the least d; a NaN is like no other.
+__device__ inline void bounds(float d, float &top, float &low) {
+    top = fmaxf(top, fabsf(d));
+    low = fminf(low, d == d ? d : -__builtin_inff());
+}
 
 __global__ __launch_bounds__(1024) void count_kernel(RankParams p) {
     __shared__ int sums[16];
-    __shared__ float tops[16];
+    __shared__ float tops[16], lows[16];
     int n = 0;
-    float top = 0.0f;
+    float top = 0.0f, low = __builtin_inff();
 #pragma unroll
     for (int k = 0; k < kRankRows / 1024; ++k) {
         const int64_t m = (int64_t)blockIdx.x * kRankRows + k * 1024 + threadIdx.x;
         const bool on = m < p.M && (uint64_t)p.target[m] < (uint64_t)p.V;
         n += on;
-        if (p.most && on) top = fmaxf(top, fabsf(p.dloss[m]));
+        if (p.most && on) bounds(p.dloss[m], top, low);
     }
     n = over_1024(n, sums, add);
     if (threadIdx.x == 0) p.counts[blockIdx.x] = n;
     if (!p.most) return;
     top = over_1024(top, tops, larger);
-    if (threadIdx.x == 0) p.tops[blockIdx.x] = top;
+    low = over_1024(low, lows, lesser);
+    if (threadIdx.x == 0) p.tops[2 * blockIdx.x] = top, p.tops[2 * blockIdx.x + 1] = low;
 }
 
 __global__ __launch_bounds__(1024) void rank_kernel(RankParams p) {
     __shared__ int ahead[128];  // rows in the waves before, of the workgroup's 8 times 16
     __shared__ int first_half, both, sums[16];
-    __shared__ float tops[16];
-    float top = 0.0f;
+    __shared__ float tops[16], lows[16];
+    float top = 0.0f, low = __builtin_inff();
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t first = (int64_t)blockIdx.x * kRankRows;
     int goal[8], before[8], base = 0;
@@ -294,14 +302,15 @@ __global__ __launch_bounds__(1024) void rank_kernel(RankParams p) {
         for (int i = threadIdx.x; i < (int)blockIdx.x; i += 1024) base += p.counts[i];
         base = over_1024(base, sums, add);
         if (blockIdx.x == 0 && p.most)
-            for (int i = threadIdx.x; i < (int)gridDim.x; i += 1024) top = fmaxf(top, p.tops[i]);
+            for (int i = threadIdx.x; i < (int)gridDim.x; i += 1024)
+                top = fmaxf(top, p.tops[2 * i]), low = fminf(low, p.tops[2 * i + 1]);
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
         const uint64_t on = __builtin_amdgcn_ballot_w64(goal[k] >= 0);
         before[k] = __popcll(on & (((uint64_t)1 << lane) - 1));
         if (lane == 0) ahead[k * 16 + wave] = __popcll(on);
-        if (gridDim.x == 1 && goal[k] >= 0 && p.most) top = fmaxf(top, fabsf(d[k]));
+        if (gridDim.x == 1 && goal[k] >= 0 && p.most) bounds(d[k], top, low);
     }
     __syncthreads();
     if (wave < 2) {  // running sums of the 128 counts, 64 a wave
@@ -338,7 +347,8 @@ __global__ __launch_bounds__(1024) void rank_kernel(RankParams p) {
     }
     if (!p.most || blockIdx.x != 0) return;
     top = over_1024(top, tops, larger);
-    if (threadIdx.x == 0) *p.most = top;
+    low = over_1024(low, lows, lesser);
+    if (threadIdx.x == 0) *p.most = top, *p.alike = low == top;
 }
 
 // Where x is 2 GiB or more, a tile's rows may lie further apart than its 32-bit offsets
@@ -361,6 +371,7 @@ struct PackParams {
     int64_t rows[2], ld[2];
     const int *rank;
     const int *apart;     // to[0] only where it says so, or null
+    const int *count;     // where all rows[0] have a target (and are not apart), nothing is copied; or null
     void *dx;
     int64_t lddx;
     int K, chunks, parts;
@@ -378,7 +389,7 @@ template <bool F32, int MODE> __global__ __launch_bounds__(256) void pack_kernel
     const int64_t start = (int64_t)blockIdx.x * rows + (SHORT ? threadIdx.x / p.lanes : threadIdx.x >> 6);
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-        if (!p.from[g]) continue;
+        if (!p.from[g] || (g == 0 && p.count && *p.count == p.rows[0] && !(p.apart && *p.apart))) continue;
         for (int64_t id = start; id < p.rows[g] * p.parts; id += step) {
             const int64_t row = PARTS ? id / p.parts : id;
             const int first = PARTS ? (int)(id - row * p.parts) * 64 + lane : lane;
@@ -392,7 +403,7 @@ template <bool F32, int MODE> __global__ __launch_bounds__(256) void pack_kernel
                 }
                 continue;
             }
-            void *const whole = g == 0 && p.apart && *p.apart == 0 ? nullptr : p.to[g];
+            void *const whole = g == 0 && p.apart && !p.count && *p.apart == 0 ? nullptr : p.to[g];
             if (!whole && !(g == 0 && p.scaled)) continue;  // only dx of the others
             const T *from = (const T *)p.from[g] + row * p.ld[g];
             u32x4_t *to = whole ? (u32x4_t *)whole + at * p.chunks : nullptr;
@@ -431,6 +442,9 @@ struct DzEpi {
     const float *lse, *dloss;   // packed
     const int *target;          // packed, of the whole vocabulary
     void *dz;                   // e: [rows][ld], ld whole 16 bytes, zeros behind the columns
+    void *scaled;               // the same times dloss / most, where not all dloss are alike; or null
+    const float *most;
+    const int *alike;
     float *sums;                // [row blocks][N] or null
     int64_t ld;
     int v0;                     // the piece's first entry
@@ -441,7 +455,7 @@ struct DzEpi {
         float sum[V];
     };
     struct Row {
-        float lse, dloss;
+        float lse, dloss, by;
         int target;
     };
     template <bool F32, int V> __device__ __forceinline__ Columns<F32, V> columns(int n) const {
@@ -449,7 +463,8 @@ struct DzEpi {
         return c;
     }
     template <bool F32, int V> __device__ __forceinline__ Row before(int64_t m, int) const {
-        return m < M ? Row{lse[m], dloss[m], target[m] - v0} : Row{};
+        if (m >= M) return Row{};
+        return Row{lse[m], dloss[m], scaled && *most != 0.0f ? dloss[m] / *most : 0.0f, target[m] - v0};
     }
     template <bool F32, int V>
     __device__ __forceinline__ void finish(int64_t m, int n, float (&z)[V], Columns<F32, V> &c, const Row &r) const {
@@ -461,6 +476,10 @@ struct DzEpi {
             c.sum[e] += r.dloss * z[e];
         }
         Pack<F32, V>::store(dz, m * ld + n, (int)(ld - n), z);
+        if (!scaled || *alike) return;
+#pragma unroll
+        for (int e = 0; e < V; ++e) z[e] *= r.by;
+        Pack<F32, V>::store(scaled, m * ld + n, (int)(ld - n), z);
     }
     template <bool F32, int V> __device__ __forceinline__ void close(const Columns<F32, V> &c, int m, int block, int n) const {
         if (!sums || m >= M) return;  // eight lanes a row, the wave's eight rows at a time
@@ -534,20 +553,34 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void dz_kernel(Gemm<DzEpi> p, cons
     run_tile<false, false, DIRECT, S, GATHER>(p, blockIdx.x, a0, a1, a2, a3, b0, b1, b2, b3);
 }
 
+// What dw is formed from where dloss is in e (see xent_bwd), as the rows turn out: e
+// itself or e times dloss, x in place or packed.
+struct DwFrom {
+    const void *scaled, *x;  // scaled null: as the product says
+    const int *alike, *apart;
+    int64_t ldx;
+    int M;
+};
+
 // dw's sum runs over the rows: their number, cut anew between the splits.
-template <bool F32> __device__ inline void sum_from(Gemm<DwEpi> &p, const int *count) {
+template <bool F32> __device__ inline void sum_from(Gemm<DwEpi> &p, const int *count, const DwFrom &f) {
     constexpr int BK = 8 * El<F32>::CE;
     p.C = *count;
+    if (f.scaled) {
+        if (!*f.alike) p.a = f.scaled;
+        if (p.C == f.M && !(f.apart && *f.apart)) p.b = f.x, p.ldb = f.ldx;
+    }
     const int steps = (p.C + BK - 1) / BK;
     p.c_per_split = max((steps + p.splits - 1) / p.splits, 1) * BK;
 }
 
 // The first `blocks` workgroups form dw, the others dx.
 template <bool F32, bool DIRECT, typename S>
-__global__ __launch_bounds__(S::NT, S::WAVES) void grads_kernel(Gemm<DwEpi> dw, Gemm<DxEpi> dx, int blocks, const int *count) {
+__global__ __launch_bounds__(S::NT, S::WAVES) void grads_kernel(Gemm<DwEpi> dw, Gemm<DxEpi> dx, int blocks, DwFrom from,
+                                                                const int *count) {
     TILE_BUFFERS(S)
     if ((int)blockIdx.x < blocks) {
-        sum_from<F32>(dw, count);
+        sum_from<F32>(dw, count, from);
         run_tile<true, true, DIRECT, S>(dw, blockIdx.x, a0, a1, a2, a3, b0, b1, b2, b3);
     } else {
         dx.M = dx.e.M = *count;
@@ -563,13 +596,13 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void grads_kernel(Gemm<DwEpi> dw, 
 // and dw's 1024 another 671.)
 template <typename S>
 __global__ __launch_bounds__(S::NT, S::WAVES) void large_grads_kernel(Gemm<DwEpi> dw, Gemm<DxEpi> dx, int lead, int dx_first,
-                                                                      const int *count) {
+                                                                      DwFrom from, const int *count) {
     TILE_BUFFERS(S)
     const bool in_lead = (int)blockIdx.x < lead;
     const int block = in_lead ? blockIdx.x : blockIdx.x - lead;
     if (in_lead != (dx_first != 0)) {
         if (block >= dw.tiles_m * dw.tiles_n * dw.splits) return;
-        sum_from<false>(dw, count);
+        sum_from<false>(dw, count, from);
         run_tile<true, true, true, S>(dw, block, a0, a1, a2, a3, b0, b1, b2, b3);
     } else {
         dx.M = dx.e.M = *count;
@@ -713,10 +746,10 @@ BwdSpace bwd_space(int64_t M, int64_t K, int64_t V, bool f32) {
         return at;
     };
     s.piece = piece_of(M, V, eb);
-    s.count = take(12), s.counts = take(rank_blocks(M) * 4), s.tops = take(rank_blocks(M) * 4);
+    s.count = take(16), s.counts = take(rank_blocks(M) * 4), s.tops = take(rank_blocks(M) * 8);
     s.rank = take(M * 4), s.index = take(M * 4), s.goal = take(M * 4);
     s.lse = take(M * 4), s.dloss = take(M * 4);
-    s.x = take(M * whole(K, eb) * eb), s.scaled = take(M * whole(K, eb) * eb);
+    s.x = take(M * whole(K, eb) * eb), s.scaled = take(M * whole(K, eb) * eb);  // x, or e of few entries
     s.w = take(whole(K, eb) != K ? V * whole(K, eb) * eb : 0);
     s.dz = take(M * whole(s.piece, eb) * eb);
     int64_t sums = 0, partial = 0;
@@ -873,11 +906,20 @@ int xent_bwd(const void *x, const void *w, const void *bias, const int64_t *targ
     r.counts = (int *)(ws + sp.counts), r.tops = (float *)(ws + sp.tops);
     const bool gather = gather_ok(x, ldx, K, eb, w);
     if (gather && !all_near(M, ldx, eb)) r.apart = r.count + 2;
+    r.alike = r.count + 3;
     if ((st = launch_rank(r, stream)) != HYENA_OK) return st;
     const int64_t ld = whole(K, eb);
+    // dw's dloss goes with e where the entries are few (x is then taken as it is where
+    // every row has a target: 8192 x 4096 bf16 with V = 512 150 against 169 us, V = 4 74
+    // against 98, though 148 against 141 with V = 512 and 0.3 of the rows masked), else
+    // with x, once for all pieces (V = 4096 694 either way).
+    const bool with_e = dw && gather && 2 * V <= K;
     PackParams k = {};
-    k.from[0] = x, k.to[0] = gather && !r.apart ? nullptr : ws + sp.x, k.apart = r.apart, k.rows[0] = M, k.ld[0] = ldx, k.rank = r.rank, k.dx = dx, k.lddx = lddx;
-    if (dw) k.scaled = ws + sp.scaled, k.dloss = dloss, k.most = r.most;
+    k.from[0] = x, k.rows[0] = M, k.ld[0] = ldx, k.rank = r.rank, k.dx = dx, k.lddx = lddx, k.apart = r.apart;
+    k.to[0] = gather && !r.apart && !with_e ? nullptr : ws + sp.x;
+    if (with_e) k.count = r.count;
+    else if (dw) k.scaled = ws + sp.scaled, k.dloss = dloss, k.most = r.most;
+    const DwFrom from = with_e ? DwFrom{ws + sp.scaled, x, r.alike, r.apart, ldx, (int)M} : DwFrom{};
     if (ld != K) k.from[1] = w, k.to[1] = ws + sp.w, k.rows[1] = V, k.ld[1] = K;
     k.K = (int)K, k.chunks = (int)(ld * eb / 16);
     if (r.apart && (st = launch_apart(r, ldx, eb, stream)) != HYENA_OK) return st;
@@ -893,6 +935,7 @@ int xent_bwd(const void *x, const void *w, const void *bias, const int64_t *targ
         DzEpi e = {};
         e.bias = bias ? (const char *)bias + v0 * eb : nullptr, e.lse = r.lse_out, e.dloss = r.dloss_out, e.target = r.goal;
         e.dz = ws + sp.dz, e.ld = ldz, e.sums = db ? (float *)(ws + sp.sums) : nullptr, e.v0 = (int)v0;
+        if (with_e) e.scaled = ws + sp.scaled, e.most = r.most, e.alike = r.alike;
         for (const bool here : {true, false}) {  // as in the forward
             if (M == 0 || (here ? !gather : gather && !r.apart)) continue;
             char *none = nullptr;
@@ -921,7 +964,7 @@ int xent_bwd(const void *x, const void *w, const void *bias, const int64_t *targ
             if (dw) {
                 DwEpi o = {};
                 o.y = (char *)dw + v0 * K * eb, o.ldy = K, o.scale = r.most;
-                j.dw = gemm_params(gp, g, sz[g], e.dz, ldz, k.scaled, ld, o, at);
+                j.dw = gemm_params(gp, g, sz[g], e.dz, ldz, with_e ? k.to[0] : k.scaled, ld, o, at);
                 if (j.dw.partial) j.blocks[0] = ceil_div(N * ceil_div(K, 4), 256);
                 ++g;
             }
@@ -941,12 +984,12 @@ int xent_bwd(const void *x, const void *w, const void *bias, const int64_t *targ
                     const int64_t n_dw = dw ? gp.blocks[0] : 0, n_dx = blocks - n_dw;
                     const int64_t lead = ceil_div(dx_first ? n_dx : n_dw, 8) * 8;
                     hipLaunchKernelGGL((large_grads_kernel<Large>), dim3((unsigned)(lead + (dx_first ? n_dw : n_dx))),
-                                       dim3(Large::NT), 0, stream, j.dw, j.dx, (int)lead, (int)dx_first, r.count);
+                                       dim3(Large::NT), 0, stream, j.dw, j.dx, (int)lead, (int)dx_first, from, r.count);
                 }
             } else {
 #define GRADS(DIRECT, S)                                                                                                \
     hipLaunchKernelGGL((grads_kernel<F32, DIRECT, S>), dim3((unsigned)blocks), dim3(S::NT), 0, stream, j.dw, j.dx, first, \
-                       r.count);
+                       from, r.count);
                 switch (tile_of(gp)) {
                 case kDeep: GRADS(true, Deep<F32>) break;
                 case kFineDeep: if constexpr (!F32) { GRADS(true, FineDeep) } break;

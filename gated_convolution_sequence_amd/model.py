@@ -264,8 +264,8 @@ def xent_bwd(x: torch.Tensor, w: torch.Tensor, target: torch.Tensor, lse: torch.
     lse is the forward's.  Rows without a target get a gradient of 0 and add
     nothing to dw and db, whatever their x holds.  Parts not requested are None; db also
     where bias is None.  ``dx`` may be given to be written to.  In bf16
-    softmax - [target] and, for dw, dloss x are rounded to bf16 before their products, as the matrix
-    cores take them; db sums unrounded values.
+    softmax - [target], for dw with dloss in it or in x, is rounded to bf16 before its products, as the
+    matrix cores take it; db sums unrounded values.
     """
     code, M, K, V, ldx = _xent_inputs(x, w, target, bias)
     dev, dt = x.device, x.dtype

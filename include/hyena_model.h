@@ -86,10 +86,11 @@ int hyena_xent_fwd(const void *x, const void *w, const void *bias,
  *     dz_iv = dloss_i (exp(z_iv - lse_i) - [v = target_i]),
  *     dx = dz w,  dw = dz^T x,  db = sum_i dz_i
  * dx [M, K] has row stride lddx; dw [V, K], db [V] contiguous; all in `dtype`.
- * Any output may be NULL, not all.  bf16: softmax - [target] and, for dw, dloss x
- * (over the largest |dloss|) are rounded once each to bf16, as operands of the products; db sums unrounded
- * values; sums are fp32, outputs rounded once.  (In dw, a dloss below 2^-126 of the
- * largest counts as 0.)  A row whose lse is not finite has gradients of NaN. */
+ * Any output may be NULL, not all.  bf16: softmax - [target] (with dloss, or else x
+ * with dloss, for dw) is rounded to bf16 as operand of the products, dloss being over
+ * the largest |dloss|; db sums unrounded values; sums are fp32, outputs rounded once.
+ * (In dw, a dloss below 2^-126 of the largest counts as 0.)  A row whose lse is not
+ * finite has gradients of NaN. */
 int hyena_xent_bwd(const void *x, const void *w, const void *bias,
                    const int64_t *target, const float *lse, const float *dloss,
                    int64_t M, int64_t K, int64_t V, int64_t ldx, int64_t lddx,

@@ -260,6 +260,28 @@ def test_rows_far_apart(dtype, masked):
         assert torch.equal(a, b)
     for need in ((1, 0), (0, 1)):
         check_all(**t, need_dx=bool(need[0]), need_dw=bool(need[1]))
+    t = {**inputs(M, K, 7, dtype, 24, masked=masked), "x": x}  # no more entries than columns
+    x.copy_(inputs(M, K, 7, dtype, 24)["x"])
+    check_all(**t, what="few entries")
+
+
+@pytest.mark.parametrize("M,K,V", [(300, 64, 31), (300, 64, 500), (20000, 72, 9), (5000, 1024, 512)])
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("masked", [0.0, 0.3])
+def test_dloss_alike_or_not(M, K, V, dtype, masked):
+    """dw from e or from e dloss, with x in place or packed: dloss alike, of one sign, of both, all negative, NaN, 0."""
+    t = inputs(M, K, V, dtype, 23, masked=masked)
+    own = t["dloss"].clone()
+    for what, d in (("own", own), ("alike", torch.full_like(own, 0.3)), ("negative", torch.full_like(own, -0.3)),
+                    ("signs", torch.where(own > own.mean(), 0.3, -0.3)), ("zero", torch.zeros_like(own))):
+        check_all(**{**t, "dloss": d}, what=what)
+    rows = torch.nonzero((t["target"] >= 0) & (t["target"] < V))[:, 0]
+    d = torch.full_like(own, 0.3)
+    d[rows[len(rows) // 2]] = math.nan
+    loss, lse = hc.xent_fwd(t["x"], t["w"], t["target"], bias=t["bias"])
+    dx, dw, db = hc.xent_bwd(t["x"], t["w"], t["target"], lse, d, bias=t["bias"])
+    assert torch.isnan(dw).all() and torch.isnan(db).all() and torch.isnan(dx[rows[len(rows) // 2]]).all()
+    assert torch.isfinite(dx[rows[:len(rows) // 2]]).all()
 
 
 @pytest.mark.parametrize("M", [8, 200])
