@@ -6,8 +6,8 @@
 // T lanes (a wave, a workgroup of 4 waves or one of 16, by the row's length), 16 bytes
 // a lane and chunk, so that mean, deviations and output come from one read; the
 // workgroups walk the rows with the next one's loads in flight, past the caches.
-// 8192 x 4096 bf16: forward 24.3 us (134 MB, 5.5 TB/s; at 32768 rows 5.9), backward
-// 45 us (201 MB, 4.5 TB/s; of it 4 to 5 us the launch that adds the workgroups' sums
+// 8192 x 4096 bf16: forward 23.5 us (134 MB, 5.7 TB/s; at 32768 rows 5.9), backward
+// 43 us (201 MB, 4.7 TB/s; of it 4 to 5 us the launch that adds the workgroups' sums
 // for dw and db; at 32768 rows 5.4).  Without the streaming accesses and the loads
 // ahead the forward took 28.5 us.
 

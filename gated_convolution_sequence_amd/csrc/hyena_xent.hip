@@ -420,8 +420,17 @@ template <bool F32, int MODE> __global__ __launch_bounds__(256) void pack_kernel
                 }
             };
             const int full = p.K / CE;  // chunks inside the row
-#pragma unroll 4
-            for (int c = first; c < min(end, full); c += 64) put(c, *(const typename El<F32>::chunk_any *)(from + c * CE));
+            const int stop = min(end, full);
+            constexpr int U = MODE == kPackRow ? 4 : 1;  // loads ahead of the stores
+            for (int c = first; c < stop; c += 64 * U) {
+                u32x4_t v[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (c + 64 * u < stop) v[u] = *(const typename El<F32>::chunk_any *)(from + (c + 64 * u) * CE);
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (c + 64 * u < stop) put(c + 64 * u, v[u]);
+            }
             if (full < end && full >= first && (full - first) % 64 == 0) {
                 T x[CE];
 #pragma unroll
