@@ -108,7 +108,7 @@ def test_many_tensors(bits):
 
 
 def test_a_tensor_past_32_bits():
-    """A seventh more than 2^32 elements in 8 bits: the index's high half takes part in the rounding (57 GB)."""
+    """An eighth more than 2^32 elements in 8 bits: the index's high half takes part in the rounding (29 GB)."""
     n = (1 << 32) + (1 << 29) + 77
     t = dict(params=[torch.zeros(n, dtype=BF16, device=DEV)], grads=[torch.full((n,), 0.5, dtype=BF16, device=DEV)],
              exp_avgs=[torch.zeros(n, dtype=torch.uint8, device=DEV).view(F8)],
