@@ -142,8 +142,7 @@ template <class S, class E> __device__ inline bool rows_from(Gemm<E> &p, const i
 }
 
 // The forward's logits.  8192 x 4096 x 65536 bf16 3.2 to 3.4 ms (1.29 to 1.37 PFLOP/s),
-// bound as layer_gemm.h's products are; the maxima and exponentials of a tile are about
-// 2 of its 110 us.
+// bound as layer_gemm.h's products are.
 template <bool F32, bool DIRECT, bool GATHER, typename S>
 __global__ __launch_bounds__(S::NT, S::WAVES) void stats_kernel(Gemm<StatsEpi> p, const int *count, const int *apart) {
     TILE_BUFFERS(S)
