@@ -90,7 +90,8 @@ int hyena_xent_fwd(const void *x, const void *w, const void *bias,
  * with dloss, for dw) is rounded to bf16 as operand of the products, dloss being over
  * the largest |dloss|; db sums unrounded values; sums are fp32, outputs rounded once.
  * (In dw, a dloss below 2^-126 of the largest counts as 0.)  A row whose lse is not
- * finite has gradients of NaN. */
+ * finite has gradients of NaN.  Where the dloss of a row with a target is not finite, neither
+ * is any element of dw and db (NaN for a NaN), nor that row of dx. */
 int hyena_xent_bwd(const void *x, const void *w, const void *bias,
                    const int64_t *target, const float *lse, const float *dloss,
                    int64_t M, int64_t K, int64_t V, int64_t ldx, int64_t lddx,
