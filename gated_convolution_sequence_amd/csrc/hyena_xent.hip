@@ -237,7 +237,7 @@ struct RankParams {
     float *loss, *lse;            // forward: zeroed where there is no target
     int *rank, *index, *goal, *count;
     int *apart;                   // cleared, for apart_kernel; or null
-    float *most;                  // backward: the largest |dloss| of them (NaN where one is)
+    float *most;                  // backward: the largest |dloss| of them (NaN where one is NaN or -inf)
     int *alike;                   // backward: whether all of them are that
     int *counts;                  // of each workgroup's rows (more than one workgroup)
     float *tops;                  // backward: the largest |dloss| there, and the least dloss
@@ -259,13 +259,11 @@ template <class T, class F> __device__ inline T over_1024(T x, T *lds, F f) {
     return x;
 }
 __device__ inline int add(int a, int b) { return a + b; }
-// A NaN is the largest of all, so that it reaches what is scaled by the largest (fmaxf would
-// drop it, and dw be 0 where every other dloss is 0).
-__device__ inline float larger(float a, float b) { return a >= b || a != a ? a : b; }
+__device__ inline float larger(float a, float b) { return fmaxf(a, b); }
 __device__ inline float lesser(float a, float b) { return fminf(a, b); }
-// The largest |d| and the least d; a NaN is like no other.
+// The largest |d| but for NaN, and the least d, with -inf for a NaN.
 __device__ inline void bounds(float d, float &top, float &low) {
-    top = larger(top, fabsf(d));
+    top = fmaxf(top, fabsf(d));
     low = fminf(low, d == d ? d : -__builtin_inff());
 }
 
@@ -310,7 +308,7 @@ __global__ __launch_bounds__(1024) void rank_kernel(RankParams p) {
         base = over_1024(base, sums, add);
         if (blockIdx.x == 0 && p.most)
             for (int i = threadIdx.x; i < (int)gridDim.x; i += 1024)
-                top = larger(top, p.tops[2 * i]), low = lesser(low, p.tops[2 * i + 1]);
+                top = fmaxf(top, p.tops[2 * i]), low = fminf(low, p.tops[2 * i + 1]);
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -355,7 +353,9 @@ __global__ __launch_bounds__(1024) void rank_kernel(RankParams p) {
     if (!p.most || blockIdx.x != 0) return;
     top = over_1024(top, tops, larger);
     low = over_1024(low, lows, lesser);
-    if (threadIdx.x == 0) *p.most = top, *p.alike = low == top;
+    // a NaN, of which only `low` tells, has to reach what `most` scales: with the others 0,
+    // their largest would leave a dw of 0
+    if (threadIdx.x == 0) *p.most = low == -__builtin_inff() ? __builtin_nanf("") : top, *p.alike = low == top;
 }
 
 // Where x is 2 GiB or more, a tile's rows may lie further apart than its 32-bit offsets
