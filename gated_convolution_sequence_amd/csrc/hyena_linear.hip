@@ -153,7 +153,7 @@ template <bool F32> __global__ __launch_bounds__(256) void finish_kernel(FinishP
 template <bool F32, int MT>
 __global__ __launch_bounds__(64 * kRowWaves) void rows_kernel(RowsParams<Epilogue> p) {
     __shared__ __attribute__((aligned(16))) float sums[kRowWaves][MT][16][16];
-    rows_product<F32, MT>(p, sums);
+    rows_product<F32, MT>(p, blockIdx.x, sums);
 }
 
 // ---- dz, db and padded rows ------------------------------------------------------------

@@ -133,12 +133,13 @@ struct StatsEpi {
     }
 };
 
-// The rows of `count` take the place of the upper bound that the host planned with.
-template <class S, class E> __device__ inline bool rows_from(Gemm<E> &p, const int *count) {
+// The rows of `count` take the place of the upper bound that the host planned with.  Whether
+// there is a tile for workgroup `block`.
+template <class S, class E> __device__ inline bool rows_from(Gemm<E> &p, const int *count, int block) {
     p.M = *count;
     p.e.M = p.M;
     p.tiles_m = (p.M + S::BM - 1) / S::BM;
-    return (int)blockIdx.x < p.tiles_m * p.tiles_n * p.splits;
+    return block < p.tiles_m * p.tiles_n * p.splits;
 }
 
 // The forward's logits.  8192 x 4096 x 65536 bf16 3.2 to 3.4 ms (1.29 to 1.37 PFLOP/s),
@@ -146,8 +147,9 @@ template <class S, class E> __device__ inline bool rows_from(Gemm<E> &p, const i
 template <bool F32, bool DIRECT, bool GATHER, typename S>
 __global__ __launch_bounds__(S::NT, S::WAVES) void stats_kernel(Gemm<StatsEpi> p, const int *count, const int *apart) {
     TILE_BUFFERS(S)
-    if ((apart && (*apart != 0) == GATHER) || !rows_from<S>(p, count)) return;
-    run_tile<false, false, DIRECT, S, GATHER>(p, blockIdx.x, a0, a1, a2, a3, b0, b1, b2, b3);
+    const int block = block_of();
+    if ((apart && (*apart != 0) == GATHER) || !rows_from<S>(p, count, block)) return;
+    run_tile<false, false, DIRECT, S, GATHER>(p, block, a0, a1, a2, a3, b0, b1, b2, b3);
 }
 
 // Few rows: 16 columns a workgroup; columns of four lanes a row.  Bound by the weights:
@@ -186,7 +188,9 @@ struct RowStats {
 };
 template <bool F32> __global__ __launch_bounds__(64 * kRowWaves) void rows_stats_kernel(RowsParams<RowStats> p) {
     __shared__ __attribute__((aligned(16))) float sums[kRowWaves][1][16][16];
-    rows_product<F32, 1>(p, sums);
+    const int block = block_of();
+    if ((int64_t)block * 16 >= p.N) return;
+    rows_product<F32, 1>(p, block, sums);
 }
 
 // Loss and lse of each row from its tiles, by SLICES lanes a row: 8192 rows of 256
@@ -205,7 +209,7 @@ template <int SLICES> __global__ __launch_bounds__(256) void merge_kernel(MergeP
     constexpr int ROWS = 256 / SLICES;
     __shared__ Part meet[SLICES][ROWS];
     const int row = threadIdx.x % ROWS, slice = threadIdx.x / ROWS;
-    const int m = blockIdx.x * ROWS + row, rows = p.count ? *p.count : p.M;
+    const int64_t m = (int64_t)block_of() * ROWS + row, rows = p.count ? *p.count : p.M;
     Part r = {-__builtin_inff(), 0.0f};
     if (m < rows) {
 #pragma unroll 4
@@ -566,8 +570,9 @@ using DxEpi = GradEpi<true>;
 template <bool F32, bool DIRECT, bool GATHER, typename S>
 __global__ __launch_bounds__(S::NT, S::WAVES) void dz_kernel(Gemm<DzEpi> p, const int *count, const int *apart) {
     TILE_BUFFERS(S)
-    if ((apart && (*apart != 0) == GATHER) || !rows_from<S>(p, count)) return;
-    run_tile<false, false, DIRECT, S, GATHER>(p, blockIdx.x, a0, a1, a2, a3, b0, b1, b2, b3);
+    const int block = block_of();
+    if ((apart && (*apart != 0) == GATHER) || !rows_from<S>(p, count, block)) return;
+    run_tile<false, false, DIRECT, S, GATHER>(p, block, a0, a1, a2, a3, b0, b1, b2, b3);
 }
 
 // What dw is formed from where dloss is in e (see xent_bwd), as the rows turn out: e
@@ -596,13 +601,14 @@ template <bool F32, bool DIRECT, typename S>
 __global__ __launch_bounds__(S::NT, S::WAVES) void grads_kernel(Gemm<DwEpi> dw, Gemm<DxEpi> dx, int blocks, DwFrom from,
                                                                 const int *count) {
     TILE_BUFFERS(S)
-    if ((int)blockIdx.x < blocks) {
+    const int id = block_of();
+    if (id < blocks) {
         sum_from<F32>(dw, count, from);
-        run_tile<true, true, DIRECT, S>(dw, blockIdx.x, a0, a1, a2, a3, b0, b1, b2, b3);
+        run_tile<true, true, DIRECT, S>(dw, id, a0, a1, a2, a3, b0, b1, b2, b3);
     } else {
         dx.M = dx.e.M = *count;
         dx.tiles_m = (dx.M + S::BM - 1) / S::BM;
-        const int block = blockIdx.x - blocks;
+        const int block = id - blocks;
         if (block >= dx.tiles_m * dx.tiles_n * dx.splits) return;
         run_tile<false, true, DIRECT, S>(dx, block, a0, a1, a2, a3, b0, b1, b2, b3);
     }
@@ -615,8 +621,9 @@ template <typename S>
 __global__ __launch_bounds__(S::NT, S::WAVES) void large_grads_kernel(Gemm<DwEpi> dw, Gemm<DxEpi> dx, int lead, int dx_first,
                                                                       DwFrom from, const int *count) {
     TILE_BUFFERS(S)
-    const bool in_lead = (int)blockIdx.x < lead;
-    const int block = in_lead ? blockIdx.x : blockIdx.x - lead;
+    const int id = block_of();
+    const bool in_lead = id < lead;
+    const int block = in_lead ? id : id - lead;
     if (in_lead != (dx_first != 0)) {
         if (block >= dw.tiles_m * dw.tiles_n * dw.splits) return;
         sum_from<false>(dw, count, from);
@@ -861,7 +868,7 @@ int xent_fwd(const void *x, const void *w, const void *bias, const int64_t *targ
         p.e.bias = bias, p.e.target = target, p.e.part = (Part *)(ws + sp.part), p.e.at = (float *)(ws + sp.at);
         mp.tiles = (int)ceil_div(V, 16), mp.target = target, mp.tile = 1, mp.row = mp.tiles;
         p.e.ldp = mp.tiles, p.e.M = p.M, p.e.N = p.N;
-        hipLaunchKernelGGL(rows_stats_kernel<F32>, dim3((unsigned)mp.tiles), dim3(64 * kRowWaves), 0, stream, p);
+        hipLaunchKernelGGL(rows_stats_kernel<F32>, grid_of(mp.tiles), dim3(64 * kRowWaves), 0, stream, p);
         if ((st = launch_status()) != HYENA_OK) return st;
     } else {
         RankParams r = {};
@@ -882,7 +889,6 @@ int xent_fwd(const void *x, const void *w, const void *bias, const int64_t *targ
         }
         const bool direct = gather || k.from[1] || direct_ok(w, K, K, eb);
         const Plan pl = whole_plan(M, V, K, F32, direct);
-        if (pl.blocks[0] > 0x7fffffff) return HYENA_ERR_UNSUPPORTED;
         StatsEpi e = {};
         e.bias = bias, e.target = r.goal, e.part = (Part *)(ws + sp.part), e.at = (float *)(ws + sp.at), e.ldp = M;
         // of rows in place, of packed rows, or of whichever apart_kernel found
@@ -893,8 +899,8 @@ int xent_fwd(const void *x, const void *w, const void *bias, const int64_t *targ
                                            k.from[1] ? k.to[1] : w, k.from[1] ? ld : K, e, none);
             p.rows = r.index;
 #define STATS(DIRECT, GATHER, S)                                                                                       \
-    hipLaunchKernelGGL((stats_kernel<F32, DIRECT, GATHER, S>), dim3((unsigned)pl.blocks[0]), dim3(S::NT), 0, stream, p, \
-                       r.count, r.apart);
+    hipLaunchKernelGGL((stats_kernel<F32, DIRECT, GATHER, S>), grid_of(pl.blocks[0]), dim3(S::NT), 0, stream, p, r.count, \
+                       r.apart);
             FOR_TILE(pl, direct, here, STATS)
 #undef STATS
             if ((st = launch_status()) != HYENA_OK) return st;
@@ -904,7 +910,7 @@ int xent_fwd(const void *x, const void *w, const void *bias, const int64_t *targ
     // a workgroup a row for few rows, whose tiles are many: 59 us at 8 rows of 4096 tiles
     // with eight lanes a row, 5 with 256
     if (M <= 256) hipLaunchKernelGGL(merge_kernel<256>, dim3((unsigned)M), dim3(256), 0, stream, mp);
-    else hipLaunchKernelGGL(merge_kernel<8>, dim3((unsigned)ceil_div(M, 32)), dim3(256), 0, stream, mp);
+    else hipLaunchKernelGGL(merge_kernel<8>, grid_of(ceil_div(M, 32)), dim3(256), 0, stream, mp);
     return launch_status();
 }
 
@@ -948,7 +954,6 @@ int xent_bwd(const void *x, const void *w, const void *bias, const int64_t *targ
         const int64_t N = V - v0 < sp.piece ? V - v0 : sp.piece, ldz = whole(N, eb);
         const char *wv = wp + v0 * ldw * eb;
         const Plan pl = whole_plan(M, N, K, F32, direct);
-        if (pl.blocks[0] > 0x7fffffff) return HYENA_ERR_UNSUPPORTED;
         DzEpi e = {};
         e.bias = bias ? (const char *)bias + v0 * eb : nullptr, e.lse = r.lse_out, e.dloss = r.dloss_out, e.target = r.goal;
         e.dz = ws + sp.dz, e.ld = ldz, e.sums = db ? (float *)(ws + sp.sums) : nullptr, e.v0 = (int)v0;
@@ -959,8 +964,8 @@ int xent_bwd(const void *x, const void *w, const void *bias, const int64_t *targ
             Gemm<DzEpi> p = gemm_params(pl, 0, Size{M, N, K}, here ? x : k.to[0], here ? ldx : ld, wv, ldw, e, none);
             p.rows = r.index;
 #define DZ(DIRECT, GATHER, S)                                                                                       \
-    hipLaunchKernelGGL((dz_kernel<F32, DIRECT, GATHER, S>), dim3((unsigned)pl.blocks[0]), dim3(S::NT), 0, stream, p, \
-                       r.count, r.apart);
+    hipLaunchKernelGGL((dz_kernel<F32, DIRECT, GATHER, S>), grid_of(pl.blocks[0]), dim3(S::NT), 0, stream, p, r.count, \
+                       r.apart);
             FOR_TILE(pl, direct, here, DZ)
 #undef DZ
             if ((st = launch_status()) != HYENA_OK) return st;
@@ -975,7 +980,6 @@ int xent_bwd(const void *x, const void *w, const void *bias, const int64_t *targ
             if (dx) sz[n++] = Size{M, K, N};
             const Plan gp = plan_of(sz, n, F32, direct);
             const int64_t blocks = gp.blocks[0] + gp.blocks[1];
-            if (blocks > 0x7fffffff) return HYENA_ERR_UNSUPPORTED;
             char *at = ws + sp.partial;
             int g = 0;
             if (dw) {
@@ -1000,13 +1004,13 @@ int xent_bwd(const void *x, const void *w, const void *bias, const int64_t *targ
                     const bool dx_first = N >= M;
                     const int64_t n_dw = dw ? gp.blocks[0] : 0, n_dx = blocks - n_dw;
                     const int64_t lead = ceil_div(dx_first ? n_dx : n_dw, 8) * 8;
-                    hipLaunchKernelGGL((large_grads_kernel<Large>), dim3((unsigned)(lead + (dx_first ? n_dw : n_dx))),
+                    hipLaunchKernelGGL((large_grads_kernel<Large>), grid_of(lead + (dx_first ? n_dw : n_dx)),
                                        dim3(Large::NT), 0, stream, j.dw, j.dx, (int)lead, (int)dx_first, from, r.count);
                 }
             } else {
 #define GRADS(DIRECT, S)                                                                                                \
-    hipLaunchKernelGGL((grads_kernel<F32, DIRECT, S>), dim3((unsigned)blocks), dim3(S::NT), 0, stream, j.dw, j.dx, first, \
-                       from, r.count);
+    hipLaunchKernelGGL((grads_kernel<F32, DIRECT, S>), grid_of(blocks), dim3(S::NT), 0, stream, j.dw, j.dx, first, from, \
+                       r.count);
                 switch (tile_of(gp)) {
                 case kDeep: GRADS(true, Deep<F32>) break;
                 case kFineDeep: if constexpr (!F32) { GRADS(true, FineDeep) } break;
@@ -1031,7 +1035,6 @@ int xent_bwd(const void *x, const void *w, const void *bias, const int64_t *targ
             blocks += ceil_div(N, 1 << j.columns);
         }
         if (blocks == 0) continue;
-        if (blocks > 0x7fffffff) return HYENA_ERR_UNSUPPORTED;
         hipLaunchKernelGGL(join_kernel<F32>, dim3((unsigned)blocks), dim3(256), 0, stream, j);
         if ((st = launch_status()) != HYENA_OK) return st;
     }
@@ -1045,6 +1048,11 @@ int check_xent(int64_t M, int64_t K, int64_t V, int dtype) {
     const int64_t most = ((int64_t)1 << 31) - 1024;  // tile coordinates are 32 bits
     if (M > most || V > most) return HYENA_ERR_SHAPE;
     if (K >= (int64_t)1 << 20) return HYENA_ERR_UNSUPPORTED;  // byte offsets inside a tile are 32 bits
+    // tiles are numbered in 31 bits (grid_of): of whole_plan's and plan_of's least edge where they are
+    // many, and some hundred of them may be cut into splits
+    const int64_t edge = dtype == HYENA_DTYPE_F32 ? 64 : 128, tiles = ((int64_t)1 << 31) - ((int64_t)1 << 22);
+    const int64_t m = ceil_div(M, edge), k = ceil_div(K, edge), v = ceil_div(V, edge);
+    if (m * v > tiles || m * k + k * v > tiles) return HYENA_ERR_UNSUPPORTED;
     return HYENA_OK;
 }
 

@@ -40,6 +40,10 @@ template <bool F32> __device__ inline void store1(void *p, size_t i, float x) {
     else ((bf16_t *)p)[i] = (bf16_t)x;
 }
 
+// A workgroup's number in a grid of grid_of (those past the number asked for have to exit).
+constexpr int64_t kGridRow = (int64_t)1 << 21;
+__device__ inline int block_of() { return (int)blockIdx.y * (int)kGridRow + (int)blockIdx.x; }
+
 // Whether any lane of the wave says so.
 __device__ inline bool any_lane(bool x) { return __builtin_amdgcn_ballot_w64(x) != 0; }
 
@@ -153,6 +157,14 @@ inline bool mul_fits(int64_t a, int64_t b, int64_t c, int64_t *out) {
 
 inline bool aligned(const void *p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 __host__ __device__ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// The grid of `blocks` workgroups, at most 2^31 - 2^21.  HIP takes fewer than 2^32 work-items
+// along x, so that more than 2^21 workgroups (2^31 items, of 1024 threads) lie in rows of that many.
+// (Rows of a length that has to be read from the launch's arguments cost a small product 1 %.)
+inline dim3 grid_of(int64_t blocks) {
+    return blocks <= kGridRow ? dim3((unsigned)blocks) : dim3((unsigned)kGridRow, (unsigned)ceil_div(blocks, kGridRow));
+}
+
 inline int launch_status() { return hipGetLastError() == hipSuccess ? HYENA_OK : HYENA_ERR_LAUNCH; }
 
 }  // namespace layer

@@ -571,13 +571,13 @@ constexpr int kRowWaves = 8;
 constexpr int kRowSteps = 2;  // steps of c in flight a wave
 
 template <bool F32, int MT, class E>
-__device__ __forceinline__ void rows_product(const RowsParams<E> &p, float (&sums)[kRowWaves][MT][16][16]) {
+__device__ __forceinline__ void rows_product(const RowsParams<E> &p, int block, float (&sums)[kRowWaves][MT][16][16]) {
     using T = typename El<F32>::type;
     using frag = typename El<F32>::frag;
     using chunk_any = typename El<F32>::chunk_any;
     constexpr int CE = El<F32>::CE, BK = 8 * CE;
     const int wave = threadIdx.x >> 6, i = threadIdx.x & 15, j = (threadIdx.x >> 4) & 3;
-    const int n0 = blockIdx.x * 16;
+    const int n0 = block * 16;
     const T *w = (const T *)p.w + (int64_t)(n0 + i) * p.K + j * CE;
     const T *x[MT];
 #pragma unroll
