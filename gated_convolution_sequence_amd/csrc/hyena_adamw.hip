@@ -35,14 +35,14 @@ struct Table {
     Entry t[kTensors];
     uint32_t first[kTensors];  // each tensor's first workgroup
     uint32_t place[kTensors];  // its place in the list
-    int n;
+    int n, blocks;             // tensors, workgroups of all of them
     int span;                  // elements a workgroup, whole turns
 };
 
 // The tensor of a workgroup, and the workgroup's place in it.
-__device__ inline int find(const Table &p, uint32_t block) {
+__device__ inline int find(const Table &p, int block) {
     const int lane = threadIdx.x & 63;
-    const uint64_t at = __builtin_amdgcn_ballot_w64(lane < p.n && p.first[lane] <= block);
+    const uint64_t at = __builtin_amdgcn_ballot_w64(lane < p.n && p.first[lane] <= (uint32_t)block);
     return __builtin_amdgcn_readfirstlane(__popcll(at) - 1);
 }
 
@@ -83,12 +83,12 @@ struct Work {
     int64_t begin, end;
     bool skip;
 };
-__device__ __forceinline__ Work work_of(const Table &p, const AdamParams &a) {
+__device__ __forceinline__ Work work_of(const Table &p, const AdamParams &a, int block) {
     __shared__ Factors shared;
     Work w;
-    const int i = find(p, blockIdx.x);
+    const int i = find(p, block);
     w.t = p.t[i];
-    w.begin = (int64_t)(blockIdx.x - p.first[i]) * p.span, w.end = min(w.t.numel, w.begin + p.span);
+    w.begin = (int64_t)((uint32_t)block - p.first[i]) * p.span, w.end = min(w.t.numel, w.begin + p.span);
     w.f = a.given;
     if (a.lr_dev || a.step_dev) {
         if (threadIdx.x == 0) shared = a.factors(a.lr_dev ? (double)*a.lr_dev : a.lr, a.step_dev ? *a.step_dev : a.step);
@@ -166,7 +166,9 @@ template <bool F32, bool WHOLE> __device__ __forceinline__ void step32(const Wor
     }
 }
 template <bool F32> __global__ __launch_bounds__(256) void adamw_kernel(Table p, AdamParams a) {
-    const Work k = work_of(p, a);
+    const int block = block_of();
+    if (block >= p.blocks) return;
+    const Work k = work_of(p, a, block);
     if (k.skip) return;
     int64_t at = k.begin;
     for (; at + kTurn <= k.end; at += kTurn) step32<F32, true>(k, at);
@@ -291,7 +293,9 @@ template <bool F32, bool WHOLE> __device__ __forceinline__ void step8(const Work
     if ((threadIdx.x & 31) == 0) k.t.m_scale[block] = sm, k.t.v_scale[block] = sv;
 }
 template <bool F32> __global__ __launch_bounds__(256) void adamw8_kernel(Table p, AdamParams a) {
-    const Work k = work_of(p, a);
+    const int block = block_of();
+    if (block >= p.blocks) return;
+    const Work k = work_of(p, a, block);
     if (k.skip) return;
     const int64_t e = k.begin + threadIdx.x * 8;
     if (k.end - k.begin == kTurn) step8<F32, true>(k, e);
@@ -314,9 +318,11 @@ __device__ inline double block_sum(double s) {
 constexpr int kNormSpan = 32768;
 template <bool F32> __global__ __launch_bounds__(256) void squares_kernel(Table p, double *partial) {
     constexpr int V = F32 ? 4 : 8, U = 4;  // loads in flight
-    const int i = find(p, blockIdx.x);
+    const int block = block_of();
+    if (block >= p.blocks) return;
+    const int i = find(p, block);
     const Entry t = p.t[i];
-    const int64_t begin = (int64_t)(blockIdx.x - p.first[i]) * kNormSpan, end = min(t.numel, begin + kNormSpan);
+    const int64_t begin = (int64_t)((uint32_t)block - p.first[i]) * kNormSpan, end = min(t.numel, begin + kNormSpan);
     double s[V] = {};
     int64_t at = begin;
     for (; at + U * 256 * V <= end; at += U * 256 * V) {
@@ -336,7 +342,7 @@ template <bool F32> __global__ __launch_bounds__(256) void squares_kernel(Table 
 #pragma unroll
     for (int k = 1; k < V; ++k) s[0] += s[k];
     s[0] = block_sum(s[0]);
-    if (threadIdx.x == 0) partial[blockIdx.x] = s[0];
+    if (threadIdx.x == 0) partial[block] = s[0];
 }
 
 __global__ __launch_bounds__(1024) void norm_kernel(const double *partial, int64_t n, double max_norm, float *norm,
@@ -354,8 +360,8 @@ __global__ __launch_bounds__(1024) void norm_kernel(const double *partial, int64
 // ---- host --------------------------------------------------------------------------------
 
 // The next launch's tensors: from `next` on, at most kTensors with elements.  A
-// tensor below 2^40 elements has less than 2^27 workgroups, 48 less than 2^33, so
-// that a launch ends at 2^30.
+// tensor below 2^40 elements has at most 2^29 workgroups (of kSpan8's 2048), 48 may have 2^34.6,
+// so that a launch ends at 2^30.
 constexpr int64_t kMostBlocks = (int64_t)1 << 30, kMostElements = (int64_t)1 << 40;
 int64_t fill(Table &p, const hyena_tensor *ts, int64_t n, int64_t &next, int64_t span) {
     p.n = 0;
@@ -371,6 +377,7 @@ int64_t fill(Table &p, const hyena_tensor *ts, int64_t n, int64_t &next, int64_t
         p.place[p.n++] = (uint32_t)next;
         blocks += more;
     }
+    p.blocks = (int)blocks;
     return blocks;
 }
 
@@ -476,7 +483,7 @@ int hyena_adamw_step(const hyena_tensor *tensors, int64_t n, double lr, double b
     Table p;
     int64_t next = 0;
     while (const int64_t blocks = fill(p, tensors, n, next, state_bits == 8 ? kSpan8 : kSpan32)) {
-        hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(256), 0, (hipStream_t)stream, p, a);
+        hipLaunchKernelGGL(kernel, grid_of(blocks), dim3(256), 0, (hipStream_t)stream, p, a);
         if ((st = launch_status()) != HYENA_OK) return st;
     }
     return HYENA_OK;
@@ -513,7 +520,7 @@ int hyena_grad_norm(const hyena_tensor *tensors, int64_t n, double max_norm, flo
     int64_t done = 0, next = 0;
     Table p;
     while (const int64_t blocks = fill(p, tensors, n, next, kNormSpan)) {
-        hipLaunchKernelGGL((f32 ? squares_kernel<true> : squares_kernel<false>), dim3((unsigned)blocks), dim3(256), 0,
+        hipLaunchKernelGGL((f32 ? squares_kernel<true> : squares_kernel<false>), grid_of(blocks), dim3(256), 0,
                            (hipStream_t)stream, p, partial + done);
         if ((st = launch_status()) != HYENA_OK) return st;
         done += blocks;

@@ -8,7 +8,7 @@ from gpu_util import DEV, log
 from model_ref import check
 
 pytestmark = pytest.mark.gpu
-BF16, F32 = torch.bfloat16, torch.float32
+BF16, F32, F8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
 
 
 @pytest.fixture(autouse=True)
@@ -71,3 +71,52 @@ def test_rows_past_2_to_the_29():
                             need_dx=False)
     # each of the two rows adds -(3 - 1) to entry 1
     assert dw.flatten().tolist() == [0.0, -4.0] and not db.any()
+
+
+def states(n):
+    """A parameter of n elements with moments in 8 bits."""
+    def zeros(n, dtype):
+        return torch.zeros(n, dtype=torch.uint8, device=DEV).view(dtype) if dtype is F8 else torch.zeros(n, dtype=dtype, device=DEV)
+
+    blocks = -(-n // hc.STATE_BLOCK)
+    return dict(params=zeros(n, BF16), exp_avgs=zeros(n, F8), exp_avg_sqs=zeros(n, F8), exp_avg_scales=zeros(blocks, F32),
+                exp_avg_sq_scales=zeros(blocks, F32))
+
+
+def same(a, b):
+    """Equality of codes, scales or parameters, 2^30 elements at a time."""
+    a, b = (x.view(torch.uint8) if x.dtype is F8 else x for x in (a, b))
+    return all(bool((p == q).all()) for p, q in zip(a.split(1 << 30), b.split(1 << 30)))
+
+
+def test_a_step_of_more_than_2_to_the_24_workgroups():
+    """17 tensors of 2^31 elements and some with moments in 8 bits (2^24 workgroups hold 2^35; 142 GB): a step gives each
+    what a call gives it that has only this tensor, at the same place in the list."""
+    n, count = (1 << 31) + 77, 17
+    log("adamw of %d x %d elements" % (count, n))
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    grad = torch.empty(n, dtype=BF16, device=DEV)  # of all of them: it is only read
+    for piece in grad.split(1 << 28):
+        piece.normal_(generator=gen)
+    kw = dict(step=1, lr=1e-2, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.1, seed=11)
+    all_of = [states(n) for _ in range(count)]
+    hc.adamw_step(grads=[grad] * count, **{k: [s[k] for s in all_of] for k in all_of[0]}, **kw)
+    empty = states(0)
+    for i in range(count):
+        if i not in (0, 7, count - 1):
+            assert same(all_of[i]["params"], all_of[0]["params"])
+            continue
+        alone = states(n)
+        lists = {k: [empty[k]] * i + [alone[k]] for k in alone}
+        hc.adamw_step(grads=[grad[:0]] * i + [grad], **lists, **kw)
+        for k in alone:
+            assert same(all_of[i][k], alone[k]), (i, k)
+        assert bool(alone["params"][-77:].any()) and bool(alone["exp_avgs"][-77:].float().any())
+
+
+def test_the_norm_of_more_than_2_to_the_24_workgroups():
+    """2^34 gradients 49 times over, in two launches, the first of 1.5 x 2^24 workgroups: squares of 2^-20 add up exactly."""
+    log("norm of 49 x 2^34 gradients")
+    grad = torch.full((1 << 34,), 2.0 ** -10, dtype=BF16, device=DEV)
+    norm, scale = hc.grad_norm([grad] * 49, max_norm=7.0)
+    assert float(norm) == 7 * 2.0 ** 7 and float(scale) == 2.0 ** -7

@@ -13,6 +13,7 @@ import textwrap
 import pytest
 
 import gated_convolution_sequence_amd as hc
+from gated_convolution_sequence_amd.model import _Tensor
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -75,6 +76,39 @@ def xent_bwd(M, K, V, dtype, dx=True, dw=True, db=True):
                                       P(7) if dw else None, P(8) if db else None, P(9), HUGE, dtype, None)
 
 
+def table(sizes):
+    """A list of tensors, their arrays 2^43 bytes apart."""
+    t = (_Tensor * len(sizes))()
+    for k, (e, n) in enumerate(zip(t, sizes)):
+        at = [(1 << 54) + ((7 * k + j) << 43) for j in range(7)]
+        e.param, e.grad, e.exp_avg, e.exp_avg_sq, e.exp_avg_scale, e.exp_avg_sq_scale, e.master = at
+        e.numel = n
+    return t
+
+
+def adamw(sizes, bits, dtype=0):
+    def call(L, t=table(sizes)):
+        return L.hyena_adamw_step(ctypes.addressof(t), len(t), 1e-3, 0.9, 0.95, 1e-8, 0.1, 1, 0, None, None, None, None, bits,
+                                  dtype, None)
+    return call
+
+
+def grad_norm(sizes, dtype=0):
+    def call(L, t=table(sizes)):
+        return L.hyena_grad_norm(ctypes.addressof(t), len(t), 1.0, P(9), P(10), P(11), HUGE, dtype, None)
+    return call
+
+
+# elements: 2048 a workgroup with moments of 8 bits, 4096 of 32 bits, 32768 for the norm
+LISTS = {
+    "adamw8 2^24": ([1 << 31] * 16, 2048), "adamw8 past": ([5, (1 << 31) + 77, 0] * 30, 2048),
+    "adamw8 one": ([(1 << 40) - 1], 2048), "adamw8 ones": ([(1 << 40) - 1] * 5, 2048),
+    "adamw32 2^24": ([1 << 33] * 8, 4096), "adamw32 one": ([(1 << 40) - 1] * 2, 4096),
+    "adamw32 many": ([(1 << 36) + 1, 9] * 70, 4096),
+    "norm 2^24": ([1 << 36] * 8, 32768), "norm many": ([(1 << 40) - 1] * 100, 32768), "norm small": ([3] * 100, 32768),
+}
+
+
 MOST = (1 << 31) - 1024  # rows, entries
 BF16, F32 = 0, 1
 CASES = {
@@ -99,6 +133,8 @@ CASES = {
     "fwd refused f32": xent_fwd(1 << 22, 8, 1 << 21, F32), "fwd refused bf16": xent_fwd(1 << 23, 8, 1 << 22, BF16),
     "bwd refused": xent_bwd(1 << 30, 1 << 17, 2, BF16), "bwd refused w": xent_bwd(2, 1 << 17, 1 << 30, BF16),
     "fwd largest": xent_fwd(1 << 22, 8, 1 << 20, F32), "bwd largest": xent_bwd(1 << 22, 8, 1 << 20, F32),
+    **{name: grad_norm(sizes) if name.startswith("norm") else adamw(sizes, 8 if "8" in name.split()[0] else 32)
+       for name, (sizes, _) in LISTS.items()},
 }
 
 
@@ -146,3 +182,15 @@ def test_readout_launches(tmp_path):
                         ("fwd rows f32", MOST // 32), ("fwd few rows", MOST // 16), ("fwd largest", 1 << 30)):
         most = max(grid[0] * grid[1] for grid, _ in found[name])
         assert tiles <= most < tiles + (1 << 21), (name, most)
+
+
+def test_launches_over_lists_of_tensors(tmp_path):
+    """Every tensor's workgroups are launched, 48 tensors or 2^30 workgroups at a time."""
+    found = check_launches(tmp_path, list(LISTS))
+    for name, (sizes, span) in LISTS.items():
+        rows = found[name][:-1] if name.startswith("norm") else found[name]  # the last one adds up the norm
+        want = sum(-(-n // span) for n in sizes)
+        got = [grid[0] * grid[1] for grid, _ in rows]
+        # (a launch of more than 2^21 is filled up to whole rows of that many)
+        assert want <= sum(got) < want + len(got) * (1 << 21) and max(got) <= 1 << 30, (name, want, got)
+        assert len(got) >= -(-sum(n > 0 for n in sizes) // 48)
