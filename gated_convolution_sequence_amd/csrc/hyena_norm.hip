@@ -343,14 +343,14 @@ struct ColumnSums {
 };
 template <bool F32> __global__ __launch_bounds__(1024) void column_sums_kernel(ColumnSums p) {
     __shared__ float part[16][64];
-    void *to = p.to[blockIdx.y];
+    void *to = p.to[blockIdx.z];
     if (!to) return;
     const int c = threadIdx.x & 63, r = threadIdx.x >> 6;
-    const int64_t d = (int64_t)blockIdx.x * 64 + c;
+    const int64_t d = (int64_t)block_of() * 64 + c;
     float s = 0.0f;
     if (d < p.D) {
 #pragma unroll 8
-        for (int i = r; i < p.n; i += 16) s += p.from[((int64_t)i * 2 + blockIdx.y) * p.D + d];
+        for (int i = r; i < p.n; i += 16) s += p.from[((int64_t)i * 2 + blockIdx.z) * p.D + d];
     }
     part[r][c] = s;
     __syncthreads();
@@ -447,7 +447,9 @@ template <bool F32> int launch_bwd(NormParams p, char *ws, hipStream_t stream) {
     ColumnSums c = {};
     c.from = p.sums, c.to[0] = p.want_dw ? p.dw : nullptr, c.to[1] = p.want_db ? p.db : nullptr;
     c.D = p.D, c.n = blocks;
-    hipLaunchKernelGGL(column_sums_kernel<F32>, dim3((unsigned)ceil_div(p.D, 64), 2), dim3(1024), 0, stream, c);
+    dim3 grid = grid_of(ceil_div(p.D, 64));
+    grid.z = 2;
+    hipLaunchKernelGGL(column_sums_kernel<F32>, grid, dim3(1024), 0, stream, c);
     return launch_status();
 }
 

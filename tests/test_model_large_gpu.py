@@ -120,3 +120,19 @@ def test_the_norm_of_more_than_2_to_the_24_workgroups():
     grad = torch.full((1 << 34,), 2.0 ** -10, dtype=BF16, device=DEV)
     norm, scale = hc.grad_norm([grad] * 49, max_norm=7.0)
     assert float(norm) == 7 * 2.0 ** 7 and float(scale) == 2.0 ** -7
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_a_row_past_2_to_the_28(dtype):
+    """One row of 2^28 channels and some: dw = dy u and db = dy, with nothing to add up."""
+    D = (1 << 28) + 4097
+    log("norm backward of %d channels %s" % (D, dtype))
+    gen = torch.Generator(device=DEV).manual_seed(4)
+    x, dy = (torch.empty(1, D, dtype=dtype, device=DEV).normal_(generator=gen) for _ in range(2))
+    w = torch.ones(D, dtype=dtype, device=DEV)
+    mean, rstd = (torch.full((1,), v, device=DEV) for v in (0.25, 2.0))
+    _, dw, db = hc.norm_bwd(x, w, dy, mean, rstd)
+    assert torch.equal(db, dy[0])
+    # u = (x - mean) rstd, a sum with one rounding and a product by a power of two; dy u one more
+    want = (x[0].double() - 0.25) * 2 * dy[0].double()
+    check(dw, want, 2 * ref.U * want.abs(), "dw")

@@ -76,6 +76,15 @@ def xent_bwd(M, K, V, dtype, dx=True, dw=True, db=True):
                                       P(7) if dw else None, P(8) if db else None, P(9), HUGE, dtype, None)
 
 
+def norm_fwd(M, D, dtype):
+    return lambda L: L.hyena_norm_fwd(P(0), P(1), P(2), M, D, D, D, 0, 1e-5, P(3), P(4), P(5), dtype, None)
+
+
+def norm_bwd(M, D, dtype, dx=True):
+    return lambda L: L.hyena_norm_bwd(P(0), P(1), P(2), P(3), P(4), M, D, D, D, D, 0, P(5) if dx else None, P(6), P(7), P(8),
+                                      HUGE, dtype, None)
+
+
 def table(sizes):
     """A list of tensors, their arrays 2^43 bytes apart."""
     t = (_Tensor * len(sizes))()
@@ -133,6 +142,11 @@ CASES = {
     "fwd refused f32": xent_fwd(1 << 22, 8, 1 << 21, F32), "fwd refused bf16": xent_fwd(1 << 23, 8, 1 << 22, BF16),
     "bwd refused": xent_bwd(1 << 30, 1 << 17, 2, BF16), "bwd refused w": xent_bwd(2, 1 << 17, 1 << 30, BF16),
     "fwd largest": xent_fwd(1 << 22, 8, 1 << 20, F32), "bwd largest": xent_bwd(1 << 22, 8, 1 << 20, F32),
+    # rows of all lengths; dw and db of 2^28 and more channels
+    "rows fwd": norm_fwd(3, 1 << 31, BF16), "rows fwd many": norm_fwd(1 << 40, 16, F32),
+    "rows bwd 2^28": norm_bwd(1, 1 << 28, BF16), "rows bwd f32": norm_bwd(300, (1 << 28) + 3, F32),
+    "rows bwd most": norm_bwd(2, 1 << 31, F32), "rows bwd dw": norm_bwd(2, 1 << 31, BF16, dx=False),
+    "rows bwd many": norm_bwd(1 << 40, 16, BF16),
     **{name: grad_norm(sizes) if name.startswith("norm") else adamw(sizes, 8 if "8" in name.split()[0] else 32)
        for name, (sizes, _) in LISTS.items()},
 }
@@ -194,3 +208,10 @@ def test_launches_over_lists_of_tensors(tmp_path):
         # (a launch of more than 2^21 is filled up to whole rows of that many)
         assert want <= sum(got) < want + len(got) * (1 << 21) and max(got) <= 1 << 30, (name, want, got)
         assert len(got) >= -(-sum(n > 0 for n in sizes) // 48)
+
+
+def test_norm_launches(tmp_path):
+    found = check_launches(tmp_path, [n for n in CASES if n.startswith("rows")])
+    for name, D in (("rows bwd 2^28", 1 << 28), ("rows bwd f32", (1 << 28) + 3), ("rows bwd most", 1 << 31)):
+        grid, _ = found[name][-1]  # 64 columns a workgroup, for dw and for db
+        assert -(-D // 64) <= grid[0] * grid[1] < -(-D // 64) + (1 << 21) and grid[2] == 2, (name, grid)
