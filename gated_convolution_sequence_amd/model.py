@@ -3,7 +3,8 @@
 A thin binding of the C ABI in ``include/hyena_model.h`` (libhyena_model.so),
 in the manner of the package's other calls: it checks and marshals arguments,
 every step of the computation runs in the library's HIP kernels, and there is
-no fallback.
+no fallback.  What a call writes into tensors that it was given raises their version, as
+torch's own in-place operations do, so that a graph that has saved one of them refuses its backward.
 
 norm_fwd, norm_bwd      layer norm and root-mean-square norm of rows (Norm: autograd)
 xent_fwd, xent_bwd      softmax cross entropy of a readout, no logits kept (LinearXent: autograd)
@@ -19,6 +20,7 @@ import os
 from typing import Optional, Sequence, Tuple, Union
 
 import torch
+from torch.autograd.graph import increment_version
 
 from . import HyenaError  # the package imports this module last
 from ._autograd import first_order
@@ -131,6 +133,7 @@ def norm_fwd(x: torch.Tensor, w: Optional[torch.Tensor] = None, b: Optional[torc
         ldx = _shared_stride((x,), ("x",), D)
     _contiguous(w, "w", (D,), dt, dev)
     _contiguous(b, "b", (D,), dt, dev)
+    given = out
     if out is None:
         out = torch.empty(x.shape, dtype=dt, device=dev)
     else:
@@ -143,6 +146,8 @@ def norm_fwd(x: torch.Tensor, w: Optional[torch.Tensor] = None, b: Optional[torc
             mean = torch.empty_like(rstd)
     _call("hyena_norm_fwd", dev, x.data_ptr(), _ptr(w), _ptr(b), M, D, ldx, ldy, kcode, eps, out.data_ptr(),
           _ptr(mean), _ptr(rstd), code)
+    if given is not None:
+        increment_version(given)
     return out, mean, rstd
 
 
@@ -175,6 +180,7 @@ def norm_bwd(x: torch.Tensor, w: Optional[torch.Tensor], dy: torch.Tensor, mean:
         raise ValueError("mean is what norm_fwd saved: a tensor for kind 'layer', None for 'rms'")
     _contiguous(mean, "mean", x.shape[:-1], torch.float32, dev)
     _contiguous(rstd, "rstd", x.shape[:-1], torch.float32, dev)
+    given = dx if need_dx else None
     if not need_dx:
         dx = None
     elif dx is None:
@@ -189,6 +195,8 @@ def norm_bwd(x: torch.Tensor, w: Optional[torch.Tensor], dy: torch.Tensor, mean:
     ws = _workspace(norm_workspace_bytes(M, D, code), workspace, dev)
     _call("hyena_norm_bwd", dev, x.data_ptr(), _ptr(w), dy.data_ptr(), _ptr(mean), rstd.data_ptr(), M, D, ldx, lddy,
           lddx, kcode, _ptr(dx), _ptr(dw), _ptr(db), *_ws_args(ws), code)
+    if given is not None:
+        increment_version(given)
     return dx, dw, db
 
 
@@ -272,6 +280,7 @@ def xent_bwd(x: torch.Tensor, w: torch.Tensor, target: torch.Tensor, lse: torch.
     _contiguous(lse, "lse", target.shape, torch.float32, dev)
     _contiguous(dloss, "dloss", target.shape, torch.float32, dev)
     lddx = K
+    given = dx if need_dx else None
     if not need_dx:
         dx = None
     elif dx is None:
@@ -286,6 +295,8 @@ def xent_bwd(x: torch.Tensor, w: torch.Tensor, target: torch.Tensor, lse: torch.
     ws = _workspace(xent_workspace_bytes(M, K, V, code, backward=True), workspace, dev)
     _call("hyena_xent_bwd", dev, x.data_ptr(), w.data_ptr(), _ptr(bias), target.data_ptr(), lse.data_ptr(),
           dloss.data_ptr(), M, K, V, ldx, lddx, _ptr(dx), _ptr(dw), _ptr(db), *_ws_args(ws), code)
+    if given is not None:
+        increment_version(given)
     return dx, dw, db
 
 
@@ -423,3 +434,4 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], ex
     number = [x if t is None else zero for x, t, zero in zip((lr, step, seed), given, (0.0, 1, 0))]
     _call("hyena_adamw_step", dev, words.buffer_info()[0], len(params), number[0], betas[0], betas[1], eps,
           weight_decay, number[1], number[2], *(_ptr(t) for t in given), _ptr(grad_scale), bits, code)
+    increment_version([*params, *exp_avgs, *exp_avg_sqs, *(masters or ()), *(exp_avg_scales or ()), *(exp_avg_sq_scales or ())])
