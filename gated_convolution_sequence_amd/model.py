@@ -393,14 +393,14 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], ex
                grad_scale: Optional[torch.Tensor] = None,
                exp_avg_scales: Optional[Sequence[torch.Tensor]] = None,
                exp_avg_sq_scales: Optional[Sequence[torch.Tensor]] = None,
-               seed: Union[int, torch.Tensor] = 0, stream: Optional[torch.cuda.Stream] = None) -> None:
+               seed: Union[int, torch.Tensor, None] = None, stream: Optional[torch.cuda.Stream] = None) -> None:
     """One AdamW step over lists of tensors, in place, in a launch for every 48 of them.
 
     params, grads: all bf16 or all fp32; masters (None, or the fp32 values of which params are the roundings, and
     which then take the step); exp_avgs, exp_avg_sqs: the moments m and v in fp32, or m and sqrt(v) in
     float8_e4m3fn with exp_avg_scales and exp_avg_sq_scales, an fp32 vector for each parameter with one scale for
     every 256 elements (codes and scales of zeros to begin with; rounding is random, by ``seed``, which should
-    differ from step to step).  All contiguous, shaped as params.  step counts from 1.  lr, step and seed may be
+    differ from step to step; None: the step's number, or what the step's tensor holds).  All contiguous, shaped as params.  step counts from 1.  lr, step and seed may be
     one-element tensors on the device (fp32, int64, int64), which a captured step reads anew in each replay.
     grad_scale: one fp32 on the device that multiplies the gradients; where it is not finite the step is skipped.
     Without masters, a bf16 parameter loses moves below half a unit of its last place.
@@ -426,6 +426,8 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], ex
         _column(table, 5, () if exp_avg_sq_scales is None else exp_avg_sq_scales, "exp_avg_sq_scales", blocks, fp32, dev)
     elif exp_avg_scales is not None or exp_avg_sq_scales is not None:
         raise ValueError("scales belong to moments in float8_e4m3fn")
+    if seed is None:
+        seed = step
     given = [t if isinstance(t, torch.Tensor) else None for t in (lr, step, seed)]
     for t, name, kind in zip((*given, grad_scale), ("lr", "step", "seed", "grad_scale"),
                              (torch.float32, torch.int64, torch.int64, torch.float32)):
@@ -434,4 +436,5 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], ex
     number = [x if t is None else zero for x, t, zero in zip((lr, step, seed), given, (0.0, 1, 0))]
     _call("hyena_adamw_step", dev, words.buffer_info()[0], len(params), number[0], betas[0], betas[1], eps,
           weight_decay, number[1], number[2], *(_ptr(t) for t in given), _ptr(grad_scale), bits, code)
-    increment_version([*params, *exp_avgs, *exp_avg_sqs, *(masters or ()), *(exp_avg_scales or ()), *(exp_avg_sq_scales or ())])
+    increment_version([*params, *exp_avgs, *exp_avg_sqs, *(masters or ()), *(exp_avg_scales or ()),
+                       *(exp_avg_sq_scales or ())])

@@ -139,7 +139,9 @@ typedef struct hyena_tensor {
  * they are rounded.  s becomes the largest magnitude / 448 (a block whose largest
  * is below 2^-117 counts as zeros), and x / s is rounded to one of the two codes around
  * it at random, up with the probability of its place between them, so that
- * moments keep changing where a step moves them by less than half a code.  (r and
+ * moments keep changing where a step moves them by less than half a code: with the same
+ * seed in every step an element would be rounded by the same bits each time, and those with low
+ * ones never up, so that the seed has to differ from step to step.  (r and
  * not v, since e4m3 spans 2^18 from its least to its largest.)  The random bits
  * are a function of seed (its low 32 bits), of the tensor's place k in the list
  * and of the element's index i: with mix the last steps of murmur3,
