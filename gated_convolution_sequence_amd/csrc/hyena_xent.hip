@@ -224,9 +224,11 @@ template <int SLICES> __global__ __launch_bounds__(256) void merge_kernel(MergeP
     r = meet[0][row];
     const int64_t to = p.index ? p.index[m] : m;
     const bool on = p.index || (uint64_t)p.target[m] < (uint64_t)p.V;
-    const float lse = shift_of(r.m) + __logf(r.s);
-    p.loss[to] = on ? lse - p.at[m] : 0.0f;
-    p.lse[to] = on ? lse : 0.0f;
+    // the loss from the logits' difference, which is exact where they are close, and not from lse: of
+    // a nearly certain token among logits of thousands, lse's rounding would be most of it
+    const float shift = shift_of(r.m), log_s = logf(r.s);
+    p.loss[to] = on ? shift - p.at[m] + log_s : 0.0f;
+    p.lse[to] = on ? shift + log_s : 0.0f;
 }
 
 // ---- rows with a target ----------------------------------------------------------------

@@ -1,11 +1,12 @@
-"""Edges of the readout cross entropy: upstream gradients that are not finite."""
+"""Edges of the readout cross entropy: upstream gradients that are not finite, tokens that are nearly certain."""
 import math
 
 import pytest
 import torch
 
 import gated_convolution_sequence_amd as hc
-from gpu_util import DEV, log
+from gpu_util import DEV
+from model_ref import U, check
 from test_xent_gpu import inputs
 
 pytestmark = pytest.mark.gpu
@@ -81,3 +82,30 @@ def test_infinite_upstream_leaves_no_weight_finite(M, K, V, value):
         dx, dw, db = hc.xent_bwd(t["x"], t["w"], t["target"], lse, d, bias=t["bias"])
         assert not torch.isfinite(dw).any() and not torch.isfinite(db).any()
         assert not torch.isfinite(dx[rows[len(rows) // 2]]).any()
+
+
+# ---- tokens that are nearly certain ------------------------------------------------------
+
+@pytest.mark.parametrize("M", [5, 60, 600])
+@pytest.mark.parametrize("K", [2, 8])
+@pytest.mark.parametrize("level", [0.0, 3968.0, -3968.0])
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_the_loss_of_a_nearly_certain_token_keeps_its_digits(M, K, level, dtype):
+    """Logits of level + 32 for the target and level + 13 to 20 for the others, exact in fp32: a loss of 0.0009.
+
+    exp(z - the largest) sums to 1.0009: some 40 additions that round what is below 2 (lanes, waves, tiles), terms by
+    their exponents' (20 + 2) U, and a logarithm.  lse, of thousands, has fewer digits than that; loss must not be
+    formed from it."""
+    V = 300
+    w = torch.zeros(V, K, device=DEV)
+    w[:, 0], w[:, 1] = level, 13.0 + torch.arange(V, device=DEV) % 8
+    w[77, 1] = 32.0
+    x = torch.zeros(M, K, device=DEV)
+    x[:, :2] = 1.0
+    target = torch.full((M,), 77, device=DEV)
+    target[1::4] = 5
+    loss, lse = hc.xent_fwd(x.to(dtype), w.to(dtype), target)
+    d = w[:, 1].double()
+    want = (torch.logsumexp(d - 32.0, 0) + 32.0 - d)[target]
+    check(loss, want, 64 * U + 4 * U * want, "loss")
+    check(lse, torch.logsumexp(level + d, 0).expand(M), 64 * U, "lse")
