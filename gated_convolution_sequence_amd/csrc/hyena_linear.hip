@@ -61,6 +61,7 @@ template <int ACT> __device__ inline float act_slope(float z) {
 
 struct Epilogue {
     static constexpr bool kSums = false;
+    static constexpr int kRun = 0;
     const void *bias, *residual;
     void *y, *preact;
     int64_t ldr, ldy;

@@ -142,6 +142,9 @@ template <bool F32, int V> struct Pack {
 //   e.finish<F32, V>(m, n, z, c, r)  the sums z of one row with both,
 //   e.close<F32, V>(c, m, block, n)  after the last row of row block `block`, the rows of one wave from m on,
 // or, where E::kSums, e.sums<S>(...) on the sums as the matrix cores leave them.
+// E::kRun: fp32 sums over c are formed in runs of so many values (0: in one), added up in
+// order.  In fp32 the matrix cores round a sum once a product, so that one chain over a long c loses
+// sqrt(c / 2) roundings' digits; bf16 products are summed 32 at a time.
 template <class E> struct Gemm {
     const void *a, *b;
     const int *rows;          // GATHER: the memory row of each row of a, ascending; a tile's within 2^31 bytes
@@ -367,6 +370,8 @@ template <bool F32, int WM, int WN, int MT, int NTL, int ST> struct Shape {
         const int wave = threadIdx.x >> 6, i = threadIdx.x & 15, j = (threadIdx.x >> 4) & 3;
         const int wm = wave / WN * MT * 16, wn = wave % WN * NTL * 16;
         f32x4_t acc[MT][NTL] = {};
+        constexpr bool RUNS = F32 && E::kRun > 0;
+        f32x4_t before[RUNS ? MT : 1][RUNS ? NTL : 1] = {};
         const int start_a = A::start(wm, i, j), start_b = B::start(wn, i, j);
         auto multiply = [&](unsigned char *la, unsigned char *lb) {
             // hidden from the compiler, or it would keep the addresses of all
@@ -409,6 +414,21 @@ template <bool F32, int WM, int WN, int MT, int NTL, int ST> struct Shape {
         // for every wave to be done with the buffer that is filled next.
         // Fills past the end of c are zeros, so that their number is the same.
         int left = c_end - c_begin;
+        // turn() while c is left, and the sums of each run to those before
+        auto walk = [&](auto turn) {
+            static_assert(E::kRun % (ST * BK) == 0, "runs of whole turns");
+            if constexpr (RUNS) {
+                while (left > E::kRun) {
+#pragma unroll 1
+                    for (int n = 0; n < E::kRun; n += ST * BK) turn();
+#pragma unroll
+                    for (int t = 0; t < MT; ++t)
+#pragma unroll
+                        for (int u = 0; u < NTL; ++u) before[t][u] += acc[t][u], acc[t][u] = f32x4_t{};
+                }
+            }
+            while (left > 0) turn();
+        };
         if constexpr (DIRECT) {
             constexpr int LOADS = A::LOADS + B::LOADS;
             const typename A::Lane lane_a = A::plan(p.lda, p.M - m0, GATHER ? p.rows + m0 : nullptr);
@@ -421,14 +441,15 @@ template <bool F32, int WM, int WN, int MT, int NTL, int ST> struct Shape {
             };
 #pragma unroll
             for (int s = 0; s < ST - 1; ++s) fetch(s, left - s * BK);
-            for (; left > 0; left -= ST * BK) {
+            walk([&] {
 #pragma unroll
                 for (int s = 0; s < ST; ++s) {
                     step_barrier<(ST - 2) * LOADS>();
                     fetch((s + ST - 1) % ST, left - (s + ST - 1) * BK);
                     if (ST == 2 || left > s * BK) multiply(la[s], lb[s]);
                 }
-            }
+                left -= ST * BK;
+            });
         } else {
             static_assert(DIRECT || (ST == 2 && !GATHER), "through registers: one step ahead");
             u32x4_t ra[A::LOADS], rb[B::LOADS];
@@ -440,7 +461,7 @@ template <bool F32, int WM, int WN, int MT, int NTL, int ST> struct Shape {
             };
             pull(left);
             A::push(ra, (lds)la[0]), B::push(rb, (lds)lb[0]);
-            for (; left > 0; left -= 2 * BK) {
+            walk([&] {
                 __syncthreads();
                 pull(left - BK);
                 multiply(la[0], lb[0]);
@@ -449,7 +470,14 @@ template <bool F32, int WM, int WN, int MT, int NTL, int ST> struct Shape {
                 if (left > 2 * BK) pull(left - 2 * BK);
                 multiply(la[1], lb[1]);
                 A::push(ra, (lds)la[0]), B::push(rb, (lds)lb[0]);
-            }
+                left -= 2 * BK;
+            });
+        }
+        if constexpr (RUNS) {
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+                for (int u = 0; u < NTL; ++u) acc[t][u] += before[t][u];
         }
 
         if constexpr (E::kSums) {

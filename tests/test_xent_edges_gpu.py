@@ -1,4 +1,5 @@
-"""Edges of the readout cross entropy: upstream gradients that are not finite, tokens that are nearly certain."""
+"""Edges of the readout cross entropy: upstream gradients that are not finite, tokens that are nearly certain,
+fp32 logits of long rows, each row's part in the sums over rows."""
 import math
 
 import pytest
@@ -109,3 +110,48 @@ def test_the_loss_of_a_nearly_certain_token_keeps_its_digits(M, K, level, dtype)
     want = (torch.logsumexp(d - 32.0, 0) + 32.0 - d)[target]
     check(loss, want, 64 * U + 4 * U * want, "loss")
     check(lse, torch.logsumexp(level + d, 0).expand(M), 64 * U, "lse")
+
+
+# ---- fp32 logits of long rows ------------------------------------------------------------
+
+def chain_error(K):
+    """The root mean square error of an fp32 logit over its own, for terms of random signs.
+
+    A sum's n-th rounding is that of n terms' random walk: sqrt(n / N) of the last one's, at most 2^-24 / sqrt(3) in
+    the mean square (a half unit, uniform).  Over a run of 256 terms, rounded once each at most, and the sums of
+    K / 256 runs that comes to sqrt(256 / 2 + K / 256 / 2) of them; a quarter more for what 64 rows' mean may stray.
+    (One chain over all K: sqrt(K / 2) of them, four to eleven times as much for the lengths below.)"""
+    return 1.25 * 2.0 ** -24 / math.sqrt(3) * math.sqrt(128 + K / 512)
+
+
+def rms(t):
+    return float(t.double().square().mean().sqrt())
+
+
+@pytest.mark.parametrize("M,V", [(64, 64), (200, 300)])
+@pytest.mark.parametrize("K", [4096, 65536])
+def test_fp32_logits_of_long_rows(M, V, K):
+    gen = torch.Generator(device=DEV).manual_seed(41)
+    x = torch.randn(M, K, generator=gen, device=DEV)
+    w = torch.randn(V, K, generator=gen, device=DEV) * (25 * K ** -0.5)  # logits of some 25
+    z = x.double() @ w.double().t()
+    target = torch.arange(M, device=DEV) % V
+    loss, lse = hc.xent_fwd(x, w, target)
+    at = z.gather(1, target[:, None])[:, 0]
+    err = rms(loss.double() - (torch.logsumexp(z, 1) - at))
+    # of two logits, the largest and the target's, and the roundings of the loss and of its two parts
+    most = chain_error(K) * math.hypot(rms(z.max(1).values), rms(at)) + 2 * U * rms(loss)
+    assert err <= most
+    # exp(z - lse) of single rows, as db shows them; lse of 0 leaves exp's (|z| + 2) U beside the logits' error
+    zero, bias = torch.zeros(M, device=DEV), torch.zeros(V, device=DEV)
+    rel = []
+    for row in range(0, M, M // 16):
+        only = torch.full_like(target, -1)
+        only[row] = target[row]
+        _, _, db = hc.xent_bwd(x, w, only, zero, zero + 1, bias=bias, need_dx=False, need_dw=False)
+        keep = torch.arange(V, device=DEV) != target[row]
+        keep &= z[row].abs() < 80
+        rel.append((db.double() / z[row].exp() - 1)[keep])
+    err = rms(torch.cat(rel))
+    most = chain_error(K) * rms(z) + 27 * U
+    assert err <= most
