@@ -502,7 +502,7 @@ int hyena_grad_norm(const hyena_tensor *tensors, int64_t n, double max_norm, flo
     int st = check_tensors(tensors, n, dtype, 0, &numel);
     if (st != HYENA_OK) return st;
     if (!norm) return HYENA_ERR_NULL;
-    if (scale && !(max_norm >= 0 && isfinite(max_norm))) return HYENA_ERR_UNSUPPORTED;
+    if (scale && !(max_norm >= 0)) return HYENA_ERR_UNSUPPORTED;
     if (!aligned(norm, 4) || !aligned(scale, 4) || !aligned(workspace, 16)) return HYENA_ERR_ALIGN;
     hyena_grad_norm_workspace(n, numel, &need);
     if (need > 0 && (!workspace || workspace_bytes < need)) return HYENA_ERR_WORKSPACE;

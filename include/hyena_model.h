@@ -159,7 +159,8 @@ int hyena_adamw_step(const hyena_tensor *tensors, int64_t n, double lr,
 
 /* norm[0] = sqrt(sum of grad^2 over all tensors) (only grad and numel are
  * read), and, where scale is not NULL, scale[0] = min(1, max_norm / norm) (1
- * where norm is 0; NaN where norm is infinite or NaN, which skips the step).
+ * where norm is 0; NaN where norm is infinite or NaN, which skips the step); max_norm
+ * is at least 0 and may be infinite.
  * Squares are summed in 64 bits.  `workspace`: at least
  * hyena_grad_norm_workspace bytes for tensors of `numel` elements together. */
 int hyena_grad_norm(const hyena_tensor *tensors, int64_t n, double max_norm,
