@@ -8,7 +8,10 @@
 // workgroups walk the rows with the next one's loads in flight, past the caches.
 // 8192 x 4096 bf16: forward 23.5 us (134 MB, 5.7 TB/s; at 32768 rows 5.9), backward
 // 43 us (201 MB, 4.7 TB/s; of it 4 to 5 us the launch that adds the workgroups' sums
-// for dw and db; at 32768 rows 5.4).  Without the streaming accesses and the loads
+// for dw and db; at 32768 rows 5.4).  The longest rows' forms do not hold w and b beside
+// a row and the next one: the compiler keeps some 100 bytes a lane of them in scratch (bf16
+// forward, 1024 x 4 chunks) or up to 48 (backward, 1024 x 2), and 2048 x 24576 takes 85 us
+// forward (2.4 TB/s), 2048 x 16384 backward 53 (3.8).  Without the streaming accesses and the loads
 // ahead the forward took 28.5 us.
 
 #include "hyena_model.h"

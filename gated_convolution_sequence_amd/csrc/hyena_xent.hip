@@ -34,7 +34,9 @@ namespace {
 // ---- maxima and sums of a softmax ---------------------------------------------------
 
 // (m, s) stands for the values' maximum m and the sum of exp(z - m); where m is
-// infinite, of exp(z), which is 0 (m = -inf: no value can occur) or inf.
+// infinite, of exp(z), which is 0 (m = -inf: no value can occur) or inf.  exp is the hardware's
+// 2^x of a rounded product: off by (|z - m| + 2) 2^-23 of a term, most where the term is small; errors
+// against 64 bits are the same with exp's own function.
 struct Part {
     float m, s;
 };
@@ -149,8 +151,9 @@ template <class S, class E> __device__ inline bool rows_from(Gemm<E> &p, const i
     return block < p.tiles_m * p.tiles_n * p.splits;
 }
 
-// The forward's logits.  8192 x 4096 x 65536 bf16 3.2 to 3.4 ms (1.29 to 1.37 PFLOP/s),
-// bound as layer_gemm.h's products are.
+// The forward's logits.  8192 x 4096 x 65536 bf16 3.2 to 3.4 ms (1.28 to 1.36 PFLOP/s),
+// bound as layer_gemm.h's products are: the matrix cores are busy in 62 % of all cycles, L2 gives
+// 10 TB/s, memory 2.
 template <bool F32, bool DIRECT, bool GATHER, typename S>
 __global__ __launch_bounds__(S::NT, S::WAVES) void stats_kernel(Gemm<StatsEpi> p, const int *count, const int *apart) {
     TILE_BUFFERS(S)

@@ -400,8 +400,8 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], ex
     which then take the step); exp_avgs, exp_avg_sqs: the moments m and v in fp32, or m and sqrt(v) in
     float8_e4m3fn with exp_avg_scales and exp_avg_sq_scales, an fp32 vector for each parameter with one scale for
     every 256 elements (codes and scales of zeros to begin with; rounding is random, by ``seed``, which should
-    differ from step to step; None: the step's number, or what the step's tensor holds).  All contiguous, shaped as params.  step counts from 1.  lr, step and seed may be
-    one-element tensors on the device (fp32, int64, int64), which a captured step reads anew in each replay.
+    differ from step to step; None: the step's number, or what the step's tensor holds).  All contiguous, shaped as
+    params.  step counts from 1.  lr, step and seed may be one-element tensors on the device (fp32, int64, int64), which a captured step reads anew in each replay.
     grad_scale: one fp32 on the device that multiplies the gradients; where it is not finite the step is skipped.
     Without masters, a bf16 parameter loses moves below half a unit of its last place.
     """

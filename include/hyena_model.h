@@ -72,14 +72,15 @@ int hyena_norm_workspace(int64_t M, int64_t D, int dtype, int64_t *bytes_out);
  * `dtype`; target int64 [M]; loss and lse float32 [M].  A row whose target lies
  * outside [0, V) has none: its loss and lse are 0, its gradient is 0, it adds
  * nothing to dw and db whatever its x holds (NaN included), and costs nothing but
- * the reading of its target.  The logits are kept nowhere: the forward keeps a
+ * the reading of its target (in a forward of no more than 16 rows, what any row does:
+ * the weights stream through whatever the targets are).  The logits are kept nowhere: the forward keeps a
  * maximum and a sum for every tile of columns, the backward forms dz in pieces of
  * the vocabulary in its workspace.  A logit of -inf (by bias) is an entry that
  * cannot occur.  Sizes: M and V up to 2^31 - 1024, K below 2^20, and M V and
  * M K + V K up to 2^42 in fp32 and 2^44 in bf16.  Precision: bf16 products are
  * summed in fp32, fp32 products and sums are fp32; logits, maxima, sums, lse and loss
- * stay fp32.  loss is formed as (max z - z_target) + log sum exp(z - max z), so that
- * small ones keep their digits. */
+ * stay fp32; an exp(y) is off by (|y| + 2) 2^-23 of itself.  loss is formed as
+ * (max z - z_target) + log sum exp(z - max z), so that small ones keep their digits. */
 int hyena_xent_fwd(const void *x, const void *w, const void *bias,
                    const int64_t *target, int64_t M, int64_t K, int64_t V,
                    int64_t ldx, float *loss, float *lse, void *workspace,

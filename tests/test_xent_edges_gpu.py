@@ -1,5 +1,5 @@
 """Edges of the readout cross entropy: upstream gradients that are not finite, tokens that are nearly certain,
-fp32 logits of long rows, each row's part in the sums over rows."""
+fp32 logits of long rows."""
 import math
 
 import pytest
