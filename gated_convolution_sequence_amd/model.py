@@ -436,5 +436,8 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], ex
     number = [x if t is None else zero for x, t, zero in zip((lr, step, seed), given, (0.0, 1, 0))]
     _call("hyena_adamw_step", dev, words.buffer_info()[0], len(params), number[0], betas[0], betas[1], eps,
           weight_decay, number[1], number[2], *(_ptr(t) for t in given), _ptr(grad_scale), bits, code)
-    increment_version([*params, *exp_avgs, *exp_avg_sqs, *(masters or ()), *(exp_avg_scales or ()),
-                       *(exp_avg_sq_scales or ())])
+    written = [*params, *exp_avgs, *exp_avg_sqs]
+    for ts in (masters, exp_avg_scales, exp_avg_sq_scales):
+        if ts is not None:
+            written.extend(ts)
+    increment_version(written)

@@ -158,7 +158,8 @@ def launches(tmp_path, names):
     with open(source, "w") as f:
         f.write(STUB)
     subprocess.run(["g++", "-shared", "-fPIC", "-o", lib, source], check=True)
-    env = dict(os.environ, LD_PRELOAD=lib, LAUNCH_LOG=log)
+    first = " ".join(filter(None, (lib, os.environ.get("LD_PRELOAD"))))  # before what is preloaded already
+    env = dict(os.environ, LD_PRELOAD=first, LAUNCH_LOG=log)
     r = subprocess.run([sys.executable, "-c", CHILD, ROOT, *names], env=env, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stdout[-2000:] + r.stderr[-2000:]
     out = {}

@@ -73,6 +73,18 @@ def test_a_step_raises_the_versions_of_what_it_writes(bits, masters):
     assert before == {k: [x._version for x in ts] for k, ts in t.items()}
 
 
+def test_a_tensor_whose_rows_are_the_list():
+    """Sequences of any kind: the rows of one tensor each, whose versions are the tensor's."""
+    t = {k: randn(3, 50, seed=i) for i, k in enumerate(("params", "grads", "masters", "exp_avgs"))}
+    t["exp_avg_sqs"] = t["exp_avgs"].square()
+    want = {k: [x.clone() for x in v] for k, v in t.items()}
+    hc.adamw_step(**want, step=3, lr=1e-2)
+    before = {k: v._version for k, v in t.items()}
+    hc.adamw_step(**t, step=3, lr=1e-2)
+    for k, v in t.items():
+        assert torch.equal(v, torch.stack(want[k])) and (v._version > before[k]) == (k != "grads"), k
+
+
 def test_steps_of_inference_tensors():
     """They have no version; a step in inference mode, and outside of it, takes them as they are."""
     with torch.inference_mode():
